@@ -231,6 +231,71 @@ moe_status moe_router_topk(const float* logits, int32_t num_tokens, int32_t num_
                            int32_t top_k, int32_t* topk_ids, float* topk_weights,
                            hipStream_t stream);
 
+/* Element type of a floating tensor of the entries below. */
+typedef enum { MOE_BF16 = 0, MOE_F32 = 1 } moe_dtype;
+
+/* MXFP4 quantisation of a matrix x [rows, cols] (cols a multiple of 32): the
+ * codes and scales that moe_mxfp4_plan takes for one expert's matrix and
+ * moe_mxfp4_matmul for either operand.  The rule is the OCP Microscaling
+ * Formats v1.0 one: per block of 32 along a row, e = floor(log2(amax)) - 2
+ * clamped to [-125, 125] (amax = 0 gives -125), codes = nearest-even E2M1 of
+ * the block scaled by 2^-e and saturated to +-6, scale byte = e + 127, so
+ * bytes are 2..252, which a plan accepts for either activation type.  A block
+ * that holds a NaN or an infinity gets byte 0xFF and codes 0 (a plan refuses
+ * it by name).
+ *   x      [rows, cols] of `dtype`, rows ldx elements apart (ldx >= cols, 16
+ *          bytes a multiple of)
+ *   codes  [rows, cols/2] u8, element 2j in bits 3:0;  scales [rows, cols/32] u8
+ * rows <= 2^24; rows = 0 is a no-op.  Enqueue-only. */
+moe_status moe_mxfp4_quantize(const void* x, int32_t dtype, int32_t rows, int32_t cols, int64_t ldx,
+                              uint8_t* codes, uint8_t* scales, hipStream_t stream);
+
+/* The values that MXFP4 codes and scales stand for, exact in either type:
+ * code * 2^(byte - 127); byte 0xFF gives NaN, a magnitude past the type's
+ * largest infinity.  out [rows, cols] of `dtype`.  Enqueue-only. */
+moe_status moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t rows, int32_t cols,
+                                int32_t dtype, void* out, hipStream_t stream);
+
+/* Product of two MXFP4 matrices, out [m, n] = A [m, k] B [n, k]^T (a dense
+ * projection or a shared expert beside the routed ones; B in checkpoint
+ * layout), summed in fp32 and rounded once to `dtype`:
+ *   a_codes [m, k/2], a_scales [m, k/32], b_codes [n, k/2], b_scales [n, k/32]
+ * k a multiple of 32 in [32, 65536]; m and n in [0, 2^19], 0 is a no-op.  Any
+ * scale byte is taken (0xFF makes its row's or column's outputs
+ * NaN; sums past fp32's range are infinite or, of both signs, NaN).
+ * Enqueue-only, no workspace. */
+moe_status moe_mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
+                            const uint8_t* b_scales, int32_t m, int32_t n, int32_t k, int32_t dtype, void* out,
+                            hipStream_t stream);
+
+/* Products of ragged groups of rows with one bf16 matrix per group: the
+ * unquantised form of the layer's expert products, on rows sorted by expert
+ * (the order and the offsets that moe_mxfp4_route writes).
+ *   x       [rows, k] bf16, rows ldx elements apart
+ *   w       [num_groups, n, k] bf16
+ *   offsets [num_groups + 1] int32 in device memory: group e's rows are
+ *           offsets[e] .. offsets[e+1] - 1; nondecreasing, within [0, rows]
+ *           (values outside are clamped there and a decreasing pair counts as
+ *           an empty group, so no offset reaches outside the tensors)
+ *   out     [rows, n] bf16: out_r = w_e x_r, summed in fp32 and rounded once;
+ *           rows outside every group are not written
+ * n and k multiples of 8 in [8, 65536], num_groups <= 4096, rows <= 2^24, row
+ * strides multiples of 8 up to 2^20.  Enqueue-only, no workspace. */
+moe_status moe_grouped_matmul(const uint16_t* x, int64_t ldx, const uint16_t* w, const int32_t* offsets, int32_t rows,
+                              int32_t num_groups, int32_t n, int32_t k, uint16_t* out, hipStream_t stream);
+
+/* Gradients of moe_grouped_matmul for dy [rows, n] bf16 (rows lddy apart):
+ *   dx [rows, k] bf16: dx_r = w_e^T dy_r; rows outside every group are not written
+ *   dw [num_groups, n, k] of `dtype`: dw_e = sum over e's rows of dy_r x_r^T,
+ *      every element written (zero for an empty group)
+ * Each output is one fp32 sum in a fixed order, rounded once (no atomics). */
+moe_status moe_grouped_matmul_dx(const uint16_t* dy, int64_t lddy, const uint16_t* w, const int32_t* offsets,
+                                 int32_t rows, int32_t num_groups, int32_t n, int32_t k, uint16_t* dx,
+                                 hipStream_t stream);
+moe_status moe_grouped_matmul_dw(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx,
+                                 const int32_t* offsets, int32_t rows, int32_t num_groups, int32_t n, int32_t k,
+                                 int32_t dtype, void* dw, hipStream_t stream);
+
 /* Peak micro-benchmarks: the measured ceilings a benchmark reports its
  * kernels against beside the published peaks (the pages record each run's
  * GPU operating state because the clock policy moved their numbers: b12x PR

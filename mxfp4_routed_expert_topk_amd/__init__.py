@@ -15,6 +15,11 @@ Names follow the C ABI in include/moe_mxfp4.h:
   Plan.workspace_region(region)         -> the workspace bytes of an intermediate (MXFP8 h)
   mxfp8_quantize(x_bf16)                -> (codes, scales)
   router_topk(logits, k)                -> (topk_ids, topk_weights)  (moe_router_topk)
+  mxfp4_quantize(x)                     -> (codes, scales)           (moe_mxfp4_quantize)
+  mxfp4_dequantize(codes, scales)       -> the values they stand for (moe_mxfp4_dequantize)
+  mxfp4_matmul(a_codes, a_scales, b_codes, b_scales)  -> A B^T       (moe_mxfp4_matmul)
+  grouped_matmul(x, w, offsets)         rows sorted by group times the group's matrix (moe_grouped_matmul)
+  grouped_matmul_backward(dy, x, w, offsets)          -> (dx, dw)    (moe_grouped_matmul_dx / _dw)
   probe_memory(kind, src, dst, sink)    peak micro-benchmarks (moe_probe_memory / moe_probe_mfma)
   probe_mfma(kind, iters, sink)         -> flops of the launch
 """
@@ -38,7 +43,8 @@ MOE_WS_H_SCALES = 1
 EXPORTS = ("moe_mxfp4_query_sizes", "moe_mxfp4_plan", "moe_mxfp4_forward", "moe_mxfp4_forward_noalloc",
            "moe_mxfp4_forward_fused",
            "moe_mxfp4_fused_status", "moe_mxfp4_route", "moe_mxfp4_workspace_region", "moe_mxfp8_quantize",
-           "moe_router_topk", "moe_probe_memory", "moe_probe_mfma", "moe_probe_mfma_f8f4_blocks",
+           "moe_router_topk", "moe_mxfp4_quantize", "moe_mxfp4_dequantize", "moe_mxfp4_matmul",
+           "moe_grouped_matmul", "moe_grouped_matmul_dx", "moe_grouped_matmul_dw", "moe_probe_memory", "moe_probe_mfma", "moe_probe_mfma_f8f4_blocks",
            "moe_mxfp4_set_stage_events",
            "moe_mxfp4_destroy", "moe_mxfp4_last_error")
 _STATUS_FNS = tuple(n for n in EXPORTS if n not in ("moe_mxfp4_destroy", "moe_mxfp4_last_error"))
@@ -93,6 +99,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_mxfp4_workspace_region.argtypes = [vp, i32, ctypes.POINTER(sz), ctypes.POINTER(sz)]
     lib.moe_mxfp8_quantize.argtypes = [vp, i32, i32, vp, vp, vp]
     lib.moe_router_topk.argtypes = [vp, i32, i32, i32, vp, vp, vp]
+    i64 = ctypes.c_int64
+    lib.moe_mxfp4_quantize.argtypes = [vp, i32, i32, i32, i64, vp, vp, vp]
+    lib.moe_mxfp4_dequantize.argtypes = [vp, vp, i32, i32, i32, vp, vp]
+    lib.moe_mxfp4_matmul.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp]
+    lib.moe_grouped_matmul.argtypes = [vp, i64, vp, vp, i32, i32, i32, i32, vp, vp]
+    lib.moe_grouped_matmul_dx.argtypes = [vp, i64, vp, vp, i32, i32, i32, i32, vp, vp]
+    lib.moe_grouped_matmul_dw.argtypes = [vp, i64, vp, i64, vp, i32, i32, i32, i32, i32, vp, vp]
     lib.moe_probe_memory.argtypes = [i32, vp, vp, sz, vp, i32, vp]
     lib.moe_probe_mfma.argtypes = [i32, i32, vp, i32, ctypes.POINTER(ctypes.c_double), vp]
     lib.moe_probe_mfma_f8f4_blocks.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp]
@@ -116,7 +129,7 @@ def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-MOE_ERR_ARG = 1
+MOE_ERR_ARG, MOE_ERR_SHAPE = 1, 2
 
 
 def _arg_error(msg: str):
@@ -311,6 +324,267 @@ def mxfp8_quantize(x_bf16, stream=None):
     scales = torch.empty((rows, max(cols // 32, 0)), dtype=torch.uint8, device=x_bf16.device)
     _check(load_library().moe_mxfp8_quantize(_ptr(x_bf16), rows, cols, _ptr(codes), _ptr(scales), _stream(stream)))
     return codes, scales
+
+
+MOE_BF16, MOE_F32 = 0, 1
+
+
+def _dtype_code(dtype, name: str) -> int:
+    import torch
+    if dtype == torch.bfloat16:
+        return MOE_BF16
+    if dtype == torch.float32:
+        return MOE_F32
+    raise _arg_error(f"{name} must be torch.bfloat16 or torch.float32, got {dtype}")
+
+
+def _need_shape(t, name: str, dtype, shape, device):
+    """Raise MoeError(MOE_ERR_ARG) unless `t` is a contiguous tensor of `dtype`
+    and exactly `shape` on `device`."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise _arg_error(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise _arg_error(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise _arg_error(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise _arg_error(f"{name} must be on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise _arg_error(f"{name} must be contiguous")
+
+
+def _rows(t, name: str, dtypes, cols: Optional[int], device):
+    """The row stride (elements) of a matrix whose rows are contiguous;
+    MoeError(MOE_ERR_ARG) otherwise."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise _arg_error(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.dtype not in dtypes:
+        raise _arg_error(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
+        raise _arg_error(f"{name} must be [rows, {'cols' if cols is None else cols}], got shape {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise _arg_error(f"{name} must be on {device}, got {t.device}")
+    rows, width = t.shape
+    row_stride, step = t.stride()
+    if width > 1 and step != 1:
+        raise _arg_error(f"the rows of {name} must be contiguous, got strides {t.stride()}")
+    return row_stride if rows > 1 else width
+
+
+def _apart(out, name: str, *inputs):
+    """Raise MoeError(MOE_ERR_ARG) if the memory of `out` and of an input overlap."""
+    lo, hi = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
+    for other, t in inputs:
+        n = t.numel()
+        if n == 0 or lo == hi:
+            continue
+        span = 1 + sum((d - 1) * s for d, s in zip(t.shape, t.stride()))
+        if t.data_ptr() < hi and lo < t.data_ptr() + span * t.element_size():
+            raise _arg_error(f"{name} must not overlap {other}")
+
+
+def _new(shape, dtype, device, stream):
+    """An uninitialised tensor, from the memory of `stream` if one is given."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _check_place(device, stream):
+    """Raise MoeError(MOE_ERR_ARG) unless `device` is a GPU and `stream`, if given, one of its streams."""
+    if device.type != "cuda":
+        raise _arg_error(f"tensors must be on a GPU, got {device}")
+    if stream is not None and stream.device != device:
+        raise _arg_error(f"stream is of {stream.device}, the tensors are on {device}")
+
+
+def _launch(device, stream, call, tensors):
+    """Run call(stream address) on `stream`, or on the device's current stream,
+    with `device` current.  On a given stream the tensors' memory is kept from
+    other use until the stream has passed this point."""
+    import torch
+    _check_place(device, stream)
+    if device.index == torch.cuda.current_device():
+        _check(call(_stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(call(_stream(stream)))
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def mxfp4_quantize(x, codes=None, scales=None, stream=None):
+    """codes uint8 [rows, cols/2] and scales uint8 [rows, cols/32] of a bf16 or
+    fp32 matrix [rows, cols], cols a multiple of 32 (moe_mxfp4_quantize).  The
+    rows of x must be contiguous; they may be a slice of wider ones."""
+    import torch
+    ld = _rows(x, "x", (torch.bfloat16, torch.float32), None, None)
+    rows, cols = x.shape
+    if cols <= 0 or cols % 32:
+        raise MoeError(MOE_ERR_SHAPE, f"cols must be a positive multiple of 32, got {cols}")
+    dev = x.device
+    if codes is None:
+        codes = _new((rows, cols // 2), torch.uint8, dev, stream)
+    else:
+        _need_shape(codes, "codes", torch.uint8, (rows, cols // 2), dev)
+        _apart(codes, "codes", ("x", x))
+    if scales is None:
+        scales = _new((rows, cols // 32), torch.uint8, dev, stream)
+    else:
+        _need_shape(scales, "scales", torch.uint8, (rows, cols // 32), dev)
+        _apart(scales, "scales", ("x", x), ("codes", codes))
+    code = MOE_BF16 if x.dtype == torch.bfloat16 else MOE_F32
+    _launch(dev, stream, lambda s: load_library().moe_mxfp4_quantize(x.data_ptr(), code, rows, cols, ld,
+                                                                     codes.data_ptr(), scales.data_ptr(), s),
+            (x, codes, scales))
+    return codes, scales
+
+
+def _mxfp4_operand(codes, scales, name: str, device):
+    """(rows, K) of an MXFP4 operand, its tensors checked."""
+    import torch
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+        raise _arg_error(f"{name}codes must be a 2-D torch.Tensor [rows, cols/2]")
+    rows, half = codes.shape
+    device = codes.device if device is None else device
+    _need_shape(codes, f"{name}codes", torch.uint8, (rows, half), device)
+    if half == 0 or half % 16:
+        raise MoeError(MOE_ERR_SHAPE, f"{name}codes must have a positive multiple of 16 columns, got {half}")
+    _need_shape(scales, f"{name}scales", torch.uint8, (rows, half // 16), device)
+    return rows, 2 * half
+
+
+def mxfp4_dequantize(codes, scales, dtype=None, out=None, stream=None):
+    """The values [rows, cols] that codes [rows, cols/2] and scales [rows, cols/32]
+    stand for, in bf16 (default) or fp32, exact (moe_mxfp4_dequantize)."""
+    import torch
+    rows, cols = _mxfp4_operand(codes, scales, "", None)
+    dev = codes.device
+    if out is None:
+        dtype = torch.bfloat16 if dtype is None else dtype
+        code = _dtype_code(dtype, "dtype")
+        out = _new((rows, cols), dtype, dev, stream)
+    else:
+        dtype = getattr(out, "dtype", None) if dtype is None else dtype
+        code = _dtype_code(dtype, "out")
+        _need_shape(out, "out", dtype, (rows, cols), dev)
+        _apart(out, "out", ("codes", codes), ("scales", scales))
+    _launch(dev, stream, lambda s: load_library().moe_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols,
+                                                                       code, out.data_ptr(), s),
+            (codes, scales, out))
+    return out
+
+
+def mxfp4_matmul(a_codes, a_scales, b_codes, b_scales, dtype=None, out=None, stream=None):
+    """A B^T [m, n] of two MXFP4 matrices A [m, k] and B [n, k], summed in fp32 and
+    rounded once to bf16 (default) or left in fp32 (moe_mxfp4_matmul)."""
+    import torch
+    m, k = _mxfp4_operand(a_codes, a_scales, "a_", None)
+    dev = a_codes.device
+    n, kb = _mxfp4_operand(b_codes, b_scales, "b_", dev)
+    if kb != k:
+        raise MoeError(MOE_ERR_SHAPE, f"A has {k} columns and B {kb}")
+    if out is None:
+        dtype = torch.bfloat16 if dtype is None else dtype
+        code = _dtype_code(dtype, "dtype")
+        out = _new((m, n), dtype, dev, stream)
+    else:
+        dtype = getattr(out, "dtype", None) if dtype is None else dtype
+        code = _dtype_code(dtype, "out")
+        _need_shape(out, "out", dtype, (m, n), dev)
+        _apart(out, "out", ("a_codes", a_codes), ("a_scales", a_scales), ("b_codes", b_codes), ("b_scales", b_scales))
+    _launch(dev, stream, lambda s: load_library().moe_mxfp4_matmul(
+        a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(), b_scales.data_ptr(), m, n, k, code,
+        out.data_ptr(), s), (a_codes, a_scales, b_codes, b_scales, out))
+    return out
+
+
+def _grouped(w, offsets, device):
+    import torch
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise _arg_error("w must be a 3-D torch.Tensor [num_groups, n, k]")
+    _need_shape(w, "w", torch.bfloat16, w.shape, device)
+    _need_shape(offsets, "offsets", torch.int32, (w.shape[0] + 1,), device)
+    return w.shape
+
+
+def grouped_matmul(x, w, offsets, out=None, stream=None):
+    """out [rows, n] bf16 with out[r] = w[e] @ x[r] for offsets[e] <= r < offsets[e+1]
+    (moe_grouped_matmul): x [rows, k] bf16 (its rows contiguous), w [num_groups, n, k]
+    bf16, offsets [num_groups + 1] int32 on the device, as Plan.route gives them.
+    Rows outside every group are left as they were (undefined in a new `out`)."""
+    import torch
+    groups, n, k = _grouped(w, offsets, w.device if isinstance(w, torch.Tensor) else None)
+    dev = w.device
+    ld = _rows(x, "x", (torch.bfloat16,), k, dev)
+    rows = x.shape[0]
+    if out is None:
+        out = _new((rows, n), torch.bfloat16, dev, stream)
+    else:
+        _need_shape(out, "out", torch.bfloat16, (rows, n), dev)
+        _apart(out, "out", ("x", x), ("w", w), ("offsets", offsets))
+    _launch(dev, stream, lambda s: load_library().moe_grouped_matmul(
+        x.data_ptr(), ld, w.data_ptr(), offsets.data_ptr(), rows, groups, n, k, out.data_ptr(), s),
+            (x, w, offsets, out))
+    return out
+
+
+def grouped_matmul_backward(dy, x, w, offsets, dx=None, dw=None, dw_dtype=None, need_dx=True, need_dw=True,
+                            stream=None):
+    """(dx, dw) of grouped_matmul for dy [rows, n] bf16: dx [rows, k] bf16 (rows
+    outside every group are left as they were), dw [num_groups, n, k] in fp32
+    (default) or bf16, zero for an empty group (moe_grouped_matmul_dx / _dw).
+    need_dx / need_dw False: that gradient is not computed and returned as None
+    (x is not read without need_dw and may then be None)."""
+    import torch
+    groups, n, k = _grouped(w, offsets, w.device if isinstance(w, torch.Tensor) else None)
+    dev = w.device
+    lddy = _rows(dy, "dy", (torch.bfloat16,), n, dev)
+    rows = dy.shape[0]
+    lib = load_library()
+    if need_dw:
+        ldx = _rows(x, "x", (torch.bfloat16,), k, dev)
+        if x.shape[0] != rows:
+            raise _arg_error(f"x must have dy's {rows} rows, got shape {tuple(x.shape)}")
+        if dw is None:
+            dw_dtype = torch.float32 if dw_dtype is None else dw_dtype
+            code = _dtype_code(dw_dtype, "dw_dtype")
+            dw = _new((groups, n, k), dw_dtype, dev, stream)
+        else:
+            dw_dtype = getattr(dw, "dtype", None) if dw_dtype is None else dw_dtype
+            code = _dtype_code(dw_dtype, "dw")
+            _need_shape(dw, "dw", dw_dtype, (groups, n, k), dev)
+            _apart(dw, "dw", ("dy", dy), ("x", x), ("w", w), ("offsets", offsets))
+    else:
+        dw = None
+    if need_dx:
+        if dx is None:
+            dx = _new((rows, k), torch.bfloat16, dev, stream)
+        else:
+            _need_shape(dx, "dx", torch.bfloat16, (rows, k), dev)
+            _apart(dx, "dx", ("dy", dy), ("w", w), ("offsets", offsets))
+            if need_dw:
+                _apart(dx, "dx", ("x", x), ("dw", dw))
+    else:
+        dx = None
+
+    def call(s):
+        status = 0
+        if need_dx:
+            status = lib.moe_grouped_matmul_dx(dy.data_ptr(), lddy, w.data_ptr(), offsets.data_ptr(), rows, groups, n,
+                                               k, dx.data_ptr(), s)
+        if status == 0 and need_dw:
+            status = lib.moe_grouped_matmul_dw(dy.data_ptr(), lddy, x.data_ptr(), ldx, offsets.data_ptr(), rows,
+                                               groups, n, k, code, dw.data_ptr(), s)
+        return status
+
+    _launch(dev, stream, call, [t for t in (dy, x if need_dw else None, w, offsets, dx, dw) if t is not None])
+    return dx, dw
 
 
 MOE_PROBE_READ, MOE_PROBE_READ_NT, MOE_PROBE_COPY = 0, 1, 2

@@ -160,6 +160,30 @@ hipError_t launch_fused_decode(const FcArgs& f1, const FcArgs& f2, const int32_t
                                const RouteOut& route, uint8_t* sync, uint32_t gen, long long spin_ticks,
                                hipStream_t stream);
 
+// MXFP4 quantiser and its inverse (mxfp4_quant.hip): cols a multiple of 32,
+// ld elements from row to row of x.  Element counts above zero.
+hipError_t launch_mxfp4_quantize(const void* x, bool f32, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
+                                 uint8_t* scales, hipStream_t stream);
+hipError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, bool f32,
+                                   void* out, hipStream_t stream);
+// out [M, N] = A [M, K] B [N, K]^T, both MXFP4 (mxfp4_matmul.hip); K a multiple of 32.
+hipError_t launch_mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
+                               const uint8_t* b_scales, int M, int N, int K, bool f32, void* out, hipStream_t stream);
+
+// Products of ragged row groups with bf16 matrices (grouped.hip): n and k
+// multiples of 8, rows and groups above zero.
+constexpr int kGroupedMaxDim = 65536;
+constexpr int kGroupedMaxGroups = 4096;
+struct GroupedArgs {
+  const void* w;            // [groups, n, k] bf16 (forward, dx)
+  const int32_t* offsets;   // [groups + 1]
+  int rows, groups, n, k;
+};
+hipError_t launch_grouped_forward(const GroupedArgs& a, const void* x, int64_t ldx, void* y, hipStream_t stream);
+hipError_t launch_grouped_dx(const GroupedArgs& a, const void* dy, int64_t lddy, void* dx, hipStream_t stream);
+hipError_t launch_grouped_dw(const GroupedArgs& a, const void* dy, int64_t lddy, const void* x, int64_t ldx, bool f32,
+                             void* dw, hipStream_t stream);
+
 // Router top-k (E <= kRouterMaxExperts, k <= 32).
 constexpr int kRouterMaxExperts = 1024;
 hipError_t launch_router_topk(const float* logits, int32_t T, int32_t E, int32_t k, int32_t* ids, float* weights,

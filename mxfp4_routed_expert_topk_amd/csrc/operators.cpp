@@ -1,0 +1,151 @@
+// C entries of the MXFP4 quantiser and product and of the grouped products:
+// argument checks before any launch, then one enqueue.  Nothing here allocates
+// or synchronises, so every call may be captured in a graph.
+#include <hip/hip_runtime.h>
+
+#include "../../include/moe_mxfp4.h"
+#include "moe_internal.h"
+#include "plan.h"
+
+namespace {
+
+using moe::fail;
+using moe::hip_fail;
+using moe::ok;
+
+constexpr int32_t kMaxMatrixRows = 1 << 24;   // quantiser rows, grouped rows
+constexpr int32_t kMaxMatmulDim = 1 << 19;
+constexpr int32_t kMaxMatmulK = 1 << 16;
+constexpr int64_t kMaxLd = 1 << 20;
+
+struct Ptr {
+  const char* name;
+  const void* p;
+};
+
+template <int N>
+moe_status check_ptrs(const Ptr (&ptrs)[N]) {
+  for (const Ptr& q : ptrs) {
+    if (!q.p) return fail(MOE_ERR_ARG, "%s is null", q.name);
+    if (reinterpret_cast<uintptr_t>(q.p) & 15u)
+      return fail(MOE_ERR_ALIGN, "%s must be 16-byte aligned, got %p", q.name, q.p);
+  }
+  return MOE_OK;
+}
+
+moe_status check_dtype(const char* name, int32_t dtype) {
+  if (dtype != MOE_BF16 && dtype != MOE_F32)
+    return fail(MOE_ERR_ARG, "%s must be MOE_BF16 (0) or MOE_F32 (1), got %d", name, dtype);
+  return MOE_OK;
+}
+
+moe_status check_matrix(int32_t rows, int32_t cols) {
+  if (rows < 0) return fail(MOE_ERR_ARG, "rows must be >= 0, got %d", rows);
+  if (rows > kMaxMatrixRows) return fail(MOE_ERR_SHAPE, "rows must be at most %d, got %d", kMaxMatrixRows, rows);
+  if (cols <= 0 || cols % 32) return fail(MOE_ERR_SHAPE, "cols must be a positive multiple of 32, got %d", cols);
+  return MOE_OK;
+}
+
+moe_status check_grouped(int32_t rows, int32_t groups, int32_t n, int32_t k) {
+  if (rows < 0) return fail(MOE_ERR_ARG, "rows must be >= 0, got %d", rows);
+  if (rows > kMaxMatrixRows) return fail(MOE_ERR_SHAPE, "rows must be at most %d, got %d", kMaxMatrixRows, rows);
+  if (groups < 0) return fail(MOE_ERR_ARG, "num_groups must be >= 0, got %d", groups);
+  if (groups > moe::kGroupedMaxGroups)
+    return fail(MOE_ERR_SHAPE, "num_groups must be at most %d, got %d", moe::kGroupedMaxGroups, groups);
+  if (n < 8 || n > moe::kGroupedMaxDim || n % 8)
+    return fail(MOE_ERR_SHAPE, "n must be a multiple of 8 in [8, %d], got %d", moe::kGroupedMaxDim, n);
+  if (k < 8 || k > moe::kGroupedMaxDim || k % 8)
+    return fail(MOE_ERR_SHAPE, "k must be a multiple of 8 in [8, %d], got %d", moe::kGroupedMaxDim, k);
+  return MOE_OK;
+}
+
+moe_status check_ld(const char* name, int64_t ld, int32_t cols) {
+  if (ld < cols || ld > kMaxLd || ld % 8)
+    return fail(MOE_ERR_SHAPE, "%s must be a multiple of 8 in [%d, %lld], got %lld", name, cols, (long long)kMaxLd,
+                (long long)ld);
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_mxfp4_quantize(const void* x, int32_t dtype, int32_t rows, int32_t cols, int64_t ldx, uint8_t* codes,
+                              uint8_t* scales, hipStream_t stream) {
+  if (moe_status s = check_dtype("dtype", dtype)) return s;
+  if (moe_status s = check_matrix(rows, cols)) return s;
+  const int unit = dtype == MOE_F32 ? 4 : 8;   // elements in 16 bytes
+  if (ldx < cols || ldx % unit)
+    return fail(MOE_ERR_SHAPE, "ldx must be a multiple of %d of at least cols=%d, got %lld", unit, cols, (long long)ldx);
+  if (rows == 0) return ok();
+  if (moe_status s = check_ptrs({{"x", x}, {"codes", codes}, {"scales", scales}})) return s;
+  const hipError_t e = moe::launch_mxfp4_quantize(x, dtype == MOE_F32, rows, cols, ldx, codes, scales, stream);
+  return e == hipSuccess ? ok() : hip_fail(e, "mxfp4 quantise launch");
+}
+
+moe_status moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t rows, int32_t cols, int32_t dtype,
+                                void* out, hipStream_t stream) {
+  if (moe_status s = check_dtype("dtype", dtype)) return s;
+  if (moe_status s = check_matrix(rows, cols)) return s;
+  if (rows == 0) return ok();
+  if (moe_status s = check_ptrs({{"codes", codes}, {"scales", scales}, {"out", out}})) return s;
+  const hipError_t e = moe::launch_mxfp4_dequantize(codes, scales, rows, cols, dtype == MOE_F32, out, stream);
+  return e == hipSuccess ? ok() : hip_fail(e, "mxfp4 dequantise launch");
+}
+
+moe_status moe_mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
+                            const uint8_t* b_scales, int32_t m, int32_t n, int32_t k, int32_t dtype, void* out,
+                            hipStream_t stream) {
+  if (moe_status s = check_dtype("dtype", dtype)) return s;
+  if (m < 0 || n < 0) return fail(MOE_ERR_ARG, "m and n must be >= 0, got m=%d n=%d", m, n);
+  if (m > kMaxMatmulDim || n > kMaxMatmulDim)
+    return fail(MOE_ERR_SHAPE, "m and n must be at most %d, got m=%d n=%d", kMaxMatmulDim, m, n);
+  if (k < 32 || k > kMaxMatmulK || k % 32)
+    return fail(MOE_ERR_SHAPE, "k must be a multiple of 32 in [32, %d], got %d", kMaxMatmulK, k);
+  if (m == 0 || n == 0) return ok();
+  if (moe_status s = check_ptrs({{"a_codes", a_codes}, {"a_scales", a_scales}, {"b_codes", b_codes},
+                                 {"b_scales", b_scales}, {"out", out}}))
+    return s;
+  const hipError_t e =
+      moe::launch_mxfp4_matmul(a_codes, a_scales, b_codes, b_scales, m, n, k, dtype == MOE_F32, out, stream);
+  return e == hipSuccess ? ok() : hip_fail(e, "mxfp4 matmul launch");
+}
+
+moe_status moe_grouped_matmul(const uint16_t* x, int64_t ldx, const uint16_t* w, const int32_t* offsets, int32_t rows,
+                              int32_t num_groups, int32_t n, int32_t k, uint16_t* out, hipStream_t stream) {
+  if (moe_status s = check_grouped(rows, num_groups, n, k)) return s;
+  if (moe_status s = check_ld("ldx", ldx, k)) return s;
+  if (rows == 0 || num_groups == 0) return ok();
+  if (moe_status s = check_ptrs({{"x", x}, {"w", w}, {"offsets", offsets}, {"out", out}})) return s;
+  const hipError_t e = moe::launch_grouped_forward({w, offsets, rows, num_groups, n, k}, x, ldx, out, stream);
+  return e == hipSuccess ? ok() : hip_fail(e, "grouped matmul launch");
+}
+
+moe_status moe_grouped_matmul_dx(const uint16_t* dy, int64_t lddy, const uint16_t* w, const int32_t* offsets,
+                                 int32_t rows, int32_t num_groups, int32_t n, int32_t k, uint16_t* dx,
+                                 hipStream_t stream) {
+  if (moe_status s = check_grouped(rows, num_groups, n, k)) return s;
+  if (moe_status s = check_ld("lddy", lddy, n)) return s;
+  if (rows == 0 || num_groups == 0) return ok();
+  if (moe_status s = check_ptrs({{"dy", dy}, {"w", w}, {"offsets", offsets}, {"dx", dx}})) return s;
+  const hipError_t e = moe::launch_grouped_dx({w, offsets, rows, num_groups, n, k}, dy, lddy, dx, stream);
+  return e == hipSuccess ? ok() : hip_fail(e, "grouped matmul dx launch");
+}
+
+moe_status moe_grouped_matmul_dw(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx,
+                                 const int32_t* offsets, int32_t rows, int32_t num_groups, int32_t n, int32_t k,
+                                 int32_t dtype, void* dw, hipStream_t stream) {
+  if (moe_status s = check_dtype("dtype", dtype)) return s;
+  if (moe_status s = check_grouped(rows, num_groups, n, k)) return s;
+  if (moe_status s = check_ld("lddy", lddy, n)) return s;
+  if (moe_status s = check_ld("ldx", ldx, k)) return s;
+  if (num_groups == 0) return ok();
+  if (moe_status s = check_ptrs({{"offsets", offsets}, {"dw", dw}})) return s;
+  if (rows > 0)   // without rows every gradient is zero and neither is read
+    if (moe_status s = check_ptrs({{"dy", dy}, {"x", x}})) return s;
+  const hipError_t e = moe::launch_grouped_dw({nullptr, offsets, rows, num_groups, n, k}, dy, lddy, x, ldx,
+                                              dtype == MOE_F32, dw, stream);
+  return e == hipSuccess ? ok() : hip_fail(e, "grouped matmul dw launch");
+}
+
+}  // extern "C"

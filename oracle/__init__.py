@@ -11,6 +11,7 @@ module):
   route    per-expert counts, offsets, stable permutation (two formulations)
   router   router top-k ids and softmax route weights from logits (upstream of the layer)
   moe      fp64 forward of the layer, MXFP8 activation quantisation
+  operators  MXFP4 quantiser and product, products of ragged row groups and their gradients
   brute    scalar-loop brute force for tiny shapes
   compare  the acceptance rule (3 bf16 ULP or 4e-3 row relative L2)
 
@@ -28,6 +29,8 @@ from .router import router_topk, router_topk_np
 from .moe import (expert_mlp, forward, fp32_dot_bound, mxfp8_dequantize, mxfp8_quantize, silu_prime,
                   mxfp8_requant_check, mxfp8_quantum, mxfp8_roundtrip, mxfp8_scale_exponent, silu, h_uncertainty)
 from .compare import check_rows, rel_l2
+from .operators import (e2m1_encode, grouped_matmul, grouped_matmul_backward, mxfp4_matmul, mxfp4_quantize,
+                        mxfp4_scale_exponent, mxfp4_values)
 from .brute import forward_brute, e2m1_closed_form
 
 __all__ = [n for n in dir() if not n.startswith("_")]

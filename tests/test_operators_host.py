@@ -1,0 +1,172 @@
+"""Refusals of the MXFP4 quantiser and product and of the grouped products:
+the C entries' checks (no GPU is touched) and the binding's."""
+import os
+
+import pytest
+import torch
+
+import mxfp4_routed_expert_topk_amd as moe
+
+BF, F32, U8, I32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(moe.LIB_PATH):
+        pytest.fail(f"library not built at {moe.LIB_PATH}: run python -m mxfp4_routed_expert_topk_amd.build")
+    return moe.load_library()
+
+
+def refused(lib, fn, args, status, needle):
+    assert getattr(lib, fn)(*args) == status, (fn, args)
+    assert needle in lib.moe_mxfp4_last_error().decode(), lib.moe_mxfp4_last_error()
+
+
+P = 64   # a pointer that is aligned and never read
+
+
+@pytest.mark.parametrize("args,status,needle", [
+    ((P, 2, 4, 64, 64, P, P, None), 1, "dtype must be MOE_BF16"),
+    ((P, 0, -1, 64, 64, P, P, None), 1, "rows must be >= 0"),
+    ((P, 0, (1 << 24) + 1, 64, 64, P, P, None), 2, "rows must be at most"),
+    ((P, 0, 4, 48, 48, P, P, None), 2, "multiple of 32"),
+    ((P, 0, 4, 0, 0, P, P, None), 2, "multiple of 32"),
+    ((P, 0, 4, 64, 32, P, P, None), 2, "ldx must be"),
+    ((P, 0, 4, 64, 68, P, P, None), 2, "ldx must be a multiple of 8"),
+    ((P, 1, 4, 64, 66, P, P, None), 2, "ldx must be a multiple of 4"),
+    ((None, 0, 4, 64, 64, P, P, None), 1, "x is null"),
+    ((P, 0, 4, 64, 64, P + 4, P, None), 3, "codes must be 16-byte aligned"),
+    ((P, 0, 4, 64, 64, P, P + 1, None), 3, "scales must be 16-byte aligned"),
+])
+def test_quantize_refusals(lib, args, status, needle):
+    refused(lib, "moe_mxfp4_quantize", args, status, needle)
+
+
+@pytest.mark.parametrize("args,status,needle", [
+    ((P, P, 4, 64, 3, P, None), 1, "dtype must be"),
+    ((P, P, -4, 64, 0, P, None), 1, "rows must be >= 0"),
+    ((P, P, 4, 33, 0, P, None), 2, "multiple of 32"),
+    ((P, None, 4, 64, 0, P, None), 1, "scales is null"),
+    ((P, P, 4, 64, 1, P + 8, None), 3, "out must be 16-byte aligned"),
+])
+def test_dequantize_refusals(lib, args, status, needle):
+    refused(lib, "moe_mxfp4_dequantize", args, status, needle)
+
+
+@pytest.mark.parametrize("args,status,needle", [
+    ((P, P, P, P, 4, 4, 64, -1, P, None), 1, "dtype must be"),
+    ((P, P, P, P, -1, 4, 64, 0, P, None), 1, "m and n must be >= 0"),
+    ((P, P, P, P, 4, (1 << 19) + 1, 64, 0, P, None), 2, "m and n must be at most"),
+    ((P, P, P, P, 4, 4, 40, 0, P, None), 2, "k must be a multiple of 32"),
+    ((P, P, P, P, 4, 4, 0, 0, P, None), 2, "k must be a multiple of 32"),
+    ((P, P, P, P, 4, 4, 65568, 0, P, None), 2, "k must be a multiple of 32"),
+    ((P, P, None, P, 4, 4, 64, 0, P, None), 1, "b_codes is null"),
+    ((P, P + 2, P, P, 4, 4, 64, 0, P, None), 3, "a_scales must be 16-byte aligned"),
+])
+def test_matmul_refusals(lib, args, status, needle):
+    refused(lib, "moe_mxfp4_matmul", args, status, needle)
+
+
+@pytest.mark.parametrize("args,status,needle", [
+    ((P, 64, P, P, -1, 2, 16, 64, P, None), 1, "rows must be >= 0"),
+    ((P, 64, P, P, (1 << 24) + 1, 2, 16, 64, P, None), 2, "rows must be at most"),
+    ((P, 64, P, P, 4, -1, 16, 64, P, None), 1, "num_groups must be >= 0"),
+    ((P, 64, P, P, 4, 4097, 16, 64, P, None), 2, "num_groups must be at most"),
+    ((P, 64, P, P, 4, 2, 12, 64, P, None), 2, "n must be a multiple of 8"),
+    ((P, 64, P, P, 4, 2, 0, 64, P, None), 2, "n must be a multiple of 8"),
+    ((P, 65, P, P, 4, 2, 16, 65, P, None), 2, "k must be a multiple of 8"),
+    ((P, 65544, P, P, 4, 2, 16, 65544, P, None), 2, "k must be a multiple of 8"),
+    ((P, 56, P, P, 4, 2, 16, 64, P, None), 2, "ldx must be"),
+    ((P, 68, P, P, 4, 2, 16, 64, P, None), 2, "ldx must be a multiple of 8"),
+    ((P, (1 << 20) + 8, P, P, 4, 2, 16, 64, P, None), 2, "ldx must be"),
+    ((P, 64, None, P, 4, 2, 16, 64, P, None), 1, "w is null"),
+    ((P, 64, P, P + 4, 4, 2, 16, 64, P, None), 3, "offsets must be 16-byte aligned"),
+])
+def test_grouped_matmul_refusals(lib, args, status, needle):
+    refused(lib, "moe_grouped_matmul", args, status, needle)
+
+
+@pytest.mark.parametrize("fn,args,status,needle", [
+    ("moe_grouped_matmul_dx", (P, 8, P, P, 4, 2, 16, 64, P, None), 2, "lddy must be"),
+    ("moe_grouped_matmul_dx", (P, 16, P, P, 4, 2, 16, 64, None, None), 1, "dx is null"),
+    ("moe_grouped_matmul_dw", (P, 16, P, 64, P, 4, 2, 16, 64, 7, P, None), 1, "dtype must be"),
+    ("moe_grouped_matmul_dw", (P, 8, P, 64, P, 4, 2, 16, 64, 0, P, None), 2, "lddy must be"),
+    ("moe_grouped_matmul_dw", (P, 16, P, 56, P, 4, 2, 16, 64, 0, P, None), 2, "ldx must be"),
+    ("moe_grouped_matmul_dw", (P, 16, None, 64, P, 4, 2, 16, 64, 0, P, None), 1, "x is null"),
+    ("moe_grouped_matmul_dw", (P, 16, P, 64, P, 4, 2, 16, 64, 0, P + 2, None), 3, "dw must be 16-byte aligned"),
+])
+def test_grouped_gradient_refusals(lib, fn, args, status, needle):
+    refused(lib, fn, args, status, needle)
+
+
+def test_empty_calls_are_no_ops(lib):
+    assert lib.moe_mxfp4_quantize(None, 0, 0, 64, 64, None, None, None) == 0
+    assert lib.moe_mxfp4_dequantize(None, None, 0, 64, 0, None, None) == 0
+    assert lib.moe_mxfp4_matmul(None, None, None, None, 0, 5, 64, 0, None, None) == 0
+    assert lib.moe_mxfp4_matmul(None, None, None, None, 5, 0, 64, 0, None, None) == 0
+    assert lib.moe_grouped_matmul(None, 64, None, None, 0, 2, 16, 64, None, None) == 0
+    assert lib.moe_grouped_matmul(None, 64, None, None, 4, 0, 16, 64, None, None) == 0
+    assert lib.moe_grouped_matmul_dx(None, 16, None, None, 0, 2, 16, 64, None, None) == 0
+    assert lib.moe_grouped_matmul_dw(None, 16, None, 64, None, 4, 0, 16, 64, 0, None, None) == 0
+
+
+def z(*shape, dtype=BF):
+    return torch.zeros(shape, dtype=dtype)
+
+
+@pytest.mark.parametrize("call,status,needle", [
+    (lambda: moe.mxfp4_quantize([1.0]), 1, "x must be a torch.Tensor"),
+    (lambda: moe.mxfp4_quantize(z(4, 64, dtype=torch.float16)), 1, "x must be torch.bfloat16 or torch.float32"),
+    (lambda: moe.mxfp4_quantize(z(64)), 1, "x must be [rows, cols]"),
+    (lambda: moe.mxfp4_quantize(z(4, 48)), 2, "multiple of 32"),
+    (lambda: moe.mxfp4_quantize(z(4, 128)[:, ::2]), 1, "rows of x must be contiguous"),
+    (lambda: moe.mxfp4_quantize(z(64, 64).t()), 1, "rows of x must be contiguous"),
+    (lambda: moe.mxfp4_quantize(z(4, 64), codes=z(4, 64, dtype=U8)), 1, "codes must have shape (4, 32)"),
+    (lambda: moe.mxfp4_quantize(z(4, 64), scales=z(4, 2)), 1, "scales must be torch.uint8"),
+    (lambda: moe.mxfp4_quantize(z(4, 64)), 1, "must be on a GPU"),
+    (lambda: moe.mxfp4_dequantize(z(4, 32), z(4, 2, dtype=U8)), 1, "codes must be torch.uint8"),
+    (lambda: moe.mxfp4_dequantize(z(4, 24, dtype=U8), z(4, 1, dtype=U8)), 2, "positive multiple of 16 columns"),
+    (lambda: moe.mxfp4_dequantize(z(4, 32, dtype=U8), z(4, 3, dtype=U8)), 1, "scales must have shape (4, 2)"),
+    (lambda: moe.mxfp4_dequantize(z(4, 32, dtype=U8), z(4, 2, dtype=U8), dtype=torch.float16), 1, "dtype must be"),
+    (lambda: moe.mxfp4_dequantize(z(4, 32, dtype=U8), z(4, 2, dtype=U8), dtype=BF, out=z(4, 64, dtype=F32)), 1,
+     "out must be torch.bfloat16"),
+    (lambda: moe.mxfp4_dequantize(z(4, 32, dtype=U8), z(4, 2, dtype=U8)), 1, "must be on a GPU"),
+    (lambda: moe.mxfp4_matmul(z(4, 32, dtype=U8), z(4, 2, dtype=U8), z(5, 16, dtype=U8), z(5, 1, dtype=U8)), 2,
+     "A has 64 columns and B 32"),
+    (lambda: moe.mxfp4_matmul(z(4, 64, dtype=U8)[:, ::2], z(4, 2, dtype=U8), z(5, 32, dtype=U8), z(5, 2, dtype=U8)), 1,
+     "a_codes must be contiguous"),
+    (lambda: moe.mxfp4_matmul(z(4, 32, dtype=U8), z(4, 2, dtype=U8), z(5, 32, dtype=U8), z(5, 2, dtype=U8),
+                              out=z(4, 4)), 1, "out must have shape (4, 5)"),
+    (lambda: moe.grouped_matmul(z(4, 64), z(2, 16, 32), z(3, dtype=I32)), 1, "x must be [rows, 32]"),
+    (lambda: moe.grouped_matmul(z(4, 64), z(2, 16, 64), z(3, dtype=torch.int64)), 1, "offsets must be torch.int32"),
+    (lambda: moe.grouped_matmul(z(4, 64), z(2, 16, 64), z(2, dtype=I32)), 1, "offsets must have shape (3,)"),
+    (lambda: moe.grouped_matmul(z(4, 64), z(2, 64, 16).transpose(1, 2), z(3, dtype=I32)), 1, "w must be contiguous"),
+    (lambda: moe.grouped_matmul(z(4, 64), z(16, 64), z(3, dtype=I32)), 1, "w must be a 3-D"),
+    (lambda: moe.grouped_matmul(z(4, 64, dtype=F32), z(2, 16, 64), z(3, dtype=I32)), 1, "x must be torch.bfloat16"),
+    (lambda: moe.grouped_matmul(z(4, 64), z(2, 16, 64), z(3, dtype=I32), out=z(4, 16, dtype=F32)), 1,
+     "out must be torch.bfloat16"),
+    (lambda: moe.grouped_matmul(z(4, 64), z(2, 16, 64), z(3, dtype=I32)), 1, "must be on a GPU"),
+    (lambda: moe.grouped_matmul_backward(z(4, 64), z(4, 64), z(2, 16, 64), z(3, dtype=I32)), 1, "dy must be [rows, 16]"),
+    (lambda: moe.grouped_matmul_backward(z(4, 16), z(3, 64), z(2, 16, 64), z(3, dtype=I32)), 1, "x must have dy's 4 rows"),
+    (lambda: moe.grouped_matmul_backward(z(4, 16), z(4, 64), z(2, 16, 64), z(3, dtype=I32), dw_dtype=torch.float16), 1,
+     "dw_dtype must be"),
+    (lambda: moe.grouped_matmul_backward(z(4, 16), z(4, 64), z(2, 16, 64), z(3, dtype=I32), dx=z(3, 64)), 1,
+     "dx must have shape (4, 64)"),
+])
+def test_binding_refusals(lib, call, status, needle):
+    with pytest.raises(moe.MoeError) as ei:
+        call()
+    assert ei.value.status == status and needle in ei.value.message, ei.value.message
+
+
+def test_binding_refuses_overlapping_outputs(lib):
+    x = z(8, 64)
+    with pytest.raises(moe.MoeError, match="out must not overlap x"):
+        moe.grouped_matmul(x, z(2, 64, 64), z(3, dtype=I32), out=x)
+    w = z(2, 64, 64)
+    with pytest.raises(moe.MoeError, match="dw must not overlap w"):
+        moe.grouped_matmul_backward(z(4, 64), z(4, 64), w, z(3, dtype=I32), dw=w)
+    # disjoint halves of one buffer are fine as far as the memory goes
+    both = z(8, 64)
+    with pytest.raises(moe.MoeError, match="must be on a GPU"):
+        moe.grouped_matmul(both[:4], z(2, 64, 64), z(3, dtype=I32), out=both[4:])
