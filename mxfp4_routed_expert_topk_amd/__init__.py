@@ -328,33 +328,39 @@ def mxfp8_quantize(x_bf16, stream=None):
 
 MOE_BF16, MOE_F32 = 0, 1
 
+# The entry points below serve single tokens too, where a call's own time on
+# the host counts (an empty launch takes 3.5 us of it): checks compare what is
+# cheap to read first and word the error only once one has failed.
+
 
 def _dtype_code(dtype, name: str) -> int:
     import torch
-    if dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         return MOE_BF16
-    if dtype == torch.float32:
+    if dtype is torch.float32:
         return MOE_F32
     raise _arg_error(f"{name} must be torch.bfloat16 or torch.float32, got {dtype}")
 
 
-def _need_shape(t, name: str, dtype, shape, device):
+def _need_shape(t, name: str, dtype, shape, like):
     """Raise MoeError(MOE_ERR_ARG) unless `t` is a contiguous tensor of `dtype`
-    and exactly `shape` on `device`."""
+    and exactly `shape` on the device of the tensor `like`."""
     import torch
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == like.device \
+            and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise _arg_error(f"{name} must be a torch.Tensor, got {type(t).__name__}")
     if t.dtype != dtype:
         raise _arg_error(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise _arg_error(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise _arg_error(f"{name} must be on {device}, got {t.device}")
-    if not t.is_contiguous():
-        raise _arg_error(f"{name} must be contiguous")
+    if t.device != like.device:
+        raise _arg_error(f"{name} must be on {like.device}, got {t.device}")
+    raise _arg_error(f"{name} must be contiguous")
 
 
-def _rows(t, name: str, dtypes, cols: Optional[int], device):
+def _rows(t, name: str, dtypes, cols: Optional[int], like):
     """The row stride (elements) of a matrix whose rows are contiguous;
     MoeError(MOE_ERR_ARG) otherwise."""
     import torch
@@ -364,55 +370,64 @@ def _rows(t, name: str, dtypes, cols: Optional[int], device):
         raise _arg_error(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
         raise _arg_error(f"{name} must be [rows, {'cols' if cols is None else cols}], got shape {tuple(t.shape)}")
-    if device is not None and t.device != device:
-        raise _arg_error(f"{name} must be on {device}, got {t.device}")
-    rows, width = t.shape
+    if like is not None and t.device != like.device:
+        raise _arg_error(f"{name} must be on {like.device}, got {t.device}")
+    if t.is_contiguous():
+        return t.shape[1]
     row_stride, step = t.stride()
-    if width > 1 and step != 1:
+    if step != 1 and t.shape[1] > 1:
         raise _arg_error(f"the rows of {name} must be contiguous, got strides {t.stride()}")
-    return row_stride if rows > 1 else width
+    return row_stride if t.shape[0] > 1 else t.shape[1]
 
 
 def _apart(out, name: str, *inputs):
-    """Raise MoeError(MOE_ERR_ARG) if the memory of `out` and of an input overlap."""
-    lo, hi = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
+    """Raise MoeError(MOE_ERR_ARG) if the memory of the contiguous `out` and of
+    an input overlap; inputs are given as (name, tensor), with their strides
+    descending."""
+    lo = out.data_ptr()
+    hi = lo + out.numel() * out.element_size()
     for other, t in inputs:
-        n = t.numel()
-        if n == 0 or lo == hi:
+        at = t.data_ptr()
+        if at >= hi or lo == hi or t.numel() == 0:
             continue
-        span = 1 + sum((d - 1) * s for d, s in zip(t.shape, t.stride()))
-        if t.data_ptr() < hi and lo < t.data_ptr() + span * t.element_size():
+        if at + ((t.shape[0] - 1) * t.stride(0) + t[0].numel()) * t.element_size() > lo:
             raise _arg_error(f"{name} must not overlap {other}")
 
 
-def _new(shape, dtype, device, stream):
-    """An uninitialised tensor, from the memory of `stream` if one is given."""
+def _new(shape, dtype, like, stream):
+    """An uninitialised tensor on the device of `like`, from the memory of
+    `stream` if one is given."""
     import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _check_place(device, stream):
-    """Raise MoeError(MOE_ERR_ARG) unless `device` is a GPU and `stream`, if given, one of its streams."""
+def _launch(fn, args, like, stream, tensors):
+    """fn(*args, stream) on `stream`, or on the current stream of the tensors'
+    device, with that device current.  On a given stream the tensors' memory is
+    kept from other use until the stream has passed this point."""
+    import torch
+    device = like.device
     if device.type != "cuda":
         raise _arg_error(f"tensors must be on a GPU, got {device}")
-    if stream is not None and stream.device != device:
+    index = device.index
+    if stream is None:
+        # the address behind torch.cuda.current_stream(index), without the
+        # 2.7 us of building the Stream object
+        at = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device != device:
         raise _arg_error(f"stream is of {stream.device}, the tensors are on {device}")
-
-
-def _launch(device, stream, call, tensors):
-    """Run call(stream address) on `stream`, or on the device's current stream,
-    with `device` current.  On a given stream the tensors' memory is kept from
-    other use until the stream has passed this point."""
-    import torch
-    _check_place(device, stream)
-    if device.index == torch.cuda.current_device():
-        _check(call(_stream(stream)))
     else:
-        with torch.cuda.device(device):
-            _check(call(_stream(stream)))
+        at = stream.cuda_stream
+    if index == torch.cuda.current_device():
+        status = fn(*args, at)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, at)
+    if status:
+        _check(status)
     if stream is not None:
         for t in tensors:
             t.record_stream(stream)
@@ -427,55 +442,56 @@ def mxfp4_quantize(x, codes=None, scales=None, stream=None):
     rows, cols = x.shape
     if cols <= 0 or cols % 32:
         raise MoeError(MOE_ERR_SHAPE, f"cols must be a positive multiple of 32, got {cols}")
-    dev = x.device
     if codes is None:
-        codes = _new((rows, cols // 2), torch.uint8, dev, stream)
+        codes = _new((rows, cols // 2), torch.uint8, x, stream)
     else:
-        _need_shape(codes, "codes", torch.uint8, (rows, cols // 2), dev)
+        _need_shape(codes, "codes", torch.uint8, (rows, cols // 2), x)
         _apart(codes, "codes", ("x", x))
     if scales is None:
-        scales = _new((rows, cols // 32), torch.uint8, dev, stream)
+        scales = _new((rows, cols // 32), torch.uint8, x, stream)
     else:
-        _need_shape(scales, "scales", torch.uint8, (rows, cols // 32), dev)
+        _need_shape(scales, "scales", torch.uint8, (rows, cols // 32), x)
         _apart(scales, "scales", ("x", x), ("codes", codes))
-    code = MOE_BF16 if x.dtype == torch.bfloat16 else MOE_F32
-    _launch(dev, stream, lambda s: load_library().moe_mxfp4_quantize(x.data_ptr(), code, rows, cols, ld,
-                                                                     codes.data_ptr(), scales.data_ptr(), s),
-            (x, codes, scales))
+    code = MOE_BF16 if x.dtype is torch.bfloat16 else MOE_F32
+    _launch(load_library().moe_mxfp4_quantize,
+            (x.data_ptr(), code, rows, cols, ld, codes.data_ptr(), scales.data_ptr()), x, stream, (x, codes, scales))
     return codes, scales
 
 
-def _mxfp4_operand(codes, scales, name: str, device):
+def _mxfp4_operand(codes, scales, name: str, like):
     """(rows, K) of an MXFP4 operand, its tensors checked."""
     import torch
     if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
         raise _arg_error(f"{name}codes must be a 2-D torch.Tensor [rows, cols/2]")
     rows, half = codes.shape
-    device = codes.device if device is None else device
-    _need_shape(codes, f"{name}codes", torch.uint8, (rows, half), device)
+    _need_shape(codes, f"{name}codes", torch.uint8, (rows, half), codes if like is None else like)
     if half == 0 or half % 16:
         raise MoeError(MOE_ERR_SHAPE, f"{name}codes must have a positive multiple of 16 columns, got {half}")
-    _need_shape(scales, f"{name}scales", torch.uint8, (rows, half // 16), device)
+    _need_shape(scales, f"{name}scales", torch.uint8, (rows, half // 16), codes)
     return rows, 2 * half
+
+
+def _float_out(out, name: str, shape, dtype, like, stream, *inputs):
+    """(out, its type code): a new tensor of `dtype` (default bf16), or the given
+    one checked against shape, dtype and the inputs' memory."""
+    import torch
+    if out is None:
+        dtype = torch.bfloat16 if dtype is None else dtype
+        code = _dtype_code(dtype, f"{name}_dtype" if name != "out" else "dtype")
+        return _new(shape, dtype, like, stream), code
+    code = _dtype_code(getattr(out, "dtype", None) if dtype is None else dtype, name)
+    _need_shape(out, name, out.dtype if dtype is None else dtype, shape, like)
+    _apart(out, name, *inputs)
+    return out, code
 
 
 def mxfp4_dequantize(codes, scales, dtype=None, out=None, stream=None):
     """The values [rows, cols] that codes [rows, cols/2] and scales [rows, cols/32]
     stand for, in bf16 (default) or fp32, exact (moe_mxfp4_dequantize)."""
-    import torch
     rows, cols = _mxfp4_operand(codes, scales, "", None)
-    dev = codes.device
-    if out is None:
-        dtype = torch.bfloat16 if dtype is None else dtype
-        code = _dtype_code(dtype, "dtype")
-        out = _new((rows, cols), dtype, dev, stream)
-    else:
-        dtype = getattr(out, "dtype", None) if dtype is None else dtype
-        code = _dtype_code(dtype, "out")
-        _need_shape(out, "out", dtype, (rows, cols), dev)
-        _apart(out, "out", ("codes", codes), ("scales", scales))
-    _launch(dev, stream, lambda s: load_library().moe_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols,
-                                                                       code, out.data_ptr(), s),
+    out, code = _float_out(out, "out", (rows, cols), dtype, codes, stream, ("codes", codes), ("scales", scales))
+    _launch(load_library().moe_mxfp4_dequantize,
+            (codes.data_ptr(), scales.data_ptr(), rows, cols, code, out.data_ptr()), codes, stream,
             (codes, scales, out))
     return out
 
@@ -483,33 +499,24 @@ def mxfp4_dequantize(codes, scales, dtype=None, out=None, stream=None):
 def mxfp4_matmul(a_codes, a_scales, b_codes, b_scales, dtype=None, out=None, stream=None):
     """A B^T [m, n] of two MXFP4 matrices A [m, k] and B [n, k], summed in fp32 and
     rounded once to bf16 (default) or left in fp32 (moe_mxfp4_matmul)."""
-    import torch
     m, k = _mxfp4_operand(a_codes, a_scales, "a_", None)
-    dev = a_codes.device
-    n, kb = _mxfp4_operand(b_codes, b_scales, "b_", dev)
+    n, kb = _mxfp4_operand(b_codes, b_scales, "b_", a_codes)
     if kb != k:
         raise MoeError(MOE_ERR_SHAPE, f"A has {k} columns and B {kb}")
-    if out is None:
-        dtype = torch.bfloat16 if dtype is None else dtype
-        code = _dtype_code(dtype, "dtype")
-        out = _new((m, n), dtype, dev, stream)
-    else:
-        dtype = getattr(out, "dtype", None) if dtype is None else dtype
-        code = _dtype_code(dtype, "out")
-        _need_shape(out, "out", dtype, (m, n), dev)
-        _apart(out, "out", ("a_codes", a_codes), ("a_scales", a_scales), ("b_codes", b_codes), ("b_scales", b_scales))
-    _launch(dev, stream, lambda s: load_library().moe_mxfp4_matmul(
-        a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(), b_scales.data_ptr(), m, n, k, code,
-        out.data_ptr(), s), (a_codes, a_scales, b_codes, b_scales, out))
+    out, code = _float_out(out, "out", (m, n), dtype, a_codes, stream, ("a_codes", a_codes), ("a_scales", a_scales),
+                           ("b_codes", b_codes), ("b_scales", b_scales))
+    _launch(load_library().moe_mxfp4_matmul,
+            (a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(), b_scales.data_ptr(), m, n, k, code,
+             out.data_ptr()), a_codes, stream, (a_codes, a_scales, b_codes, b_scales, out))
     return out
 
 
-def _grouped(w, offsets, device):
+def _grouped(w, offsets):
     import torch
     if not isinstance(w, torch.Tensor) or w.dim() != 3:
         raise _arg_error("w must be a 3-D torch.Tensor [num_groups, n, k]")
-    _need_shape(w, "w", torch.bfloat16, w.shape, device)
-    _need_shape(offsets, "offsets", torch.int32, (w.shape[0] + 1,), device)
+    _need_shape(w, "w", torch.bfloat16, w.shape, w)
+    _need_shape(offsets, "offsets", torch.int32, (w.shape[0] + 1,), w)
     return w.shape
 
 
@@ -519,17 +526,16 @@ def grouped_matmul(x, w, offsets, out=None, stream=None):
     bf16, offsets [num_groups + 1] int32 on the device, as Plan.route gives them.
     Rows outside every group are left as they were (undefined in a new `out`)."""
     import torch
-    groups, n, k = _grouped(w, offsets, w.device if isinstance(w, torch.Tensor) else None)
-    dev = w.device
-    ld = _rows(x, "x", (torch.bfloat16,), k, dev)
+    groups, n, k = _grouped(w, offsets)
+    ld = _rows(x, "x", (torch.bfloat16,), k, w)
     rows = x.shape[0]
     if out is None:
-        out = _new((rows, n), torch.bfloat16, dev, stream)
+        out = _new((rows, n), torch.bfloat16, x, stream)
     else:
-        _need_shape(out, "out", torch.bfloat16, (rows, n), dev)
+        _need_shape(out, "out", torch.bfloat16, (rows, n), w)
         _apart(out, "out", ("x", x), ("w", w), ("offsets", offsets))
-    _launch(dev, stream, lambda s: load_library().moe_grouped_matmul(
-        x.data_ptr(), ld, w.data_ptr(), offsets.data_ptr(), rows, groups, n, k, out.data_ptr(), s),
+    _launch(load_library().moe_grouped_matmul,
+            (x.data_ptr(), ld, w.data_ptr(), offsets.data_ptr(), rows, groups, n, k, out.data_ptr()), w, stream,
             (x, w, offsets, out))
     return out
 
@@ -542,48 +548,41 @@ def grouped_matmul_backward(dy, x, w, offsets, dx=None, dw=None, dw_dtype=None, 
     need_dx / need_dw False: that gradient is not computed and returned as None
     (x is not read without need_dw and may then be None)."""
     import torch
-    groups, n, k = _grouped(w, offsets, w.device if isinstance(w, torch.Tensor) else None)
-    dev = w.device
-    lddy = _rows(dy, "dy", (torch.bfloat16,), n, dev)
+    groups, n, k = _grouped(w, offsets)
+    lddy = _rows(dy, "dy", (torch.bfloat16,), n, w)
     rows = dy.shape[0]
     lib = load_library()
+    used = [dy, w, offsets]
     if need_dw:
-        ldx = _rows(x, "x", (torch.bfloat16,), k, dev)
+        ldx = _rows(x, "x", (torch.bfloat16,), k, w)
         if x.shape[0] != rows:
             raise _arg_error(f"x must have dy's {rows} rows, got shape {tuple(x.shape)}")
-        if dw is None:
-            dw_dtype = torch.float32 if dw_dtype is None else dw_dtype
-            code = _dtype_code(dw_dtype, "dw_dtype")
-            dw = _new((groups, n, k), dw_dtype, dev, stream)
-        else:
-            dw_dtype = getattr(dw, "dtype", None) if dw_dtype is None else dw_dtype
-            code = _dtype_code(dw_dtype, "dw")
-            _need_shape(dw, "dw", dw_dtype, (groups, n, k), dev)
-            _apart(dw, "dw", ("dy", dy), ("x", x), ("w", w), ("offsets", offsets))
+        if dw is None and dw_dtype is None:
+            dw_dtype = torch.float32
+        dw, code = _float_out(dw, "dw", (groups, n, k), dw_dtype, w, stream, ("dy", dy), ("x", x), ("w", w),
+                              ("offsets", offsets))
+        used += [x, dw]
     else:
         dw = None
     if need_dx:
         if dx is None:
-            dx = _new((rows, k), torch.bfloat16, dev, stream)
+            dx = _new((rows, k), torch.bfloat16, w, stream)
         else:
-            _need_shape(dx, "dx", torch.bfloat16, (rows, k), dev)
+            _need_shape(dx, "dx", torch.bfloat16, (rows, k), w)
             _apart(dx, "dx", ("dy", dy), ("w", w), ("offsets", offsets))
             if need_dw:
                 _apart(dx, "dx", ("x", x), ("dw", dw))
+        used.append(dx)
     else:
         dx = None
-
-    def call(s):
-        status = 0
-        if need_dx:
-            status = lib.moe_grouped_matmul_dx(dy.data_ptr(), lddy, w.data_ptr(), offsets.data_ptr(), rows, groups, n,
-                                               k, dx.data_ptr(), s)
-        if status == 0 and need_dw:
-            status = lib.moe_grouped_matmul_dw(dy.data_ptr(), lddy, x.data_ptr(), ldx, offsets.data_ptr(), rows,
-                                               groups, n, k, code, dw.data_ptr(), s)
-        return status
-
-    _launch(dev, stream, call, [t for t in (dy, x if need_dw else None, w, offsets, dx, dw) if t is not None])
+    if need_dx:
+        _launch(lib.moe_grouped_matmul_dx,
+                (dy.data_ptr(), lddy, w.data_ptr(), offsets.data_ptr(), rows, groups, n, k, dx.data_ptr()), w, stream,
+                used)
+    if need_dw:
+        _launch(lib.moe_grouped_matmul_dw,
+                (dy.data_ptr(), lddy, x.data_ptr(), ldx, offsets.data_ptr(), rows, groups, n, k, code, dw.data_ptr()),
+                w, stream, used)
     return dx, dw
 
 
