@@ -6,7 +6,7 @@
 //   dw         dw_e = sum over e's rows dy_r x_r^T  reduction over the rows
 // One tile kernel on v_mfma_f32_32x32x16_bf16 serves the three: an output tile
 // of BM x BN is the product of a row operand P (output rows) and a column
-// operand Q (output columns) over 64 of the reduction at a time.  An operand
+// operand Q (output columns).  An operand
 // lies in memory either along its reduction ("plain": x and w forward, dy for
 // dx) or across it ("crossed": w for dx; dy and x for dw); a crossed operand
 // is staged as it lies and read through ds_read_b64_tr_b16, which hands each
@@ -14,14 +14,14 @@
 // transposed in memory.
 //
 // Staging: buffer_load ... lds copies of 1 KB per wave instruction into a ring
-// of kSlots stages, loaded kSlots - 1 stages ahead.  Addresses past an edge
-// (rows past the group, reduction past its length, columns past the matrix)
-// get an out-of-range offset, for which the copy writes zeros: no other
-// group's row, NaN or not, enters a sum.
-//   plain tile: 128-byte rows of 64 reduction values whose eight 16-byte
-//     chunks are permuted by chunk ^ (row & 7) ^ ((row >> 3) & 1), which
-//     spreads a quarter-wave's ds_read_b128 over all 64 banks;
-//   crossed tile: 64 rows (the reduction) of BM or BN columns whose 64-byte
+// of four stages of 32 of the reduction, loaded three stages ahead.  Addresses
+// past an edge (rows past the group, reduction past its length, columns past
+// the matrix) get an out-of-range offset, for which the copy writes zeros: no
+// other group's row, NaN or not, enters a sum.
+//   plain tile: 64-byte rows of 32 reduction values whose four 16-byte chunks
+//     are permuted by chunk ^ ((row >> 2) & 3), which spreads a quarter-wave's
+//     ds_read_b128 over all 64 banks;
+//   crossed tile: 32 rows (the reduction) of BM or BN columns whose 64-byte
 //     units are permuted by unit ^ (row & 3): the four rows a transposed read
 //     takes lie in four different units, again all 64 banks.
 // Both operands number the reduction alike, so every output is one fp32 sum
@@ -30,6 +30,7 @@
 // Q is the instruction's first operand: a lane then ends with four
 // consecutive columns of one output row, stored together.
 #include <algorithm>
+#include <type_traits>
 
 #include "moe_internal.h"
 
@@ -42,14 +43,22 @@ typedef short s16x8_t __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void lds_void_t;
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 
-constexpr int kStep = 64;                      // reduction per stage
+constexpr int kStep = 32;                      // reduction per stage
+constexpr int kRing = 4;                       // stages in LDS
 constexpr uint32_t kPastEnd = 0x80000000u;     // beyond every buffer resource below
 constexpr int kMaxRange = 0x7FFFFFFF;          // bytes a resource covers
 
 // vmcnt <= n and lgkmcnt 0
 #define MOE_WAIT_VM(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (7 << 4) | ((((n) >> 4) & 3) << 14))
 
-__device__ __forceinline__ int swz(int c, int r) { return c ^ (r & 7) ^ ((r >> 3) & 1); }
+__device__ __forceinline__ int swz(int c, int r) { return c ^ ((r >> 2) & 3); }
+
+// Four reduction values of one column (see Operand::read).  The __restrict__
+// matters: without alias information on the read the compiler takes it to
+// depend on every LDS copy in flight and waits for all of them (vmcnt(0)).
+__device__ __forceinline__ s16x4_t read_crossed(const uint8_t* __restrict__ p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p));
+}
 
 // One operand's tile of B rows (plain) or columns (crossed), `count` of them
 // live, over `length` of the reduction; `base` is its first element and `ld`
@@ -75,7 +84,7 @@ struct Operand {
     for (int j = 0; j < kCopies; ++j) {
       const int i = wave + WAVES * j;
       if constexpr (!CROSSED) {
-        const int r = 8 * i + (lane >> 3), c = swz(lane & 7, r);
+        const int r = 16 * i + (lane >> 2), c = swz(lane & 3, r);
         red[j] = 8 * c;
         off[j] = r < count ? (uint32_t)((long long)r * ld * 2) + 16 * c : kPastEnd;
       } else {
@@ -87,15 +96,13 @@ struct Operand {
     }
   }
 
-  // copies of stage s into `buf`
-  __device__ __forceinline__ void issue(uint8_t* buf, int s) const {
+  // copy j of stage s into `buf`
+  __device__ __forceinline__ void issue(uint8_t* buf, int s, int j) const {
     const long long skip = (long long)s * kStep * (CROSSED ? ld : 1);
     const __amdgpu_buffer_rsrc_t r =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + skip), (short)0, kMaxRange, kRsrcWord3);
-#pragma unroll
-    for (int j = 0; j < kCopies; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)(buf + (wave + WAVES * j) * 1024), 16,
-                                               red[j] + s * kStep < length ? off[j] : kPastEnd, 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)(buf + (wave + WAVES * j) * 1024), 16,
+                                             red[j] + s * kStep < length ? off[j] : kPastEnd, 0, 0, 0);
   }
 
   // MFMA operand of 32-row block b, 16-deep step k, from a staged tile
@@ -103,70 +110,179 @@ struct Operand {
     const int h = lane >> 5;
     if constexpr (!CROSSED) {
       const int r = lane & 31;
-      return *reinterpret_cast<const bf16x8_t*>(buf + (b * 32 + r) * 128 + swz(2 * k + h, r) * 16);
+      return *reinterpret_cast<const bf16x8_t*>(buf + (b * 32 + r) * (2 * kStep) + swz(2 * k + h, r) * 16);
     } else {
       // lane i of 16 points at row i/4 and columns 4 (i%4).. of a 4 x 16 block
       const int i = lane & 15, g = (lane >> 4) & 1;
       const uint8_t* p = buf + (16 * k + 8 * h + (i >> 2)) * (B * 2) + ((b ^ (i >> 2)) * 4 + 2 * g + ((i >> 1) & 1)) * 16 +
                          (i & 1) * 8;
-      const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p));
-      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + 4 * (B * 2)));
+      const s16x4_t lo = read_crossed(p), hi = read_crossed(p + 4 * (B * 2));
       const s16x8_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
       return __builtin_bit_cast(bf16x8_t, v);
     }
   }
 };
 
-// The group and first row of row tile `tile` (tiles of BM rows, groups in
-// order), or e = -1 past the last one.  Offsets are clamped to [0, rows] and
-// to their predecessor, so no offset leads outside the tensors.  Every wave
-// finds it by itself: a lane counts the tiles of ceil(groups / 64) groups, a
-// wave scan gives each lane its first tile.
+// Row tiles (of bm rows, groups in order) and the place of one of them.
+// Offsets are clamped to [0, rows] and to their predecessor, so no offset
+// leads outside the tensors.  Every wave counts by itself: a lane takes
+// ceil(groups / 64) groups, a wave scan gives each lane its first tile.
 struct Tile { int e, row0, rows; };
-__device__ __forceinline__ Tile find_tile(const int32_t* offsets, int groups, int rows, int bm, int tile, int lane) {
-  const int per = (groups + kWave - 1) / kWave;
-  const int e0 = lane * per, e1 = min(e0 + per, groups);
-  int mine = 0;
-  for (int e = e0; e < e1; ++e) {
-    const int lo = min(max(offsets[e], 0), rows), hi = min(max(offsets[e + 1], lo), rows);
-    mine += (hi - lo + bm - 1) / bm;
+struct RowTiles {
+  const int32_t* offsets;
+  int rows, bm, e0, e1, first, mine, total;
+
+  __device__ __forceinline__ void range(int e, int& lo, int& hi) const {
+    lo = min(max(offsets[e], 0), rows);
+    hi = min(max(offsets[e + 1], lo), rows);
   }
-  int upto = mine;
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {
-    const int v = __shfl_up(upto, d, kWave);
-    if (lane >= d) upto += v;
-  }
-  Tile t = {-1, 0, 0};
-  int first = upto - mine;
-  if (tile >= first && tile < upto) {
+  __device__ __forceinline__ RowTiles(const int32_t* o, int groups, int r, int b, int lane) : offsets(o), rows(r), bm(b) {
+    const int per = (groups + kWave - 1) / kWave;
+    e0 = min(lane * per, groups);
+    e1 = min(e0 + per, groups);
+    mine = 0;
     for (int e = e0; e < e1; ++e) {
-      const int lo = min(max(offsets[e], 0), rows), hi = min(max(offsets[e + 1], lo), rows);
-      const int n = (hi - lo + bm - 1) / bm;
-      if (tile < first + n) {
-        t.e = e;
-        t.row0 = lo + (tile - first) * bm;
-        t.rows = min(bm, hi - t.row0);
-        break;
-      }
-      first += n;
+      int lo, hi;
+      range(e, lo, hi);
+      mine += (hi - lo + bm - 1) / bm;
     }
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+      const int v = __shfl_up(upto, d, kWave);
+      if (lane >= d) upto += v;
+    }
+    first = upto - mine;
+    total = __builtin_amdgcn_readlane(upto, kWave - 1);
   }
-  const uint64_t owner = __ballot(t.e >= 0);
-  if (owner == 0) return t;
-  const int src = __ffsll((unsigned long long)owner) - 1;
-  t.e = __builtin_amdgcn_readfirstlane(__shfl(t.e, src, kWave));
-  t.row0 = __builtin_amdgcn_readfirstlane(__shfl(t.row0, src, kWave));
-  t.rows = __builtin_amdgcn_readfirstlane(__shfl(t.rows, src, kWave));
-  return t;
+  // tile in [0, total)
+  __device__ __forceinline__ Tile place(int tile) const {
+    Tile t = {0, 0, 0};
+    const bool here = tile >= first && tile < first + mine;
+    if (here) {
+      int at = first;
+      for (int e = e0; e < e1; ++e) {
+        int lo, hi;
+        range(e, lo, hi);
+        const int n = (hi - lo + bm - 1) / bm;
+        if (tile < at + n) {
+          t.e = e;
+          t.row0 = lo + (tile - at) * bm;
+          t.rows = min(bm, hi - t.row0);
+          break;
+        }
+        at += n;
+      }
+    }
+    const int src = __ffsll((unsigned long long)__ballot(here)) - 1;
+    t.e = __builtin_amdgcn_readlane(t.e, src);
+    t.row0 = __builtin_amdgcn_readlane(t.row0, src);
+    t.rows = __builtin_amdgcn_readlane(t.rows, src);
+    return t;
+  }
+};
+
+// Workgroups go to the XCDs in turn: XCD x takes the x-th eighth of `total`
+// items in order, so that items which share operands share an L2.  -1: none.
+__device__ __forceinline__ int xcd_item(int total) {
+  const int chunk = (total + kXcds - 1) / kXcds, i = blockIdx.x / kXcds;
+  const int id = (int)(blockIdx.x % kXcds) * chunk + i;
+  return i < chunk && id < total ? id : -1;
 }
 
-template <int BM_, int BN_, int WM_, int WN_, int SLOTS_>
+// W waves as WM x WN.  A wave's 32-row blocks are every WM-th one, so that the
+// blocks past a tile's last row, which are skipped, are spread over the waves;
+// its 32-column blocks lie side by side.
+template <int BM_, int BN_, int WM_, int WN_, int PER_CU_>
 struct Shape {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, kSlots = SLOTS_;
-  static constexpr int kWaves = WM * WN;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int kWaves = WM * WN, kPerCU = PER_CU_;
   static constexpr int MI = BM / WM / 32, NJ = BN / WN / 32;
   static constexpr int kSlotBytes = (BM + BN) * kStep * 2;
+};
+
+// The K loop over a wave's first LIVE row blocks.
+template <class C, bool PX, bool QX, int LIVE>
+struct Reduce {
+  static __device__ __forceinline__ void run(uint8_t* smem, const Operand<PX, C::BM, C::kWaves>& op,
+                                             const Operand<QX, C::BN, C::kWaves>& oq, int stages, int wm, int wn,
+                                             int lane, f32x16_t (&acc)[C::MI][C::NJ]) {
+    using P = Operand<PX, C::BM, C::kWaves>;
+    using Q = Operand<QX, C::BN, C::kWaves>;
+    constexpr int D = kRing - 1, G = P::kCopies + Q::kCopies;
+    auto copy = [&](int slot, int s, auto c) {   // copy c of stage s
+      constexpr int i = decltype(c)::value;
+      uint8_t* const buf = smem + slot * C::kSlotBytes;
+      if constexpr (i < P::kCopies) op.issue(buf, s, i);
+      else oq.issue(buf + P::kBytes, s, i - P::kCopies);
+    };
+    unrolled<D>([&](auto d) { unrolled<G>([&](auto c) { copy(d, d, c); }); });
+
+    // Each stage has two 16-deep steps, each a list of LIVE x NJ MFMAs.  Behind
+    // each MFMA stands a share of the LDS reads of the step after it (and, in
+    // the second half of a stage, of the global copies): a run of reads would
+    // fill the LDS queue from eight waves at once and hold up the MFMAs behind
+    // it.  A stage's second list therefore runs after the next stage's
+    // barrier, over that stage's first reads.  Before the first stage its
+    // operands are zeros (0 * 0 leaves the accumulators at +0).
+    static_assert(kStep == 32, "two steps per stage");
+    constexpr int kM = LIVE * C::NJ, kR = LIVE + C::NJ;              // MFMAs and operands of a step
+    constexpr int kAhead = kM > 0 ? (4 * kR + 3 * kM - 1) / (3 * kM) : 0;   // operands read behind an MFMA: done by 3/4 of them
+    constexpr int kRows = LIVE ? LIVE : 1;
+    bf16x8_t p0[kRows], q0[C::NJ], p1[kRows] = {}, q1[C::NJ] = {};
+    auto stage = [&](auto slot_c, int s) {
+      constexpr int slot = decltype(slot_c)::value, next = (slot + D) % kRing;   // next: stage s - 1's slot
+      // this wave's copies of stage s have landed and its reads of stage s - 1
+      // are done; the barrier extends both to every wave
+      MOE_WAIT_VM((D - 1) * G);
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      const uint8_t* bp = smem + slot * C::kSlotBytes;
+      const uint8_t* bq = bp + P::kBytes;
+      auto read = [&](auto k, auto r, bf16x8_t (&fp)[kRows], bf16x8_t (&fq)[C::NJ]) {   // operand r of step k
+        constexpr int i = decltype(r)::value, step = decltype(k)::value;
+        if constexpr (i == 1) fp[0] = P::read(bp, wm, step, lane);
+        else if constexpr (i <= C::NJ) fq[i ? i - 1 : 0] = Q::read(bq, wn * C::NJ + (i ? i - 1 : 0), step, lane);
+        else fp[i - C::NJ] = P::read(bp, (i - C::NJ) * C::WM + wm, step, lane);
+      };
+      auto half = [&](auto k, bf16x8_t (&fp)[kRows], bf16x8_t (&fq)[C::NJ], bf16x8_t (&np)[kRows],
+                      bf16x8_t (&nq)[C::NJ]) {   // the MFMAs of fp, fq over the reads of np, nq (step k of this stage)
+        unrolled<kM>([&](auto mc) {
+          constexpr int m = decltype(mc)::value, i = m / C::NJ, j = m % C::NJ;
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fq[j], fp[i], acc[i][j], 0, 0, 0);
+          unrolled<kAhead>([&](auto r) {
+            if constexpr (m * kAhead + decltype(r)::value < kR)
+              read(k, std::integral_constant<int, m * kAhead + decltype(r)::value>{}, np, nq);
+          });
+          if constexpr (decltype(k)::value == 1)
+            unrolled<G>([&](auto c) {
+              if constexpr (decltype(c)::value * kM / G == m) copy(next, s + D, c);
+            });
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      };
+      half(std::integral_constant<int, 0>{}, p1, q1, p0, q0);
+      half(std::integral_constant<int, 1>{}, p0, q0, p1, q1);
+      if constexpr (LIVE == 0) unrolled<G>([&](auto c) { copy(next, s + D, c); });
+      unrolled<kM>([&](auto m) { pin(acc[decltype(m)::value / C::NJ][decltype(m)::value % C::NJ][0]); });
+    };
+    int s = 0;
+    for (; s + kRing <= stages; s += kRing) {
+      stage(std::integral_constant<int, 0>{}, s);
+      stage(std::integral_constant<int, 1>{}, s + 1);
+      stage(std::integral_constant<int, 2>{}, s + 2);
+      stage(std::integral_constant<int, 3>{}, s + 3);
+    }
+    if (s < stages) stage(std::integral_constant<int, 0>{}, s);
+    if (s + 1 < stages) stage(std::integral_constant<int, 1>{}, s + 1);
+    if (s + 2 < stages) stage(std::integral_constant<int, 2>{}, s + 2);
+    unrolled<kM>([&](auto mc) {
+      constexpr int m = decltype(mc)::value, i = m / C::NJ, j = m % C::NJ;
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q1[j], p1[i], acc[i][j], 0, 0, 0);
+    });
+    MOE_WAIT_VM(0);   // the copies past the end still write LDS
+  }
 };
 
 // One output tile: rows 0..rows-1, columns 0..cols-1 from `out` on.
@@ -180,7 +296,6 @@ __device__ __forceinline__ void tile_product(uint8_t* smem, const uint16_t* p, l
   const Q oq(q, ldq, cols, length, wave, lane);
   const int wm = wave / C::WN, wn = wave % C::WN;
   const int stages = (length + kStep - 1) / kStep;
-  constexpr int D = C::kSlots - 1, G = P::kCopies + Q::kCopies;
   f32x16_t acc[C::MI][C::NJ];
 #pragma unroll
   for (int i = 0; i < C::MI; ++i)
@@ -189,45 +304,19 @@ __device__ __forceinline__ void tile_product(uint8_t* smem, const uint16_t* p, l
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-#pragma unroll
-  for (int d = 0; d < D; ++d) {
-    op.issue(smem + d * C::kSlotBytes, d);
-    oq.issue(smem + d * C::kSlotBytes + P::kBytes, d);
-  }
-  int slot = 0;
-  for (int s = 0; s < stages; ++s) {
-    // this wave's copies of stage s have landed and its reads of stage s - 1
-    // are done; the barrier extends both to every wave
-    MOE_WAIT_VM((D - 1) * G);
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    const int next = slot == 0 ? C::kSlots - 1 : slot - 1;   // stage s - 1's slot
-    op.issue(smem + next * C::kSlotBytes, s + D);
-    oq.issue(smem + next * C::kSlotBytes + P::kBytes, s + D);
-    const uint8_t* bp = smem + slot * C::kSlotBytes;
-    const uint8_t* bq = bp + P::kBytes;
-#pragma unroll
-    for (int k = 0; k < kStep / 16; ++k) {
-      bf16x8_t fp[C::MI], fq[C::NJ];
-#pragma unroll
-      for (int i = 0; i < C::MI; ++i) fp[i] = P::read(bp, wm * C::MI + i, k, lane);
-#pragma unroll
-      for (int j = 0; j < C::NJ; ++j) fq[j] = Q::read(bq, wn * C::NJ + j, k, lane);
-#pragma unroll
-      for (int i = 0; i < C::MI; ++i)
-#pragma unroll
-        for (int j = 0; j < C::NJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fq[j], fp[i], acc[i][j], 0, 0, 0);
-    }
-    slot = slot + 1 == C::kSlots ? 0 : slot + 1;
-  }
-  MOE_WAIT_VM(0);   // the copies past the end still write LDS
+  static_assert(C::MI == 2 || C::MI == 4, "cases below");
+  const int blocks = (rows + 31) / 32, live = (blocks - wm + C::WM - 1) / C::WM;   // this wave's
+  if (live >= C::MI) Reduce<C, PX, QX, C::MI>::run(smem, op, oq, stages, wm, wn, lane, acc);
+  else if (C::MI > 3 && live == 3) Reduce<C, PX, QX, C::MI - 1>::run(smem, op, oq, stages, wm, wn, lane, acc);
+  else if (C::MI > 2 && live == 2) Reduce<C, PX, QX, 2>::run(smem, op, oq, stages, wm, wn, lane, acc);
+  else if (live == 1) Reduce<C, PX, QX, 1>::run(smem, op, oq, stages, wm, wn, lane, acc);
+  else Reduce<C, PX, QX, 0>::run(smem, op, oq, stages, wm, wn, lane, acc);
 
   // 32x32 D layout with Q first: lane holds output row l%32, columns 8(r/4) + 4(l/32) + r%4
   const int h = lane >> 5;
 #pragma unroll
   for (int i = 0; i < C::MI; ++i) {
-    const int row = (wm * C::MI + i) * 32 + (lane & 31);
+    const int row = (i * C::WM + wm) * 32 + (lane & 31);
     if (row >= rows) continue;
 #pragma unroll
     for (int j = 0; j < C::NJ; ++j)
@@ -250,14 +339,25 @@ __device__ __forceinline__ void tile_product(uint8_t* smem, const uint16_t* p, l
 
 // forward (QX false: w_e [cols, length]) and dx (QX true: w_e [length, cols]).
 template <class C, bool QX>
-__global__ __launch_bounds__(C::kWaves* kWave) void grouped_rows(const uint16_t* p, long long ldp, const uint16_t* w,
+__global__ __launch_bounds__(C::kWaves* kWave, C::kPerCU* C::kWaves / 4) void grouped_rows(const uint16_t* p, long long ldp, const uint16_t* w,
                                                                  const int32_t* offsets, int rows, int groups, int cols,
                                                                  int length, int slices, uint16_t* out) {
-  __shared__ __align__(1024) uint8_t smem[C::kSlots * C::kSlotBytes];
-  const int tile = blockIdx.x / slices, slice = blockIdx.x - tile * slices;
-  const Tile t = find_tile(offsets, groups, rows, C::BM, tile, threadIdx.x & 63);
-  if (t.e < 0) return;
-  const int c0 = slice * C::BN;
+  __shared__ __align__(1024) uint8_t smem[kRing * C::kSlotBytes];
+  const RowTiles tiles(offsets, groups, rows, C::BM, threadIdx.x & 63);
+#ifdef CHUNK
+  const int id = xcd_item(tiles.total * slices);
+  if (id < 0) return;
+  const int tile = id / slices;
+  const Tile t = tiles.place(tile);
+  const int c0 = (id - tile * slices) * C::BN;
+#else
+  // row tiles are dealt to the XCDs in turn, each with all its column slices
+  // one after another: the slices share their rows of x in one L2
+  const int turn = blockIdx.x / kXcds / slices, tile = turn * kXcds + blockIdx.x % kXcds;
+  if (tile >= tiles.total) return;
+  const Tile t = tiles.place(tile);
+  const int c0 = (int)(blockIdx.x / kXcds - turn * slices) * C::BN;
+#endif
   const uint16_t* we = w + (size_t)t.e * cols * length;
   tile_product<C, false, QX, false>(smem, p + (long long)t.row0 * ldp, ldp, QX ? we + c0 : we + (size_t)c0 * length,
                                     QX ? cols : length, t.rows, min(C::BN, cols - c0), length,
@@ -266,12 +366,18 @@ __global__ __launch_bounds__(C::kWaves* kWave) void grouped_rows(const uint16_t*
 
 // dw: [n, k] per group
 template <class C, bool F32>
-__global__ __launch_bounds__(C::kWaves* kWave) void grouped_dw(const uint16_t* dy, long long lddy, const uint16_t* x,
-                                                               long long ldx, const int32_t* offsets, int rows, int n,
-                                                               int k, int mtiles, int ntiles, void* out) {
-  __shared__ __align__(1024) uint8_t smem[C::kSlots * C::kSlotBytes];
-  const int per = mtiles * ntiles, e = blockIdx.x / per, i = blockIdx.x - e * per;
-  const int n0 = i / ntiles * C::BM, k0 = i % ntiles * C::BN;
+__global__ __launch_bounds__(C::kWaves* kWave, C::kPerCU* C::kWaves / 4) void grouped_dw(const uint16_t* dy, long long lddy, const uint16_t* x,
+                                                               long long ldx, const int32_t* offsets, int rows, int groups,
+                                                               int n, int k, int mtiles, int ntiles, void* out) {
+  __shared__ __align__(1024) uint8_t smem[kRing * C::kSlotBytes];
+  const int per = mtiles * ntiles, id = xcd_item(groups * per);
+  if (id < 0) return;
+  // a group's tiles in bands of eight tile rows: the concurrent ones share
+  // their columns of dy and x
+  const int e = id / per, i = id - e * per;
+  constexpr int kBand = 8;
+  const int band = i / (kBand * ntiles), in = i - band * kBand * ntiles, high = min(kBand, mtiles - band * kBand);
+  const int n0 = (band * kBand + in % high) * C::BM, k0 = in / high * C::BN;
   const int lo = min(max(offsets[e], 0), rows), hi = min(max(offsets[e + 1], lo), rows);
   const size_t at = ((size_t)e * n + n0) * k + k0;
   void* o = F32 ? static_cast<void*>(static_cast<float*>(out) + at) : static_cast<void*>(static_cast<uint16_t*>(out) + at);
@@ -279,15 +385,24 @@ __global__ __launch_bounds__(C::kWaves* kWave) void grouped_dw(const uint16_t* d
                                    min(C::BM, n - n0), min(C::BN, k - k0), hi - lo, o, k);
 }
 
-using Tile128 = Shape<128, 128, 2, 2, 3>;
+unsigned grid_of(long long items) { return (unsigned)((items + kXcds - 1) / kXcds * kXcds); }
+
+#ifndef ROWS_SHAPE
+#define ROWS_SHAPE 256, 256, 2, 4, 1
+#endif
+#ifndef DW_SHAPE
+#define DW_SHAPE 128, 128, 2, 2, 2
+#endif
+using RowsShape = Shape<ROWS_SHAPE>;
+using DwShape = Shape<DW_SHAPE>;
 
 template <bool QX>
 hipError_t launch_rows(const GroupedArgs& a, const void* p, int64_t ldp, int cols, int length, void* out,
                        hipStream_t stream) {
-  using C = Tile128;
+  using C = RowsShape;
   const int slices = (cols + C::BN - 1) / C::BN;
   const long long tiles = a.rows / C::BM + std::min(a.groups, a.rows);
-  hipLaunchKernelGGL((grouped_rows<C, QX>), dim3((unsigned)(tiles * slices)), dim3(C::kWaves * kWave), 0, stream,
+  hipLaunchKernelGGL((grouped_rows<C, QX>), dim3((unsigned)((tiles + kXcds - 1) / kXcds * kXcds * slices)), dim3(C::kWaves * kWave), 0, stream,
                      static_cast<const uint16_t*>(p), ldp, static_cast<const uint16_t*>(a.w), a.offsets, a.rows, a.groups,
                      cols, length, slices, static_cast<uint16_t*>(out));
   return hipGetLastError();
@@ -305,15 +420,15 @@ hipError_t launch_grouped_dx(const GroupedArgs& a, const void* dy, int64_t lddy,
 
 hipError_t launch_grouped_dw(const GroupedArgs& a, const void* dy, int64_t lddy, const void* x, int64_t ldx, bool f32,
                              void* dw, hipStream_t stream) {
-  using C = Tile128;
+  using C = DwShape;
   const int mt = (a.n + C::BM - 1) / C::BM, nt = (a.k + C::BN - 1) / C::BN;
-  const dim3 grid((unsigned)((long long)a.groups * mt * nt)), block(C::kWaves * kWave);
+  const dim3 grid(grid_of((long long)a.groups * mt * nt)), block(C::kWaves * kWave);
   if (f32)
     hipLaunchKernelGGL((grouped_dw<C, true>), grid, block, 0, stream, static_cast<const uint16_t*>(dy), lddy,
-                       static_cast<const uint16_t*>(x), ldx, a.offsets, a.rows, a.n, a.k, mt, nt, dw);
+                       static_cast<const uint16_t*>(x), ldx, a.offsets, a.rows, a.groups, a.n, a.k, mt, nt, dw);
   else
     hipLaunchKernelGGL((grouped_dw<C, false>), grid, block, 0, stream, static_cast<const uint16_t*>(dy), lddy,
-                       static_cast<const uint16_t*>(x), ldx, a.offsets, a.rows, a.n, a.k, mt, nt, dw);
+                       static_cast<const uint16_t*>(x), ldx, a.offsets, a.rows, a.groups, a.n, a.k, mt, nt, dw);
   return hipGetLastError();
 }
 

@@ -21,6 +21,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace moe {
 
 constexpr int kWave = 64;
@@ -208,6 +210,20 @@ typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
+
+// Keeps the instruction that makes v above this point: without it the
+// compiler moves MFMAs past a later barrier, collecting several stages'
+// operands in registers.
+__device__ __forceinline__ void pin(float v) { asm volatile("" ::"v"(v)); }
+
+// f(integral_constant 0) .. f(integral_constant N - 1)
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void unrolled(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    unrolled<N, I + 1>(f);
+  }
+}
 
 // E8M0 byte -> fp32 power of two (exact for bytes 1..254).
 __device__ __forceinline__ float e8m0_to_f32(uint32_t b) { return __uint_as_float(b << 23); }

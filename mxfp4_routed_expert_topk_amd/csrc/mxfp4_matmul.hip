@@ -245,7 +245,7 @@ __device__ __forceinline__ void matmul_tile(uint8_t* smem, const uint8_t* ac, co
 #pragma unroll
     for (int i = 0; i < C::MI; ++i)
 #pragma unroll
-      for (int j = 0; j < C::NJ; ++j) asm volatile("" ::"v"(acc[i][j]));
+      for (int j = 0; j < C::NJ; ++j) pin(acc[i][j][0]);
   };
   for (int g = 0; g < full; ++g) {
     run_stage(std::integral_constant<int, 0>{}, g);
