@@ -13,15 +13,19 @@
 // lane one column's four consecutive reduction values, so nothing is
 // transposed in memory.
 //
-// Staging: buffer_load ... lds copies of 1 KB per wave instruction into a ring
-// of four stages of 32 of the reduction, loaded three stages ahead.  Addresses
-// past an edge (rows past the group, reduction past its length, columns past
-// the matrix) get an out-of-range offset, for which the copy writes zeros: no
+// Staging: buffer_load ... lds copies of 1 KB per wave instruction, 64 of the
+// reduction at a time, into a ring of five operand tiles (all 160 KB of LDS at
+// 256 x 256): while a stage multiplies its Q and P, the next stage's Q and P
+// and the Q after that are on their way.  Q is the operand that comes from
+// HBM (the weights), P the rows that a tile's column slices share in L2; with
+// both one stage ahead, the weights' latency held the loop up.  Addresses past
+// an edge (rows past the group, reduction past its length, columns past the
+// matrix) get an out-of-range offset, for which the copy writes zeros: no
 // other group's row, NaN or not, enters a sum.
-//   plain tile: 64-byte rows of 32 reduction values whose four 16-byte chunks
-//     are permuted by chunk ^ ((row >> 2) & 3), which spreads a quarter-wave's
-//     ds_read_b128 over all 64 banks;
-//   crossed tile: 32 rows (the reduction) of BM or BN columns whose 64-byte
+//   plain tile: 128-byte rows of 64 reduction values (whole cache lines) whose
+//     eight 16-byte chunks are permuted by chunk ^ (row & 7) ^ ((row >> 3) & 1),
+//     which spreads a quarter-wave's ds_read_b128 over all 64 banks;
+//   crossed tile: 64 rows (the reduction) of BM or BN columns whose 64-byte
 //     units are permuted by unit ^ (row & 3): the four rows a transposed read
 //     takes lie in four different units, again all 64 banks.
 // Both operands number the reduction alike, so every output is one fp32 sum
@@ -43,15 +47,15 @@ typedef short s16x8_t __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void lds_void_t;
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 
-constexpr int kStep = 32;                      // reduction per stage
-constexpr int kRing = 4;                       // stages in LDS
+constexpr int kStep = 64;                      // reduction per stage
+constexpr int kRing = 5;                       // operand tiles in LDS
 constexpr uint32_t kPastEnd = 0x80000000u;     // beyond every buffer resource below
 constexpr int kMaxRange = 0x7FFFFFFF;          // bytes a resource covers
 
 // vmcnt <= n and lgkmcnt 0
 #define MOE_WAIT_VM(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (7 << 4) | ((((n) >> 4) & 3) << 14))
 
-__device__ __forceinline__ int swz(int c, int r) { return c ^ ((r >> 2) & 3); }
+__device__ __forceinline__ int swz(int c, int r) { return c ^ (r & 7) ^ ((r >> 3) & 1); }
 
 // Four reduction values of one column (see Operand::read).  The __restrict__
 // matters: without alias information on the read the compiler takes it to
@@ -84,7 +88,7 @@ struct Operand {
     for (int j = 0; j < kCopies; ++j) {
       const int i = wave + WAVES * j;
       if constexpr (!CROSSED) {
-        const int r = 16 * i + (lane >> 2), c = swz(lane & 3, r);
+        const int r = 8 * i + (lane >> 3), c = swz(lane & 7, r);
         red[j] = 8 * c;
         off[j] = r < count ? (uint32_t)((long long)r * ld * 2) + 16 * c : kPastEnd;
       } else {
@@ -198,7 +202,7 @@ struct Shape {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
   static constexpr int kWaves = WM * WN, kPerCU = PER_CU_;
   static constexpr int MI = BM / WM / 32, NJ = BN / WN / 32;
-  static constexpr int kSlotBytes = (BM + BN) * kStep * 2;
+  static constexpr int kSlotBytes = (BM > BN ? BM : BN) * kStep * 2;   // one operand tile
 };
 
 // The K loop over a wave's first LIVE row blocks.
@@ -209,77 +213,74 @@ struct Reduce {
                                              int lane, f32x16_t (&acc)[C::MI][C::NJ]) {
     using P = Operand<PX, C::BM, C::kWaves>;
     using Q = Operand<QX, C::BN, C::kWaves>;
-    constexpr int D = kRing - 1, G = P::kCopies + Q::kCopies;
-    auto copy = [&](int slot, int s, auto c) {   // copy c of stage s
-      constexpr int i = decltype(c)::value;
-      uint8_t* const buf = smem + slot * C::kSlotBytes;
-      if constexpr (i < P::kCopies) op.issue(buf, s, i);
-      else oq.issue(buf + P::kBytes, s, i - P::kCopies);
-    };
-    unrolled<D>([&](auto d) { unrolled<G>([&](auto c) { copy(d, d, c); }); });
+    // tile 2s of the ring is stage s's Q, tile 2s + 1 its P
+    auto copy_q = [&](int slot, int s, int c) { oq.issue(smem + slot * C::kSlotBytes, s, c); };
+    auto copy_p = [&](int slot, int s, int c) { op.issue(smem + slot * C::kSlotBytes, s, c); };
+    unrolled<Q::kCopies>([&](auto c) { copy_q(0, 0, c); });
+    unrolled<P::kCopies>([&](auto c) { copy_p(1, 0, c); });
+    unrolled<Q::kCopies>([&](auto c) { copy_q(2, 1, c); });
 
-    // Each stage has two 16-deep steps, each a list of LIVE x NJ MFMAs.  Behind
-    // each MFMA stands a share of the LDS reads of the step after it (and, in
-    // the second half of a stage, of the global copies): a run of reads would
-    // fill the LDS queue from eight waves at once and hold up the MFMAs behind
-    // it.  A stage's second list therefore runs after the next stage's
-    // barrier, over that stage's first reads.  Before the first stage its
-    // operands are zeros (0 * 0 leaves the accumulators at +0).
-    static_assert(kStep == 32, "two steps per stage");
-    constexpr int kM = LIVE * C::NJ, kR = LIVE + C::NJ;              // MFMAs and operands of a step
+    // A stage has four 16-deep steps, each a list of LIVE x NJ MFMAs.  Behind
+    // each MFMA stands a share of the LDS reads of the step after it and of
+    // the global copies: a run of reads would fill the LDS queue from eight
+    // waves at once and hold up the MFMAs behind it.  A stage's last list
+    // therefore runs after the next stage's barrier, over that stage's first
+    // reads.  Before the first stage its operands are zeros (0 * 0 leaves the
+    // accumulators at +0).
+    constexpr int kSteps = kStep / 16;
+    constexpr int kM = LIVE * C::NJ, kR = LIVE + C::NJ;   // MFMAs and operands of a step
     constexpr int kAhead = kM > 0 ? (4 * kR + 3 * kM - 1) / (3 * kM) : 0;   // operands read behind an MFMA: done by 3/4 of them
+    constexpr int kG = P::kCopies + Q::kCopies;
     constexpr int kRows = LIVE ? LIVE : 1;
-    bf16x8_t p0[kRows], q0[C::NJ], p1[kRows] = {}, q1[C::NJ] = {};
-    auto stage = [&](auto slot_c, int s) {
-      constexpr int slot = decltype(slot_c)::value, next = (slot + D) % kRing;   // next: stage s - 1's slot
-      // this wave's copies of stage s have landed and its reads of stage s - 1
-      // are done; the barrier extends both to every wave
-      MOE_WAIT_VM((D - 1) * G);
+    bf16x8_t fp[2][kRows], fq[2][C::NJ];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) fp[1][i] = bf16x8_t{};
+#pragma unroll
+    for (int j = 0; j < C::NJ; ++j) fq[1][j] = bf16x8_t{};
+    int at = 0;   // ring slot of stage s's Q
+    for (int s = 0; s < stages; ++s) {
+      // this wave's copies of stage s have landed (the Q after them may be in
+      // flight) and its reads of stage s - 1 are done; the barrier extends
+      // both to every wave
+      MOE_WAIT_VM(Q::kCopies);
       asm volatile("" ::: "memory");
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
-      const uint8_t* bp = smem + slot * C::kSlotBytes;
-      const uint8_t* bq = bp + P::kBytes;
-      auto read = [&](auto k, auto r, bf16x8_t (&fp)[kRows], bf16x8_t (&fq)[C::NJ]) {   // operand r of step k
-        constexpr int i = decltype(r)::value, step = decltype(k)::value;
-        if constexpr (i == 1) fp[0] = P::read(bp, wm, step, lane);
-        else if constexpr (i <= C::NJ) fq[i ? i - 1 : 0] = Q::read(bq, wn * C::NJ + (i ? i - 1 : 0), step, lane);
-        else fp[i - C::NJ] = P::read(bp, (i - C::NJ) * C::WM + wm, step, lane);
+      const int at_p = at + 1 >= kRing ? at + 1 - kRing : at + 1;
+      // the two slots of stage s - 1: P of stage s + 1, then Q of stage s + 2
+      const int to_p = at + 3 >= kRing ? at + 3 - kRing : at + 3, to_q = at + 4 >= kRing ? at + 4 - kRing : at + 4;
+      const uint8_t* bq = smem + at * C::kSlotBytes;
+      const uint8_t* bp = smem + at_p * C::kSlotBytes;
+      auto copy = [&](auto c) {
+        constexpr int i = decltype(c)::value;
+        if constexpr (i < P::kCopies) copy_p(to_p, s + 1, i);
+        else copy_q(to_q, s + 2, i - P::kCopies);
       };
-      auto half = [&](auto k, bf16x8_t (&fp)[kRows], bf16x8_t (&fq)[C::NJ], bf16x8_t (&np)[kRows],
-                      bf16x8_t (&nq)[C::NJ]) {   // the MFMAs of fp, fq over the reads of np, nq (step k of this stage)
+      unrolled<kSteps>([&](auto kc) {
+        // the MFMAs of the step before (the last one of stage s - 1 first) over the reads of step k
+        constexpr int k = decltype(kc)::value, now = (k + 1) % 2, then = k % 2;
         unrolled<kM>([&](auto mc) {
           constexpr int m = decltype(mc)::value, i = m / C::NJ, j = m % C::NJ;
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fq[j], fp[i], acc[i][j], 0, 0, 0);
-          unrolled<kAhead>([&](auto r) {
-            if constexpr (m * kAhead + decltype(r)::value < kR)
-              read(k, std::integral_constant<int, m * kAhead + decltype(r)::value>{}, np, nq);
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fq[now][j], fp[now][i], acc[i][j], 0, 0, 0);
+          unrolled<kAhead>([&](auto rc) {   // q0, p0, the other q's, the other p's
+            constexpr int r = m * kAhead + decltype(rc)::value;
+            if constexpr (r == 1) fp[then][0] = P::read(bp, wm, k, lane);
+            else if constexpr (r <= C::NJ) fq[then][r ? r - 1 : 0] = Q::read(bq, wn * C::NJ + (r ? r - 1 : 0), k, lane);
+            else if constexpr (r < kR) fp[then][r - C::NJ] = P::read(bp, (r - C::NJ) * C::WM + wm, k, lane);
           });
-          if constexpr (decltype(k)::value == 1)
-            unrolled<G>([&](auto c) {
-              if constexpr (decltype(c)::value * kM / G == m) copy(next, s + D, c);
-            });
+          unrolled<kG>([&](auto c) {   // over the stage's first half: P is needed one stage on
+            if constexpr (decltype(c)::value * (kSteps / 2) * kM / kG == k * kM + m) copy(c);
+          });
           __builtin_amdgcn_sched_barrier(0);
         });
-      };
-      half(std::integral_constant<int, 0>{}, p1, q1, p0, q0);
-      half(std::integral_constant<int, 1>{}, p0, q0, p1, q1);
-      if constexpr (LIVE == 0) unrolled<G>([&](auto c) { copy(next, s + D, c); });
+      });
+      if constexpr (LIVE == 0) unrolled<kG>([&](auto c) { copy(c); });
       unrolled<kM>([&](auto m) { pin(acc[decltype(m)::value / C::NJ][decltype(m)::value % C::NJ][0]); });
-    };
-    int s = 0;
-    for (; s + kRing <= stages; s += kRing) {
-      stage(std::integral_constant<int, 0>{}, s);
-      stage(std::integral_constant<int, 1>{}, s + 1);
-      stage(std::integral_constant<int, 2>{}, s + 2);
-      stage(std::integral_constant<int, 3>{}, s + 3);
+      at = at + 2 >= kRing ? at + 2 - kRing : at + 2;
     }
-    if (s < stages) stage(std::integral_constant<int, 0>{}, s);
-    if (s + 1 < stages) stage(std::integral_constant<int, 1>{}, s + 1);
-    if (s + 2 < stages) stage(std::integral_constant<int, 2>{}, s + 2);
     unrolled<kM>([&](auto mc) {
       constexpr int m = decltype(mc)::value, i = m / C::NJ, j = m % C::NJ;
-      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q1[j], p1[i], acc[i][j], 0, 0, 0);
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fq[1][j], fp[1][i], acc[i][j], 0, 0, 0);
     });
     MOE_WAIT_VM(0);   // the copies past the end still write LDS
   }
@@ -344,20 +345,12 @@ __global__ __launch_bounds__(C::kWaves* kWave, C::kPerCU* C::kWaves / 4) void gr
                                                                  int length, int slices, uint16_t* out) {
   __shared__ __align__(1024) uint8_t smem[kRing * C::kSlotBytes];
   const RowTiles tiles(offsets, groups, rows, C::BM, threadIdx.x & 63);
-#ifdef CHUNK
-  const int id = xcd_item(tiles.total * slices);
-  if (id < 0) return;
-  const int tile = id / slices;
-  const Tile t = tiles.place(tile);
-  const int c0 = (id - tile * slices) * C::BN;
-#else
   // row tiles are dealt to the XCDs in turn, each with all its column slices
   // one after another: the slices share their rows of x in one L2
   const int turn = blockIdx.x / kXcds / slices, tile = turn * kXcds + blockIdx.x % kXcds;
   if (tile >= tiles.total) return;
   const Tile t = tiles.place(tile);
   const int c0 = (int)(blockIdx.x / kXcds - turn * slices) * C::BN;
-#endif
   const uint16_t* we = w + (size_t)t.e * cols * length;
   tile_product<C, false, QX, false>(smem, p + (long long)t.row0 * ldp, ldp, QX ? we + c0 : we + (size_t)c0 * length,
                                     QX ? cols : length, t.rows, min(C::BN, cols - c0), length,
@@ -391,7 +384,7 @@ unsigned grid_of(long long items) { return (unsigned)((items + kXcds - 1) / kXcd
 #define ROWS_SHAPE 256, 256, 2, 4, 1
 #endif
 #ifndef DW_SHAPE
-#define DW_SHAPE 128, 128, 2, 2, 2
+#define DW_SHAPE 256, 256, 2, 4, 1
 #endif
 using RowsShape = Shape<ROWS_SHAPE>;
 using DwShape = Shape<DW_SHAPE>;
