@@ -13,19 +13,17 @@
 // lane one column's four consecutive reduction values, so nothing is
 // transposed in memory.
 //
-// Staging: buffer_load ... lds copies of 1 KB per wave instruction, 64 of the
-// reduction at a time, into a ring of five operand tiles (all 160 KB of LDS at
-// 256 x 256): while a stage multiplies its Q and P, the next stage's Q and P
-// and the Q after that are on their way.  Q is the operand that comes from
-// HBM (the weights), P the rows that a tile's column slices share in L2; with
-// both one stage ahead, the weights' latency held the loop up.  Addresses past
-// an edge (rows past the group, reduction past its length, columns past the
-// matrix) get an out-of-range offset, for which the copy writes zeros: no
-// other group's row, NaN or not, enters a sum.
-//   plain tile: 128-byte rows of 64 reduction values (whole cache lines) whose
-//     eight 16-byte chunks are permuted by chunk ^ (row & 7) ^ ((row >> 3) & 1),
-//     which spreads a quarter-wave's ds_read_b128 over all 64 banks;
-//   crossed tile: 64 rows (the reduction) of BM or BN columns whose 64-byte
+// Staging: buffer_load ... lds copies of 1 KB per wave instruction, STEP of the
+// reduction at a time, into one ring of tiles for Q and one for P.  Q is the
+// operand that comes from HBM (the weights) and has the longer ring, P the rows
+// that a tile's column slices share in L2.  Addresses past an edge (rows past
+// the group, reduction past its length, columns past the matrix) get an
+// out-of-range offset, for which the copy writes zeros: no other group's row,
+// NaN or not, enters a sum.
+//   plain tile: rows of STEP reduction values (128 bytes or 64) whose 16-byte
+//     chunks are permuted by swz below, which spreads a quarter-wave's
+//     ds_read_b128 over all 64 banks;
+//   crossed tile: STEP rows (the reduction) of BM or BN columns whose 64-byte
 //     units are permuted by unit ^ (row & 3): the four rows a transposed read
 //     takes lie in four different units, again all 64 banks.
 // Both operands number the reduction alike, so every output is one fp32 sum
@@ -42,20 +40,24 @@ namespace moe {
 namespace {
 
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x8_t __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void lds_void_t;
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 
-constexpr int kStep = 64;                      // reduction per stage
-constexpr int kRing = 5;                       // operand tiles in LDS
 constexpr uint32_t kPastEnd = 0x80000000u;     // beyond every buffer resource below
+constexpr size_t kL2Bytes = 32u << 20;         // eight of 4 MB
 constexpr int kMaxRange = 0x7FFFFFFF;          // bytes a resource covers
 
 // vmcnt <= n and lgkmcnt 0
 #define MOE_WAIT_VM(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (7 << 4) | ((((n) >> 4) & 3) << 14))
 
-__device__ __forceinline__ int swz(int c, int r) { return c ^ (r & 7) ^ ((r >> 3) & 1); }
+// LDS place of 16-byte chunk c in a plain tile's row r of STEP values.
+template <int STEP>
+__device__ __forceinline__ int swz(int c, int r) {
+  return STEP == 64 ? c ^ (r & 7) ^ ((r >> 3) & 1) : c ^ ((r >> 2) & 3);
+}
 
 // Four reduction values of one column (see Operand::read).  The __restrict__
 // matters: without alias information on the read the compiler takes it to
@@ -67,9 +69,9 @@ __device__ __forceinline__ s16x4_t read_crossed(const uint8_t* __restrict__ p) {
 // One operand's tile of B rows (plain) or columns (crossed), `count` of them
 // live, over `length` of the reduction; `base` is its first element and `ld`
 // the elements from one memory row to the next.
-template <bool CROSSED, int B, int WAVES>
+template <bool CROSSED, int B, int WAVES, int STEP>
 struct Operand {
-  static constexpr int kBytes = B * kStep * 2;
+  static constexpr int kBytes = B * STEP * 2;
   static constexpr int kCopies = kBytes / 1024 / WAVES;   // copies per wave and stage
   static constexpr int kChunks = B / 8;                   // crossed: 16-byte chunks per staged row
   static_assert(!CROSSED || B >= 128, "four 64-byte units to permute");
@@ -88,7 +90,8 @@ struct Operand {
     for (int j = 0; j < kCopies; ++j) {
       const int i = wave + WAVES * j;
       if constexpr (!CROSSED) {
-        const int r = 8 * i + (lane >> 3), c = swz(lane & 7, r);
+        constexpr int kPerRow = STEP / 8;     // chunks
+        const int r = 64 / kPerRow * i + lane / kPerRow, c = swz<STEP>(lane % kPerRow, r);
         red[j] = 8 * c;
         off[j] = r < count ? (uint32_t)((long long)r * ld * 2) + 16 * c : kPastEnd;
       } else {
@@ -102,11 +105,11 @@ struct Operand {
 
   // copy j of stage s into `buf`
   __device__ __forceinline__ void issue(uint8_t* buf, int s, int j) const {
-    const long long skip = (long long)s * kStep * (CROSSED ? ld : 1);
+    const long long skip = (long long)s * STEP * (CROSSED ? ld : 1);
     const __amdgpu_buffer_rsrc_t r =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + skip), (short)0, kMaxRange, kRsrcWord3);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)(buf + (wave + WAVES * j) * 1024), 16,
-                                             red[j] + s * kStep < length ? off[j] : kPastEnd, 0, 0, 0);
+                                             red[j] + s * STEP < length ? off[j] : kPastEnd, 0, 0, 0);
   }
 
   // MFMA operand of 32-row block b, 16-deep step k, from a staged tile
@@ -114,7 +117,7 @@ struct Operand {
     const int h = lane >> 5;
     if constexpr (!CROSSED) {
       const int r = lane & 31;
-      return *reinterpret_cast<const bf16x8_t*>(buf + (b * 32 + r) * (2 * kStep) + swz(2 * k + h, r) * 16);
+      return *reinterpret_cast<const bf16x8_t*>(buf + (b * 32 + r) * (2 * STEP) + swz<STEP>(2 * k + h, r) * 16);
     } else {
       // lane i of 16 points at row i/4 and columns 4 (i%4).. of a 4 x 16 block
       const int i = lane & 15, g = (lane >> 4) & 1;
@@ -197,64 +200,69 @@ __device__ __forceinline__ int xcd_item(int total) {
 // W waves as WM x WN.  A wave's 32-row blocks are every WM-th one, so that the
 // blocks past a tile's last row, which are skipped, are spread over the waves;
 // its 32-column blocks lie side by side.
-template <int BM_, int BN_, int WM_, int WN_, int PER_CU_>
+// NP and NQ tiles of the rings; PER_CU workgroups fit a CU.
+template <int BM_, int BN_, int WM_, int WN_, int STEP_, int NP_, int NQ_, int PER_CU_>
 struct Shape {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STEP = STEP_, NP = NP_, NQ = NQ_;
   static constexpr int kWaves = WM * WN, kPerCU = PER_CU_;
   static constexpr int MI = BM / WM / 32, NJ = BN / WN / 32;
-  static constexpr int kSlotBytes = (BM > BN ? BM : BN) * kStep * 2;   // one operand tile
+  static constexpr int kSmem = 2 * STEP * (BM * NP + BN * NQ);
+  static_assert(NQ >= NP && NP >= 2 && kPerCU * kSmem <= 160 * 1024, "rings fit");
 };
 
 // The K loop over a wave's first LIVE row blocks.
 template <class C, bool PX, bool QX, int LIVE>
 struct Reduce {
-  static __device__ __forceinline__ void run(uint8_t* smem, const Operand<PX, C::BM, C::kWaves>& op,
-                                             const Operand<QX, C::BN, C::kWaves>& oq, int stages, int wm, int wn,
+  static __device__ __forceinline__ void run(uint8_t* smem, const Operand<PX, C::BM, C::kWaves, C::STEP>& op,
+                                             const Operand<QX, C::BN, C::kWaves, C::STEP>& oq, int stages, int wm, int wn,
                                              int lane, f32x16_t (&acc)[C::MI][C::NJ]) {
-    using P = Operand<PX, C::BM, C::kWaves>;
-    using Q = Operand<QX, C::BN, C::kWaves>;
-    // tile 2s of the ring is stage s's Q, tile 2s + 1 its P
-    auto copy_q = [&](int slot, int s, int c) { oq.issue(smem + slot * C::kSlotBytes, s, c); };
-    auto copy_p = [&](int slot, int s, int c) { op.issue(smem + slot * C::kSlotBytes, s, c); };
-    unrolled<Q::kCopies>([&](auto c) { copy_q(0, 0, c); });
-    unrolled<P::kCopies>([&](auto c) { copy_p(1, 0, c); });
-    unrolled<Q::kCopies>([&](auto c) { copy_q(2, 1, c); });
+    using P = Operand<PX, C::BM, C::kWaves, C::STEP>;
+    using Q = Operand<QX, C::BN, C::kWaves, C::STEP>;
+    constexpr int kG = P::kCopies + Q::kCopies;
+    // Stage s issues P of stage s + NP - 1 and Q of stage s + NQ - 1 into the
+    // tiles that stage s - 1 has read; the stages before 0 fill the rings.
+    uint8_t* const ring_q = smem;
+    uint8_t* const ring_p = smem + C::NQ * Q::kBytes;
+    unrolled<C::NQ - 1>([&](auto d) {
+      constexpr int v = decltype(d)::value, sp = v - (C::NQ - C::NP);
+      if constexpr (sp >= 0) unrolled<P::kCopies>([&](auto c) { op.issue(ring_p + sp * P::kBytes, sp, c); });
+      unrolled<Q::kCopies>([&](auto c) { oq.issue(ring_q + v * Q::kBytes, v, c); });
+    });
 
-    // A stage has four 16-deep steps, each a list of LIVE x NJ MFMAs.  Behind
+    // A stage has STEP / 16 steps, each a list of LIVE x NJ MFMAs.  Behind
     // each MFMA stands a share of the LDS reads of the step after it and of
     // the global copies: a run of reads would fill the LDS queue from eight
     // waves at once and hold up the MFMAs behind it.  A stage's last list
     // therefore runs after the next stage's barrier, over that stage's first
     // reads.  Before the first stage its operands are zeros (0 * 0 leaves the
     // accumulators at +0).
-    constexpr int kSteps = kStep / 16;
+    constexpr int kSteps = C::STEP / 16;
+    static_assert(kSteps % 2 == 0, "two operand sets in turn");
     constexpr int kM = LIVE * C::NJ, kR = LIVE + C::NJ;   // MFMAs and operands of a step
     constexpr int kAhead = kM > 0 ? (4 * kR + 3 * kM - 1) / (3 * kM) : 0;   // operands read behind an MFMA: done by 3/4 of them
-    constexpr int kG = P::kCopies + Q::kCopies;
     constexpr int kRows = LIVE ? LIVE : 1;
     bf16x8_t fp[2][kRows], fq[2][C::NJ];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) fp[1][i] = bf16x8_t{};
 #pragma unroll
     for (int j = 0; j < C::NJ; ++j) fq[1][j] = bf16x8_t{};
-    int at = 0;   // ring slot of stage s's Q
+    int iq = 0, ip = 0;   // stage s's tiles
     for (int s = 0; s < stages; ++s) {
-      // this wave's copies of stage s have landed (the Q after them may be in
-      // flight) and its reads of stage s - 1 are done; the barrier extends
-      // both to every wave
-      MOE_WAIT_VM(Q::kCopies);
+      // this wave's copies of stage s have landed (what was issued after them
+      // may be in flight) and its reads of stage s - 1 are done; the barrier
+      // extends both to every wave
+      MOE_WAIT_VM((C::NP - 2) * kG + (C::NQ > C::NP ? Q::kCopies : 0));
       asm volatile("" ::: "memory");
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
-      const int at_p = at + 1 >= kRing ? at + 1 - kRing : at + 1;
-      // the two slots of stage s - 1: P of stage s + 1, then Q of stage s + 2
-      const int to_p = at + 3 >= kRing ? at + 3 - kRing : at + 3, to_q = at + 4 >= kRing ? at + 4 - kRing : at + 4;
-      const uint8_t* bq = smem + at * C::kSlotBytes;
-      const uint8_t* bp = smem + at_p * C::kSlotBytes;
+      const uint8_t* bq = ring_q + iq * Q::kBytes;
+      const uint8_t* bp = ring_p + ip * P::kBytes;
+      uint8_t* const to_q = ring_q + (iq ? iq - 1 : C::NQ - 1) * Q::kBytes;
+      uint8_t* const to_p = ring_p + (ip ? ip - 1 : C::NP - 1) * P::kBytes;
       auto copy = [&](auto c) {
         constexpr int i = decltype(c)::value;
-        if constexpr (i < P::kCopies) copy_p(to_p, s + 1, i);
-        else copy_q(to_q, s + 2, i - P::kCopies);
+        if constexpr (i < P::kCopies) op.issue(to_p, s + C::NP - 1, i);
+        else oq.issue(to_q, s + C::NQ - 1, i - P::kCopies);
       };
       unrolled<kSteps>([&](auto kc) {
         // the MFMAs of the step before (the last one of stage s - 1 first) over the reads of step k
@@ -276,7 +284,8 @@ struct Reduce {
       });
       if constexpr (LIVE == 0) unrolled<kG>([&](auto c) { copy(c); });
       unrolled<kM>([&](auto m) { pin(acc[decltype(m)::value / C::NJ][decltype(m)::value % C::NJ][0]); });
-      at = at + 2 >= kRing ? at + 2 - kRing : at + 2;
+      iq = iq + 1 == C::NQ ? 0 : iq + 1;
+      ip = ip + 1 == C::NP ? 0 : ip + 1;
     }
     unrolled<kM>([&](auto mc) {
       constexpr int m = decltype(mc)::value, i = m / C::NJ, j = m % C::NJ;
@@ -286,17 +295,18 @@ struct Reduce {
   }
 };
 
-// One output tile: rows 0..rows-1, columns 0..cols-1 from `out` on.
-template <class C, bool PX, bool QX, bool F32>
+// One output tile: rows 0..rows-1, columns 0..cols-1 from `out` on.  STREAM:
+// the output passes the caches by.
+template <class C, bool PX, bool QX, bool F32, bool STREAM>
 __device__ __forceinline__ void tile_product(uint8_t* smem, const uint16_t* p, long long ldp, const uint16_t* q,
                                              long long ldq, int rows, int cols, int length, void* out, long long ldo) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  using P = Operand<PX, C::BM, C::kWaves>;
-  using Q = Operand<QX, C::BN, C::kWaves>;
+  using P = Operand<PX, C::BM, C::kWaves, C::STEP>;
+  using Q = Operand<QX, C::BN, C::kWaves, C::STEP>;
   const P op(p, ldp, rows, length, wave, lane);
   const Q oq(q, ldq, cols, length, wave, lane);
   const int wm = wave / C::WN, wn = wave % C::WN;
-  const int stages = (length + kStep - 1) / kStep;
+  const int stages = (length + C::STEP - 1) / C::STEP;
   f32x16_t acc[C::MI][C::NJ];
 #pragma unroll
   for (int i = 0; i < C::MI; ++i)
@@ -313,28 +323,53 @@ __device__ __forceinline__ void tile_product(uint8_t* smem, const uint16_t* p, l
   else if (live == 1) Reduce<C, PX, QX, 1>::run(smem, op, oq, stages, wm, wn, lane, acc);
   else Reduce<C, PX, QX, 0>::run(smem, op, oq, stages, wm, wn, lane, acc);
 
-  // 32x32 D layout with Q first: lane holds output row l%32, columns 8(r/4) + 4(l/32) + r%4
-  const int h = lane >> 5;
+  // 32x32 D layout with Q first: lane holds output row l%32, columns
+  // 8 t + 4 (l/32) + [0, 4).  The wave's blocks pass through its own part of
+  // the rings, 32 rows at a time, and leave as whole rows, 16 bytes a lane:
+  // stored from the MFMA layout a row's line would be written in four parts
+  // (non-temporal stores of such parts took dw from 1.4 to 4.4 ms).  Chunks
+  // are permuted by chunk ^ row, for the banks.  The barrier finds every wave
+  // done reading the rings.
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  constexpr int kSize = F32 ? 4 : 2, kRowBytes = C::NJ * 32 * kSize, kChunks = kRowBytes / 16;
+  constexpr int kMask = kChunks < 16 ? kChunks - 1 : 15;
+  static_assert(C::kWaves * 32 * kRowBytes <= C::kSmem && 64 % kChunks == 0, "a block of every wave fits");
+  uint8_t* const stg = smem + wave * (32 * kRowBytes);
+  const int h = lane >> 5, rl = lane & 31;
 #pragma unroll
   for (int i = 0; i < C::MI; ++i) {
-    const int row = (i * C::WM + wm) * 32 + (lane & 31);
-    if (row >= rows) continue;
+    const int r0 = (i * C::WM + wm) * 32;
+    if (r0 >= rows) break;
 #pragma unroll
     for (int j = 0; j < C::NJ; ++j)
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const int col = (wn * C::NJ + j) * 32 + 8 * t + 4 * h;
-        if (col >= cols) continue;   // cols is a multiple of 8
         const f32x16_t& a = acc[i][j];
+        uint8_t* const at = stg + rl * kRowBytes;
         if constexpr (F32) {
-          *reinterpret_cast<float4*>(static_cast<float*>(out) + (long long)row * ldo + col) =
+          *reinterpret_cast<float4*>(at + (((8 * j + 2 * t + h) ^ (rl & kMask)) * 16)) =
               make_float4(a[4 * t], a[4 * t + 1], a[4 * t + 2], a[4 * t + 3]);
         } else {
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + (long long)row * ldo + col) =
+          *reinterpret_cast<uint2*>(at + (((4 * j + t) ^ (rl & kMask)) * 16) + 8 * h) =
               make_uint2(f32_to_bf16_rne(a[4 * t]) | ((uint32_t)f32_to_bf16_rne(a[4 * t + 1]) << 16),
                          f32_to_bf16_rne(a[4 * t + 2]) | ((uint32_t)f32_to_bf16_rne(a[4 * t + 3]) << 16));
         }
       }
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int k = 0; k < kChunks / 2; ++k) {   // 64 / kChunks rows at a time
+      const int r = k * (64 / kChunks) + lane / kChunks, c = lane % kChunks;
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(stg + r * kRowBytes + ((c ^ (r & kMask)) * 16));
+      const int col = wn * (C::NJ * 32) + c * (16 / kSize);
+      u32x4_t* const to = reinterpret_cast<u32x4_t*>(static_cast<uint8_t*>(out) + ((long long)(r0 + r) * ldo + col) * kSize);
+      if (r0 + r < rows && col < cols) {   // cols is a multiple of 8
+        if constexpr (STREAM) __builtin_nontemporal_store(v, to);
+        else *to = v;
+      }
+    }
+    asm volatile("" ::: "memory");
   }
 }
 
@@ -343,7 +378,7 @@ template <class C, bool QX>
 __global__ __launch_bounds__(C::kWaves* kWave, C::kPerCU* C::kWaves / 4) void grouped_rows(const uint16_t* p, long long ldp, const uint16_t* w,
                                                                  const int32_t* offsets, int rows, int groups, int cols,
                                                                  int length, int slices, uint16_t* out) {
-  __shared__ __align__(1024) uint8_t smem[kRing * C::kSlotBytes];
+  __shared__ __align__(1024) uint8_t smem[C::kSmem];
   const RowTiles tiles(offsets, groups, rows, C::BM, threadIdx.x & 63);
   // row tiles are dealt to the XCDs in turn, each with all its column slices
   // one after another: the slices share their rows of x in one L2
@@ -352,17 +387,17 @@ __global__ __launch_bounds__(C::kWaves* kWave, C::kPerCU* C::kWaves / 4) void gr
   const Tile t = tiles.place(tile);
   const int c0 = (int)(blockIdx.x / kXcds - turn * slices) * C::BN;
   const uint16_t* we = w + (size_t)t.e * cols * length;
-  tile_product<C, false, QX, false>(smem, p + (long long)t.row0 * ldp, ldp, QX ? we + c0 : we + (size_t)c0 * length,
+  tile_product<C, false, QX, false, false>(smem, p + (long long)t.row0 * ldp, ldp, QX ? we + c0 : we + (size_t)c0 * length,
                                     QX ? cols : length, t.rows, min(C::BN, cols - c0), length,
                                     out + (long long)t.row0 * cols + c0, cols);
 }
 
 // dw: [n, k] per group
-template <class C, bool F32>
+template <class C, bool F32, bool STREAM>
 __global__ __launch_bounds__(C::kWaves* kWave, C::kPerCU* C::kWaves / 4) void grouped_dw(const uint16_t* dy, long long lddy, const uint16_t* x,
                                                                long long ldx, const int32_t* offsets, int rows, int groups,
                                                                int n, int k, int mtiles, int ntiles, void* out) {
-  __shared__ __align__(1024) uint8_t smem[kRing * C::kSlotBytes];
+  __shared__ __align__(1024) uint8_t smem[C::kSmem];
   const int per = mtiles * ntiles, id = xcd_item(groups * per);
   if (id < 0) return;
   // a group's tiles in bands of eight tile rows: the concurrent ones share
@@ -374,17 +409,17 @@ __global__ __launch_bounds__(C::kWaves* kWave, C::kPerCU* C::kWaves / 4) void gr
   const int lo = min(max(offsets[e], 0), rows), hi = min(max(offsets[e + 1], lo), rows);
   const size_t at = ((size_t)e * n + n0) * k + k0;
   void* o = F32 ? static_cast<void*>(static_cast<float*>(out) + at) : static_cast<void*>(static_cast<uint16_t*>(out) + at);
-  tile_product<C, true, true, F32>(smem, dy + (long long)lo * lddy + n0, lddy, x + (long long)lo * ldx + k0, ldx,
+  tile_product<C, true, true, F32, STREAM>(smem, dy + (long long)lo * lddy + n0, lddy, x + (long long)lo * ldx + k0, ldx,
                                    min(C::BM, n - n0), min(C::BN, k - k0), hi - lo, o, k);
 }
 
 unsigned grid_of(long long items) { return (unsigned)((items + kXcds - 1) / kXcds * kXcds); }
 
 #ifndef ROWS_SHAPE
-#define ROWS_SHAPE 256, 256, 2, 4, 1
+#define ROWS_SHAPE 256, 256, 2, 4, 64, 2, 3, 1
 #endif
 #ifndef DW_SHAPE
-#define DW_SHAPE 256, 256, 2, 4, 1
+#define DW_SHAPE 256, 256, 2, 4, 64, 2, 3, 1
 #endif
 using RowsShape = Shape<ROWS_SHAPE>;
 using DwShape = Shape<DW_SHAPE>;
@@ -416,12 +451,15 @@ hipError_t launch_grouped_dw(const GroupedArgs& a, const void* dy, int64_t lddy,
   using C = DwShape;
   const int mt = (a.n + C::BM - 1) / C::BM, nt = (a.k + C::BN - 1) / C::BN;
   const dim3 grid(grid_of((long long)a.groups * mt * nt)), block(C::kWaves * kWave);
-  if (f32)
-    hipLaunchKernelGGL((grouped_dw<C, true>), grid, block, 0, stream, static_cast<const uint16_t*>(dy), lddy,
+  // gradients beyond the L2s' 32 MB leave nothing there to read again, and
+  // writing past them keeps dy and x in (64 experts... see the table): streamed
+  const bool stream_out = (size_t)a.groups * a.n * a.k * (f32 ? 4 : 2) > kL2Bytes;
+  auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, block, 0, stream, static_cast<const uint16_t*>(dy), lddy,
                        static_cast<const uint16_t*>(x), ldx, a.offsets, a.rows, a.groups, a.n, a.k, mt, nt, dw);
-  else
-    hipLaunchKernelGGL((grouped_dw<C, false>), grid, block, 0, stream, static_cast<const uint16_t*>(dy), lddy,
-                       static_cast<const uint16_t*>(x), ldx, a.offsets, a.rows, a.groups, a.n, a.k, mt, nt, dw);
+  };
+  if (f32) run(stream_out ? grouped_dw<C, true, true> : grouped_dw<C, true, false>);
+  else run(stream_out ? grouped_dw<C, false, true> : grouped_dw<C, false, false>);
   return hipGetLastError();
 }
 
