@@ -284,17 +284,19 @@ moe_status moe_mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, con
 moe_status moe_grouped_matmul(const uint16_t* x, int64_t ldx, const uint16_t* w, const int32_t* offsets, int32_t rows,
                               int32_t num_groups, int32_t n, int32_t k, uint16_t* out, hipStream_t stream);
 
-/* Gradients of moe_grouped_matmul for dy [rows, n] bf16 (rows lddy apart):
- *   dx [rows, k] bf16: dx_r = w_e^T dy_r; rows outside every group are not written
- *   dw [num_groups, n, k] of `dtype`: dw_e = sum over e's rows of dy_r x_r^T,
- *      every element written (zero for an empty group)
- * Each output is one fp32 sum in a fixed order, rounded once (no atomics). */
-moe_status moe_grouped_matmul_dx(const uint16_t* dy, int64_t lddy, const uint16_t* w, const int32_t* offsets,
-                                 int32_t rows, int32_t num_groups, int32_t n, int32_t k, uint16_t* dx,
-                                 hipStream_t stream);
-moe_status moe_grouped_matmul_dw(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx,
-                                 const int32_t* offsets, int32_t rows, int32_t num_groups, int32_t n, int32_t k,
-                                 int32_t dtype, void* dw, hipStream_t stream);
+/* Gradients of moe_grouped_matmul for dy [rows, n] bf16 (rows lddy apart), in
+ * one launch:
+ *   dx [rows, k] bf16 or NULL: dx_r = w_e^T dy_r; rows outside every group are
+ *      not written
+ *   dw [num_groups, n, k] of `dw_dtype` or NULL: dw_e = sum over e's rows of
+ *      dy_r x_r^T, every element written (zero for an empty group)
+ * A NULL gradient is not computed; w is read for dx only, x for dw only, and
+ * either may be NULL where it is not read.  Each output is one fp32 sum in a
+ * fixed order, rounded once (no atomics).  Enqueue-only, no workspace. */
+moe_status moe_grouped_matmul_backward(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx,
+                                       const uint16_t* w, const int32_t* offsets, int32_t rows, int32_t num_groups,
+                                       int32_t n, int32_t k, uint16_t* dx, void* dw, int32_t dw_dtype,
+                                       hipStream_t stream);
 
 /* Peak micro-benchmarks: the measured ceilings a benchmark reports its
  * kernels against beside the published peaks (the pages record each run's

@@ -19,7 +19,7 @@ Names follow the C ABI in include/moe_mxfp4.h:
   mxfp4_dequantize(codes, scales)       -> the values they stand for (moe_mxfp4_dequantize)
   mxfp4_matmul(a_codes, a_scales, b_codes, b_scales)  -> A B^T       (moe_mxfp4_matmul)
   grouped_matmul(x, w, offsets)         rows sorted by group times the group's matrix (moe_grouped_matmul)
-  grouped_matmul_backward(dy, x, w, offsets)          -> (dx, dw)    (moe_grouped_matmul_dx / _dw)
+  grouped_matmul_backward(dy, x, w, offsets)          -> (dx, dw)    (moe_grouped_matmul_backward)
   probe_memory(kind, src, dst, sink)    peak micro-benchmarks (moe_probe_memory / moe_probe_mfma)
   probe_mfma(kind, iters, sink)         -> flops of the launch
 """
@@ -44,7 +44,7 @@ EXPORTS = ("moe_mxfp4_query_sizes", "moe_mxfp4_plan", "moe_mxfp4_forward", "moe_
            "moe_mxfp4_forward_fused",
            "moe_mxfp4_fused_status", "moe_mxfp4_route", "moe_mxfp4_workspace_region", "moe_mxfp8_quantize",
            "moe_router_topk", "moe_mxfp4_quantize", "moe_mxfp4_dequantize", "moe_mxfp4_matmul",
-           "moe_grouped_matmul", "moe_grouped_matmul_dx", "moe_grouped_matmul_dw", "moe_probe_memory", "moe_probe_mfma", "moe_probe_mfma_f8f4_blocks",
+           "moe_grouped_matmul", "moe_grouped_matmul_backward", "moe_probe_memory", "moe_probe_mfma", "moe_probe_mfma_f8f4_blocks",
            "moe_mxfp4_set_stage_events",
            "moe_mxfp4_destroy", "moe_mxfp4_last_error")
 _STATUS_FNS = tuple(n for n in EXPORTS if n not in ("moe_mxfp4_destroy", "moe_mxfp4_last_error"))
@@ -104,8 +104,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_mxfp4_dequantize.argtypes = [vp, vp, i32, i32, i32, vp, vp]
     lib.moe_mxfp4_matmul.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp]
     lib.moe_grouped_matmul.argtypes = [vp, i64, vp, vp, i32, i32, i32, i32, vp, vp]
-    lib.moe_grouped_matmul_dx.argtypes = [vp, i64, vp, vp, i32, i32, i32, i32, vp, vp]
-    lib.moe_grouped_matmul_dw.argtypes = [vp, i64, vp, i64, vp, i32, i32, i32, i32, i32, vp, vp]
+    lib.moe_grouped_matmul_backward.argtypes = [vp, i64, vp, i64, vp, vp, i32, i32, i32, i32, vp, vp, i32, vp]
     lib.moe_probe_memory.argtypes = [i32, vp, vp, sz, vp, i32, vp]
     lib.moe_probe_mfma.argtypes = [i32, i32, vp, i32, ctypes.POINTER(ctypes.c_double), vp]
     lib.moe_probe_mfma_f8f4_blocks.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp]
@@ -544,15 +543,15 @@ def grouped_matmul_backward(dy, x, w, offsets, dx=None, dw=None, dw_dtype=None, 
                             stream=None):
     """(dx, dw) of grouped_matmul for dy [rows, n] bf16: dx [rows, k] bf16 (rows
     outside every group are left as they were), dw [num_groups, n, k] in fp32
-    (default) or bf16, zero for an empty group (moe_grouped_matmul_dx / _dw).
+    (default) or bf16, zero for an empty group (moe_grouped_matmul_backward).
     need_dx / need_dw False: that gradient is not computed and returned as None
     (x is not read without need_dw and may then be None)."""
     import torch
     groups, n, k = _grouped(w, offsets)
     lddy = _rows(dy, "dy", (torch.bfloat16,), n, w)
     rows = dy.shape[0]
-    lib = load_library()
     used = [dy, w, offsets]
+    ldx, code, x_at, dw_at, dx_at = k, MOE_F32, None, None, None
     if need_dw:
         ldx = _rows(x, "x", (torch.bfloat16,), k, w)
         if x.shape[0] != rows:
@@ -561,6 +560,7 @@ def grouped_matmul_backward(dy, x, w, offsets, dx=None, dw=None, dw_dtype=None, 
             dw_dtype = torch.float32
         dw, code = _float_out(dw, "dw", (groups, n, k), dw_dtype, w, stream, ("dy", dy), ("x", x), ("w", w),
                               ("offsets", offsets))
+        x_at, dw_at = x.data_ptr(), dw.data_ptr()
         used += [x, dw]
     else:
         dw = None
@@ -572,17 +572,13 @@ def grouped_matmul_backward(dy, x, w, offsets, dx=None, dw=None, dw_dtype=None, 
             _apart(dx, "dx", ("dy", dy), ("w", w), ("offsets", offsets))
             if need_dw:
                 _apart(dx, "dx", ("x", x), ("dw", dw))
+        dx_at = dx.data_ptr()
         used.append(dx)
     else:
         dx = None
-    if need_dx:
-        _launch(lib.moe_grouped_matmul_dx,
-                (dy.data_ptr(), lddy, w.data_ptr(), offsets.data_ptr(), rows, groups, n, k, dx.data_ptr()), w, stream,
-                used)
-    if need_dw:
-        _launch(lib.moe_grouped_matmul_dw,
-                (dy.data_ptr(), lddy, x.data_ptr(), ldx, offsets.data_ptr(), rows, groups, n, k, code, dw.data_ptr()),
-                w, stream, used)
+    _launch(load_library().moe_grouped_matmul_backward,
+            (dy.data_ptr(), lddy, x_at, ldx, w.data_ptr(), offsets.data_ptr(), rows, groups, n, k, dx_at, dw_at, code),
+            w, stream, used)
     return dx, dw
 
 

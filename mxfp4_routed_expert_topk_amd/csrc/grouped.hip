@@ -189,14 +189,6 @@ struct RowTiles {
   }
 };
 
-// Workgroups go to the XCDs in turn: XCD x takes the x-th eighth of `total`
-// items in order, so that items which share operands share an L2.  -1: none.
-__device__ __forceinline__ int xcd_item(int total) {
-  const int chunk = (total + kXcds - 1) / kXcds, i = blockIdx.x / kXcds;
-  const int id = (int)(blockIdx.x % kXcds) * chunk + i;
-  return i < chunk && id < total ? id : -1;
-}
-
 // W waves as WM x WN.  A wave's 32-row blocks are every WM-th one, so that the
 // blocks past a tile's last row, which are skipped, are spread over the waves;
 // its 32-column blocks lie side by side.
@@ -373,47 +365,91 @@ __device__ __forceinline__ void tile_product(uint8_t* smem, const uint16_t* p, l
   }
 }
 
-// forward (QX false: w_e [cols, length]) and dx (QX true: w_e [length, cols]).
+// How the (row tile, column slice) items are dealt to the XCDs: to `parts`
+// (4, 2 or 1) shares of the slices and kXcds / parts turns of the row tiles.
+// Each weight then crosses to kXcds / parts L2s only, and 32 concurrent
+// workgroups of an XCD (one per CU) hold e.g. 8 row tiles x 4 slices: 12
+// operand tiles to fetch per stage where 2 x 16 (every XCD all slices) need 18.
+struct Deal {
+  int slices, parts, share;   // share: slices per part, the last part may have fewer
+};
+inline Deal deal(int slices) {
+  const int parts = slices % 4 == 0 || slices > 12 ? 4 : slices % 2 == 0 || slices > 4 ? 2 : 1;
+  return {slices, parts, (slices + parts - 1) / parts};
+}
+
+// Item i of XCD `xcd`'s list.
 template <class C, bool QX>
-__global__ __launch_bounds__(C::kWaves* kWave, C::kPerCU* C::kWaves / 4) void grouped_rows(const uint16_t* p, long long ldp, const uint16_t* w,
-                                                                 const int32_t* offsets, int rows, int groups, int cols,
-                                                                 int length, int slices, uint16_t* out) {
-  __shared__ __align__(1024) uint8_t smem[C::kSmem];
+__device__ __forceinline__ void rows_item(uint8_t* smem, const uint16_t* p, long long ldp, const uint16_t* w,
+                                          const int32_t* offsets, int rows, int groups, int cols, int length, Deal d,
+                                          uint16_t* out, int xcd, int i) {
+  const int turn = i / d.share, slice = xcd % d.parts * d.share + i - turn * d.share;
+  const int tile = turn * (kXcds / d.parts) + xcd / d.parts;
+  if (slice >= d.slices) return;
   const RowTiles tiles(offsets, groups, rows, C::BM, threadIdx.x & 63);
-  // row tiles are dealt to the XCDs in turn, each with all its column slices
-  // one after another: the slices share their rows of x in one L2
-  const int turn = blockIdx.x / kXcds / slices, tile = turn * kXcds + blockIdx.x % kXcds;
   if (tile >= tiles.total) return;
   const Tile t = tiles.place(tile);
-  const int c0 = (int)(blockIdx.x / kXcds - turn * slices) * C::BN;
+  const int c0 = slice * C::BN;
   const uint16_t* we = w + (size_t)t.e * cols * length;
-  tile_product<C, false, QX, false, false>(smem, p + (long long)t.row0 * ldp, ldp, QX ? we + c0 : we + (size_t)c0 * length,
-                                    QX ? cols : length, t.rows, min(C::BN, cols - c0), length,
-                                    out + (long long)t.row0 * cols + c0, cols);
+  tile_product<C, false, QX, false, false>(smem, p + (long long)t.row0 * ldp, ldp,
+                                           QX ? we + c0 : we + (size_t)c0 * length, QX ? cols : length, t.rows,
+                                           min(C::BN, cols - c0), length, out + (long long)t.row0 * cols + c0, cols);
 }
 
-// dw: [n, k] per group
-template <class C, bool F32, bool STREAM>
-__global__ __launch_bounds__(C::kWaves* kWave, C::kPerCU* C::kWaves / 4) void grouped_dw(const uint16_t* dy, long long lddy, const uint16_t* x,
-                                                               long long ldx, const int32_t* offsets, int rows, int groups,
-                                                               int n, int k, int mtiles, int ntiles, void* out) {
+// y = x w_e^T
+template <class C>
+__global__ __launch_bounds__(C::kWaves* kWave, C::kPerCU* C::kWaves / 4) void grouped_forward(
+    const uint16_t* x, long long ldx, const uint16_t* w, const int32_t* offsets, int rows, int groups, int n, int k,
+    Deal d, uint16_t* out) {
   __shared__ __align__(1024) uint8_t smem[C::kSmem];
-  const int per = mtiles * ntiles, id = xcd_item(groups * per);
-  if (id < 0) return;
-  // a group's tiles in bands of eight tile rows: the concurrent ones share
-  // their columns of dy and x
-  const int e = id / per, i = id - e * per;
-  constexpr int kBand = 8;
-  const int band = i / (kBand * ntiles), in = i - band * kBand * ntiles, high = min(kBand, mtiles - band * kBand);
-  const int n0 = (band * kBand + in % high) * C::BM, k0 = in / high * C::BN;
-  const int lo = min(max(offsets[e], 0), rows), hi = min(max(offsets[e + 1], lo), rows);
-  const size_t at = ((size_t)e * n + n0) * k + k0;
-  void* o = F32 ? static_cast<void*>(static_cast<float*>(out) + at) : static_cast<void*>(static_cast<uint16_t*>(out) + at);
-  tile_product<C, true, true, F32, STREAM>(smem, dy + (long long)lo * lddy + n0, lddy, x + (long long)lo * ldx + k0, ldx,
-                                   min(C::BM, n - n0), min(C::BN, k - k0), hi - lo, o, k);
+  rows_item<C, false>(smem, x, ldx, w, offsets, rows, groups, n, k, d, out, blockIdx.x % kXcds, blockIdx.x / kXcds);
 }
 
-unsigned grid_of(long long items) { return (unsigned)((items + kXcds - 1) / kXcds * kXcds); }
+struct BackwardArgs {
+  const uint16_t *dy, *x, *w;
+  long long lddy, ldx;
+  const int32_t* offsets;
+  int rows, groups, n, k;
+  uint16_t* dx;
+  void* dw;
+  Deal dx_deal;
+  int dx_items, dw_items;   // per XCD (dx: at most)
+};
+
+// Both gradients in one launch, an XCD's dw tiles and then its dx items.
+// (Mixed in proportion, so that some CUs would write while others multiply,
+// 32 experts x 4096 x 7168 with 12288 rows took 2033 us; dw first 1977.)
+template <class C, bool F32, bool STREAM>
+__global__ __launch_bounds__(C::kWaves* kWave, C::kPerCU* C::kWaves / 4) void grouped_backward(BackwardArgs a) {
+  __shared__ __align__(1024) uint8_t smem[C::kSmem];
+  const int xcd = blockIdx.x % kXcds, i = blockIdx.x / kXcds;
+  if (i >= a.dw_items) {
+    rows_item<C, true>(smem, a.dy, a.lddy, a.w, a.offsets, a.rows, a.groups, a.k, a.n, a.dx_deal, a.dx, xcd,
+                       i - a.dw_items);
+    return;
+  }
+  // XCD x takes the x-th eighth of the dw tiles: a group's tiles in bands of
+  // eight tile rows, whose concurrent ones share their columns of dy and x
+  const int mtiles = (a.n + C::BM - 1) / C::BM, ntiles = (a.k + C::BN - 1) / C::BN, per = mtiles * ntiles;
+  const int id = xcd * a.dw_items + i;
+  const int e = id / per, j = id - e * per;
+  if (e >= a.groups) return;
+  constexpr int kBand = 8;
+  const int band = j / (kBand * ntiles), in = j - band * kBand * ntiles, high = min(kBand, mtiles - band * kBand);
+  const int n0 = (band * kBand + in % high) * C::BM, k0 = in / high * C::BN;
+  const int lo = min(max(a.offsets[e], 0), a.rows), hi = min(max(a.offsets[e + 1], lo), a.rows);
+  const size_t at = ((size_t)e * a.n + n0) * a.k + k0;
+  void* o = F32 ? static_cast<void*>(static_cast<float*>(a.dw) + at) : static_cast<void*>(static_cast<uint16_t*>(a.dw) + at);
+  tile_product<C, true, true, F32, STREAM>(smem, a.dy + (long long)lo * a.lddy + n0, a.lddy,
+                                           a.x + (long long)lo * a.ldx + k0, a.ldx, min(C::BM, a.n - n0),
+                                           min(C::BN, a.k - k0), hi - lo, o, a.k);
+}
+
+// items per XCD there can be with row tiles of bm rows
+long long items_per_xcd(const GroupedArgs& a, int bm, const Deal& d) {
+  const int turns = kXcds / d.parts;
+  return ((long long)a.rows / bm + std::min(a.groups, a.rows) + turns - 1) / turns * d.share;
+}
 
 #ifndef ROWS_SHAPE
 #define ROWS_SHAPE 256, 256, 2, 4, 64, 2, 3, 1
@@ -424,42 +460,35 @@ unsigned grid_of(long long items) { return (unsigned)((items + kXcds - 1) / kXcd
 using RowsShape = Shape<ROWS_SHAPE>;
 using DwShape = Shape<DW_SHAPE>;
 
-template <bool QX>
-hipError_t launch_rows(const GroupedArgs& a, const void* p, int64_t ldp, int cols, int length, void* out,
-                       hipStream_t stream) {
-  using C = RowsShape;
-  const int slices = (cols + C::BN - 1) / C::BN;
-  const long long tiles = a.rows / C::BM + std::min(a.groups, a.rows);
-  hipLaunchKernelGGL((grouped_rows<C, QX>), dim3((unsigned)((tiles + kXcds - 1) / kXcds * kXcds * slices)), dim3(C::kWaves * kWave), 0, stream,
-                     static_cast<const uint16_t*>(p), ldp, static_cast<const uint16_t*>(a.w), a.offsets, a.rows, a.groups,
-                     cols, length, slices, static_cast<uint16_t*>(out));
-  return hipGetLastError();
-}
-
 }  // namespace
 
 hipError_t launch_grouped_forward(const GroupedArgs& a, const void* x, int64_t ldx, void* y, hipStream_t stream) {
-  return launch_rows<false>(a, x, ldx, a.n, a.k, y, stream);
+  using C = RowsShape;
+  const Deal d = deal((a.n + C::BN - 1) / C::BN);
+  hipLaunchKernelGGL((grouped_forward<C>), dim3((unsigned)(items_per_xcd(a, C::BM, d) * kXcds)),
+                     dim3(C::kWaves * kWave), 0, stream, static_cast<const uint16_t*>(x), ldx,
+                     static_cast<const uint16_t*>(a.w), a.offsets, a.rows, a.groups, a.n, a.k, d,
+                     static_cast<uint16_t*>(y));
+  return hipGetLastError();
 }
 
-hipError_t launch_grouped_dx(const GroupedArgs& a, const void* dy, int64_t lddy, void* dx, hipStream_t stream) {
-  return launch_rows<true>(a, dy, lddy, a.k, a.n, dx, stream);
-}
-
-hipError_t launch_grouped_dw(const GroupedArgs& a, const void* dy, int64_t lddy, const void* x, int64_t ldx, bool f32,
-                             void* dw, hipStream_t stream) {
+hipError_t launch_grouped_backward(const GroupedArgs& a, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                   void* dx, bool f32, void* dw, hipStream_t stream) {
   using C = DwShape;
-  const int mt = (a.n + C::BM - 1) / C::BM, nt = (a.k + C::BN - 1) / C::BN;
-  const dim3 grid(grid_of((long long)a.groups * mt * nt)), block(C::kWaves * kWave);
-  // gradients beyond the L2s' 32 MB leave nothing there to read again, and
-  // writing past them keeps dy and x in (64 experts... see the table): streamed
+  BackwardArgs b{static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(a.w),
+                 lddy, ldx, a.offsets, a.rows, a.groups, a.n, a.k, static_cast<uint16_t*>(dx), dw, deal((a.k + C::BN - 1) / C::BN), 0, 0};
+  if (dx) b.dx_items = (int)items_per_xcd(a, C::BM, b.dx_deal);
+  if (dw)
+    b.dw_items = (int)(((long long)a.groups * ((a.n + C::BM - 1) / C::BM) * ((a.k + C::BN - 1) / C::BN) + kXcds - 1) / kXcds);
+  if (b.dx_items + b.dw_items == 0) return hipSuccess;
+  // dw beyond the L2s' 32 MB leaves nothing there to read again and would
+  // push dy and x out: streamed
   const bool stream_out = (size_t)a.groups * a.n * a.k * (f32 ? 4 : 2) > kL2Bytes;
   auto run = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, block, 0, stream, static_cast<const uint16_t*>(dy), lddy,
-                       static_cast<const uint16_t*>(x), ldx, a.offsets, a.rows, a.groups, a.n, a.k, mt, nt, dw);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(b.dx_items + b.dw_items) * kXcds), dim3(C::kWaves * kWave), 0, stream, b);
   };
-  if (f32) run(stream_out ? grouped_dw<C, true, true> : grouped_dw<C, true, false>);
-  else run(stream_out ? grouped_dw<C, false, true> : grouped_dw<C, false, false>);
+  if (f32) run(stream_out ? grouped_backward<C, true, true> : grouped_backward<C, true, false>);
+  else run(stream_out ? grouped_backward<C, false, true> : grouped_backward<C, false, false>);
   return hipGetLastError();
 }
 

@@ -182,9 +182,9 @@ struct GroupedArgs {
   int rows, groups, n, k;
 };
 hipError_t launch_grouped_forward(const GroupedArgs& a, const void* x, int64_t ldx, void* y, hipStream_t stream);
-hipError_t launch_grouped_dx(const GroupedArgs& a, const void* dy, int64_t lddy, void* dx, hipStream_t stream);
-hipError_t launch_grouped_dw(const GroupedArgs& a, const void* dy, int64_t lddy, const void* x, int64_t ldx, bool f32,
-                             void* dw, hipStream_t stream);
+// dx or dw null: not computed (x null too without dw, w without dx); dx only with rows above zero
+hipError_t launch_grouped_backward(const GroupedArgs& a, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                   void* dx, bool f32, void* dw, hipStream_t stream);
 
 // Router top-k (E <= kRouterMaxExperts, k <= 32).
 constexpr int kRouterMaxExperts = 1024;

@@ -121,31 +121,29 @@ moe_status moe_grouped_matmul(const uint16_t* x, int64_t ldx, const uint16_t* w,
   return e == hipSuccess ? ok() : hip_fail(e, "grouped matmul launch");
 }
 
-moe_status moe_grouped_matmul_dx(const uint16_t* dy, int64_t lddy, const uint16_t* w, const int32_t* offsets,
-                                 int32_t rows, int32_t num_groups, int32_t n, int32_t k, uint16_t* dx,
-                                 hipStream_t stream) {
-  if (moe_status s = check_grouped(rows, num_groups, n, k)) return s;
-  if (moe_status s = check_ld("lddy", lddy, n)) return s;
-  if (rows == 0 || num_groups == 0) return ok();
-  if (moe_status s = check_ptrs({{"dy", dy}, {"w", w}, {"offsets", offsets}, {"dx", dx}})) return s;
-  const hipError_t e = moe::launch_grouped_dx({w, offsets, rows, num_groups, n, k}, dy, lddy, dx, stream);
-  return e == hipSuccess ? ok() : hip_fail(e, "grouped matmul dx launch");
-}
-
-moe_status moe_grouped_matmul_dw(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx,
-                                 const int32_t* offsets, int32_t rows, int32_t num_groups, int32_t n, int32_t k,
-                                 int32_t dtype, void* dw, hipStream_t stream) {
-  if (moe_status s = check_dtype("dtype", dtype)) return s;
+moe_status moe_grouped_matmul_backward(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx,
+                                       const uint16_t* w, const int32_t* offsets, int32_t rows, int32_t num_groups,
+                                       int32_t n, int32_t k, uint16_t* dx, void* dw, int32_t dw_dtype,
+                                       hipStream_t stream) {
+  if (moe_status s = check_dtype("dw_dtype", dw_dtype)) return s;
   if (moe_status s = check_grouped(rows, num_groups, n, k)) return s;
   if (moe_status s = check_ld("lddy", lddy, n)) return s;
   if (moe_status s = check_ld("ldx", ldx, k)) return s;
-  if (num_groups == 0) return ok();
-  if (moe_status s = check_ptrs({{"offsets", offsets}, {"dw", dw}})) return s;
-  if (rows > 0)   // without rows every gradient is zero and neither is read
-    if (moe_status s = check_ptrs({{"dy", dy}, {"x", x}})) return s;
-  const hipError_t e = moe::launch_grouped_dw({nullptr, offsets, rows, num_groups, n, k}, dy, lddy, x, ldx,
-                                              dtype == MOE_F32, dw, stream);
-  return e == hipSuccess ? ok() : hip_fail(e, "grouped matmul dw launch");
+  if (rows == 0) dx = nullptr;   // no rows to write
+  if (num_groups == 0 || (!dx && !dw)) return ok();
+  if (moe_status s = check_ptrs({{"offsets", offsets}})) return s;
+  if (rows > 0)   // without rows every weight gradient is zero and nothing is read
+    if (moe_status s = check_ptrs({{"dy", dy}})) return s;
+  if (dx)
+    if (moe_status s = check_ptrs({{"w", w}, {"dx", dx}})) return s;
+  if (dw) {
+    if (moe_status s = check_ptrs({{"dw", dw}})) return s;
+    if (rows > 0)
+      if (moe_status s = check_ptrs({{"x", x}})) return s;
+  }
+  const hipError_t e = moe::launch_grouped_backward({w, offsets, rows, num_groups, n, k}, dy, lddy, x, ldx, dx,
+                                                    dw_dtype == MOE_F32, dw, stream);
+  return e == hipSuccess ? ok() : hip_fail(e, "grouped matmul backward launch");
 }
 
 }  // extern "C"

@@ -86,17 +86,21 @@ def test_grouped_matmul_refusals(lib, args, status, needle):
     refused(lib, "moe_grouped_matmul", args, status, needle)
 
 
-@pytest.mark.parametrize("fn,args,status,needle", [
-    ("moe_grouped_matmul_dx", (P, 8, P, P, 4, 2, 16, 64, P, None), 2, "lddy must be"),
-    ("moe_grouped_matmul_dx", (P, 16, P, P, 4, 2, 16, 64, None, None), 1, "dx is null"),
-    ("moe_grouped_matmul_dw", (P, 16, P, 64, P, 4, 2, 16, 64, 7, P, None), 1, "dtype must be"),
-    ("moe_grouped_matmul_dw", (P, 8, P, 64, P, 4, 2, 16, 64, 0, P, None), 2, "lddy must be"),
-    ("moe_grouped_matmul_dw", (P, 16, P, 56, P, 4, 2, 16, 64, 0, P, None), 2, "ldx must be"),
-    ("moe_grouped_matmul_dw", (P, 16, None, 64, P, 4, 2, 16, 64, 0, P, None), 1, "x is null"),
-    ("moe_grouped_matmul_dw", (P, 16, P, 64, P, 4, 2, 16, 64, 0, P + 2, None), 3, "dw must be 16-byte aligned"),
+@pytest.mark.parametrize("args,status,needle", [
+    ((P, 16, P, 64, P, P, 4, 2, 16, 64, P, P, 7, None), 1, "dw_dtype must be"),
+    ((P, 8, P, 64, P, P, 4, 2, 16, 64, P, P, 0, None), 2, "lddy must be"),
+    ((P, 16, P, 56, P, P, 4, 2, 16, 64, P, P, 0, None), 2, "ldx must be"),
+    ((P, 16, P, 64, P, P, -4, 2, 16, 64, P, P, 0, None), 1, "rows must be >= 0"),
+    ((P, 16, P, 64, P, P, 4, 2, 20, 64, P, P, 0, None), 2, "n must be a multiple of 8"),
+    ((None, 16, P, 64, P, P, 4, 2, 16, 64, P, P, 0, None), 1, "dy is null"),
+    ((P, 16, None, 64, P, P, 4, 2, 16, 64, None, P, 0, None), 1, "x is null"),
+    ((P, 16, P, 64, None, P, 4, 2, 16, 64, P, None, 0, None), 1, "w is null"),
+    ((P, 16, P, 64, P, None, 4, 2, 16, 64, P, P, 0, None), 1, "offsets is null"),
+    ((P, 16, P, 64, P, P, 4, 2, 16, 64, P + 8, None, 0, None), 3, "dx must be 16-byte aligned"),
+    ((P, 16, P, 64, P, P, 4, 2, 16, 64, None, P + 2, 0, None), 3, "dw must be 16-byte aligned"),
 ])
-def test_grouped_gradient_refusals(lib, fn, args, status, needle):
-    refused(lib, fn, args, status, needle)
+def test_grouped_backward_refusals(lib, args, status, needle):
+    refused(lib, "moe_grouped_matmul_backward", args, status, needle)
 
 
 def test_empty_calls_are_no_ops(lib):
@@ -106,8 +110,9 @@ def test_empty_calls_are_no_ops(lib):
     assert lib.moe_mxfp4_matmul(None, None, None, None, 5, 0, 64, 0, None, None) == 0
     assert lib.moe_grouped_matmul(None, 64, None, None, 0, 2, 16, 64, None, None) == 0
     assert lib.moe_grouped_matmul(None, 64, None, None, 4, 0, 16, 64, None, None) == 0
-    assert lib.moe_grouped_matmul_dx(None, 16, None, None, 0, 2, 16, 64, None, None) == 0
-    assert lib.moe_grouped_matmul_dw(None, 16, None, 64, None, 4, 0, 16, 64, 0, None, None) == 0
+    assert lib.moe_grouped_matmul_backward(None, 16, None, 64, None, None, 4, 0, 16, 64, None, None, 0, None) == 0
+    assert lib.moe_grouped_matmul_backward(None, 16, None, 64, None, None, 4, 2, 16, 64, None, None, 0, None) == 0
+    assert lib.moe_grouped_matmul_backward(None, 16, None, 64, None, None, 0, 2, 16, 64, P, None, 0, None) == 0
 
 
 def z(*shape, dtype=BF):
