@@ -18,8 +18,6 @@
 namespace moe {
 namespace {
 
-constexpr int kSplit = 4;   // waves per workgroup, each a share of K
-
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ f32x4_t mfma_fp4(u32x4_t b, u32x4_t a, f32x4_t c, int sb, int sa) {
@@ -28,78 +26,122 @@ __device__ __forceinline__ f32x4_t mfma_fp4(u32x4_t b, u32x4_t a, f32x4_t c, int
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(B, A, c, 4, 4, 0, sb, 0, sa);
 }
 
-// One workgroup per 16 x 16 outputs.  groups: K / 32.
-template <bool F32>
-__global__ __launch_bounds__(kSplit* kWave) void matmul_mxfp4(const uint8_t* __restrict__ ac, const uint8_t* __restrict__ as,
-                                                              const uint8_t* __restrict__ bc, const uint8_t* __restrict__ bs,
-                                                              int M, int N, int groups, void* __restrict__ out) {
-  __shared__ f32x4_t part[kSplit - 1][kWave];
+// ---- few rows: B is streamed once per 16 MT rows of A.
+//
+// A workgroup owns 16 columns and MT 16-row blocks; its kSplit waves take 256
+// K at a time in turn and their partial sums are added in wave order.  In 256
+// K a lane takes the 32 contiguous bytes of blocks 2q and 2q + 1 (of A alike),
+// one MFMA step each, so that a row's 128 bytes are fetched as a whole line;
+// which blocks share a step does not matter to the sum.  Two such units are
+// in flight per wave.
+constexpr int kSplit = 8;
+
+// 16 bytes of codes, a chunk past K as zeros with scale 2^0
+struct Operand4 {
+  u32x4_t v[2];
+  int s[2];
+  __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, size_t row, int unit, int q, int groups) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int g = 8 * unit + 2 * q + i;
+      v[i] = u32x4_t{0, 0, 0, 0};
+      s[i] = 127;
+      if (g < groups) {
+        v[i] = *reinterpret_cast<const u32x4_t*>(codes + (row * groups + g) * 16);
+        s[i] = scales[row * groups + g];
+      }
+    }
+  }
+};
+
+// groups: K / 32
+template <int MT, bool F32>
+__global__ __launch_bounds__(kSplit* kWave) void matmul_mxfp4_rows(const uint8_t* __restrict__ ac, const uint8_t* __restrict__ as,
+                                                                   const uint8_t* __restrict__ bc, const uint8_t* __restrict__ bs,
+                                                                   int M, int N, int groups, void* __restrict__ out) {
+  __shared__ f32x4_t part[kSplit][MT][kWave];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, q = lane >> 4;
-  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16;
+  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * (16 * MT);
   // rows past the matrix repeat its last row and are not stored
-  const size_t arow = (size_t)min(m0 + r, M - 1) * groups, brow = (size_t)min(n0 + r, N - 1) * groups;
-  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-  const int steps = (groups + 3) / 4;
-  for (int s = wave; s < steps; s += kSplit) {
-    const int g = 4 * s + q;             // this lane's block of 32
-    u32x4_t a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-    int sa = 127, sb = 127;
-    if (g < groups) {
-      a = *reinterpret_cast<const u32x4_t*>(ac + (arow + g) * 16);
-      b = *reinterpret_cast<const u32x4_t*>(bc + (brow + g) * 16);
-      sa = as[arow + g];
-      sb = bs[brow + g];
-    }
-    acc = mfma_fp4(b, a, acc, sb, sa);
-  }
-  if (wave) part[wave - 1][lane] = acc;
-  __syncthreads();
-  if (wave) return;
-  for (int w = 0; w < kSplit - 1; ++w) acc += part[w][lane];
-  const int m = m0 + r;
-  if (m >= M) return;
+  const size_t brow = min(n0 + r, N - 1);
+  f32x4_t acc[MT];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int n = n0 + 4 * q + i;
-    if (n >= N) break;
-    if (F32) static_cast<float*>(out)[(size_t)m * N + n] = acc[i];
-    else static_cast<uint16_t*>(out)[(size_t)m * N + n] = f32_to_bf16_rne(acc[i]);
+  for (int i = 0; i < MT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int units = (groups + 7) / 8;
+  for (int u = wave; u < units; u += 2 * kSplit) {
+    Operand4 b[2], a[2][MT];
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      b[d].load(bc, bs, brow, u + d * kSplit, q, groups);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) a[d][i].load(ac, as, min(m0 + 16 * i + r, M - 1), u + d * kSplit, q, groups);
+    }
+#pragma unroll
+    for (int d = 0; d < 2; ++d)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[i] = mfma_fp4(b[d].v[h], a[d][i].v[h], acc[i], b[d].s[h], a[d][i].s[h]);
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
+  __syncthreads();
+  if (wave >= MT) return;   // wave i adds and stores row block i
+  f32x4_t v = part[0][wave][lane];
+#pragma unroll
+  for (int w = 1; w < kSplit; ++w) v += part[w][wave][lane];
+  const int m = m0 + 16 * wave + r, n = n0 + 4 * q;
+  if (m >= M) return;
+  const size_t at = (size_t)m * N + n;
+  if (N % 4 == 0) {
+    if (n >= N) return;
+    if constexpr (F32) *reinterpret_cast<f32x4_t*>(static_cast<float*>(out) + at) = v;
+    else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
+        make_uint2(f32_to_bf16_rne(v[0]) | ((uint32_t)f32_to_bf16_rne(v[1]) << 16),
+                   f32_to_bf16_rne(v[2]) | ((uint32_t)f32_to_bf16_rne(v[3]) << 16));
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (n + e >= N) break;
+    if (F32) static_cast<float*>(out)[at + e] = v[e];
+    else static_cast<uint16_t*>(out)[at + e] = f32_to_bf16_rne(v[e]);
   }
 }
 
 // ---- many rows: BM x BN output tiles, operands staged through LDS.
 //
-// One stage is 128 K: 64 bytes of codes per row, copied global -> LDS by
-// buffer_load ... lds (16 rows per wave instruction) into a ring of four
-// stages, three ahead.  The four 16-byte chunks of a staged row are permuted
-// by chunk ^ ((row >> 2) & 3): the sixteen rows of a quarter-wave's
-// ds_read_b128 then cover all 64 banks once.  Copies past an edge get an
-// out-of-range offset and write zeros.
-// A group of four stages (512 K) has 16 scale bytes per row.  Thread t loads
-// those of row t one group ahead, transposes them to four dwords (dword q:
-// the bytes of blocks q, q + 4, q + 8, q + 12, that is lane quarter q's
-// scales of the four stages) and stores them in LDS; a wave reads one dword
-// per lane, 16-row block and group, and each stage's MFMA picks its byte.
+// One stage is 256 K: 128 bytes of codes per row, whole cache lines, copied
+// global -> LDS by buffer_load ... lds (8 rows per wave instruction) into one
+// of two buffers while the other multiplies.  (With 128 K a stage, half lines,
+// the copies took 62 us against 59 at 4096 x 4096 x 7168.)  The eight 16-byte chunks of a staged row are permuted
+// by chunk ^ (row & 7) ^ ((row >> 3) & 1): the sixteen rows of a
+// quarter-wave's ds_read_b128 then cover all 64 banks once.  Copies past an
+// edge get an out-of-range offset and write zeros.
+// A pair of stages (512 K) has 16 scale bytes per row.  Thread t loads those
+// of row t one pair ahead, transposes them to four dwords (dword q: the bytes
+// of blocks q, q + 4, q + 8, q + 12, that is lane quarter q's scales of the
+// pair's four MFMA steps) and stores them in LDS; a wave reads one dword per
+// lane, 16-row block and pair, and each step's MFMA picks its byte.
 typedef __attribute__((address_space(3))) void lds_void_t;
 
-constexpr int kRing = 4;
 constexpr uint32_t kPastEnd = 0x80000000u;   // beyond every buffer resource below
 
 #define MOE_WAIT_VM(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (7 << 4) | ((((n) >> 4) & 3) << 14))
 
-__device__ __forceinline__ int swz4(int c, int r) { return c ^ ((r >> 2) & 3); }
+__device__ __forceinline__ int swz(int c, int r) { return c ^ (r & 7) ^ ((r >> 3) & 1); }
 
 template <int BM_, int BN_, int WM_, int WN_>
 struct MxShape {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, kWaves = WM * WN;
   static constexpr int MI = BM / WM / 16, NJ = BN / WN / 16;
   static constexpr int kRows = BM + BN;                 // staged rows: A's, then B's
-  static constexpr int kStageBytes = kRows * 64;
-  static constexpr int kCopies = kRows / 16 / kWaves;   // copies per wave and stage
-  static constexpr int kScaleBytes = kRows * 16;        // one group
-  static constexpr int kSmem = kRing * kStageBytes + 2 * kScaleBytes;
-  static_assert(kCopies * kWaves * 16 == kRows && (BM / 16) % kWaves == 0 && kRows % (kWaves * kWave) == 0, "even split");
+  static constexpr int kStageBytes = kRows * 128;
+  static constexpr int kCopies = kRows / 8 / kWaves;    // copies per wave and stage
+  static constexpr int kScaleBytes = kRows * 16;        // one pair of stages
+  static constexpr int kSmem = 2 * kStageBytes + 2 * kScaleBytes;
+  static_assert(kCopies * kWaves * 8 == kRows && (BM / 8) % kWaves == 0 && kWaves % 2 == 0 && kRows == kWaves * kWave && BM % kWave == 0, "even split");
 };
 
 // the four dwords of a row's 16 scale bytes: dword q holds bytes q, 4 + q, 8 + q, 12 + q
@@ -133,62 +175,64 @@ __device__ __forceinline__ void matmul_tile(uint8_t* smem, const uint8_t* ac, co
   const int m0 = (band * kBand + in % high) * C::BM, n0 = in / high * C::BN;
   const int mrows = min(C::BM, M - m0), nrows = min(C::BN, N - n0);
   const uint32_t pitch = (uint32_t)groups * 16;   // bytes of a row's codes
-  const int stages = (groups + 3) / 4;
+  // whole pairs of stages: what is past K multiplies zeros
+  const int pairs = (groups + 15) / 16;
 
   const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(ac) + (size_t)m0 * pitch, (short)0, (int)(mrows * pitch), kRsrcWord3);
   const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(bc) + (size_t)n0 * pitch, (short)0, (int)(nrows * pitch), kRsrcWord3);
-  // copy j of this wave fills staged rows 16 (wave + kWaves j) ..; the first BM rows are A's
-  constexpr int kCopiesA = C::BM / 16 / C::kWaves;
+  // copy j of this wave fills staged rows 8 (wave + kWaves j) ..; the first BM rows are A's
+  constexpr int kCopiesA = C::BM / 8 / C::kWaves;
   uint32_t off[C::kCopies];
-  int chunk_of[C::kCopies];
+  const int chunk_of = swz(lane & 7, 8 * wave + (lane >> 3));   // the same in every copy: 16 rows apart
 #pragma unroll
   for (int j = 0; j < C::kCopies; ++j) {
-    const int r = 16 * (wave + C::kWaves * j) + (lane >> 2) - (j < kCopiesA ? 0 : C::BM);
-    chunk_of[j] = swz4(lane & 3, r);
-    off[j] = r < (j < kCopiesA ? mrows : nrows) ? (uint32_t)r * pitch + 16 * chunk_of[j] : kPastEnd;
+    const int r = 8 * (wave + C::kWaves * j) + (lane >> 3) - (j < kCopiesA ? 0 : C::BM);
+    off[j] = r < (j < kCopiesA ? mrows : nrows) ? (uint32_t)r * pitch + 16 * chunk_of : kPastEnd;
   }
-  auto issue = [&](int slot, int s) {
-#pragma unroll
-    for (int j = 0; j < C::kCopies; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          j < kCopiesA ? ra : rb, (lds_void_t*)(smem + slot * C::kStageBytes + (wave + C::kWaves * j) * 1024), 16,
-          4 * s + chunk_of[j] < groups ? off[j] : kPastEnd, s < stages ? s * 64 : 0, 0, 0);
+  auto issue = [&](int slot, int s, int j) {   // copy j of stage s
+    const bool in = 8 * s + chunk_of < groups;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        j < kCopiesA ? ra : rb, (lds_void_t*)(smem + slot * C::kStageBytes + (wave + C::kWaves * j) * 1024), 16,
+        in ? off[j] : kPastEnd, s < 2 * pairs ? s * 128 : 0, 0, 0);
   };
-  // scales: kPer rows per thread, 16 bytes each
-  constexpr int kPer = C::kRows / (C::kWaves * kWave);
-  const uint8_t* srow[kPer];
+  // scales: thread t's row of the staged ones (a wave's are all A's or all B's)
+  const bool of_a = wave < C::BM / kWave;
+  const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(of_a ? as + (size_t)m0 * groups : bs + (size_t)n0 * groups), (short)0,
+      (of_a ? mrows : nrows) * groups, kRsrcWord3);
+  const uint32_t srow = (uint32_t)(of_a ? min(t, mrows - 1) : min(t - C::BM, nrows - 1)) * groups;
+  uint8_t* const sscale = smem + 2 * C::kStageBytes;
+  u32x4_t sreg;
+  // pair g's 16 bytes of the row; of a last pair that is not whole, the row's last 16
+  auto load_scales = [&](int g) { sreg = __builtin_amdgcn_raw_buffer_load_b128(rs, srow, max(min(16 * g, groups - 16), 0), 0); };
+  auto load_few_scales = [&] {   // K below 512: byte by byte, those past K as 2^0 (times zeros)
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int r = t + i * C::kWaves * kWave;
-    srow[i] = r < C::BM ? as + (size_t)(m0 + min(r, mrows - 1)) * groups
-                        : bs + (size_t)(n0 + min(r - C::BM, nrows - 1)) * groups;
-  }
-  uint8_t* const sscale = smem + kRing * C::kStageBytes;
-  u32x4_t sreg[kPer];
-  auto load_scales = [&](int g) {   // a whole group
+    for (int d = 0; d < 4; ++d) {
+      uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) __builtin_memcpy(&sreg[i], srow[i] + 16 * g, 16);
-  };
-  auto load_last_scales = [&](int g) {   // fewer than 16 blocks: the others as 2^0 (times zeros)
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        uint32_t w = 0;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int at = 16 * g + 4 * d + b;
-          w |= (at < groups ? (uint32_t)srow[i][min(at, groups - 1)] : 127u) << (8 * b);
-        }
-        sreg[i][d] = w;
+      for (int b = 0; b < 4; ++b) {
+        const int at = 4 * d + b;
+        w |= (at < groups ? (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rs, srow, at, 0) : 127u) << (8 * b);
       }
+      sreg[d] = w;
+    }
+  };
+  // moves the last 16 bytes of a row down to where its last pair starts; what
+  // follows counts as 2^0 (times zeros)
+  auto align_scales = [&](u32x4_t v) {
+    const int past = 16 * pairs - groups;   // bytes of the pair before it
+#pragma unroll
+    for (int w = 0; w < 3; ++w)
+      if (4 * w + 4 <= past) v = u32x4_t{v[1], v[2], v[3], 0x7F7F7F7Fu};
+    const uint32_t by = past & 3;
+    return u32x4_t{__builtin_amdgcn_alignbyte(v[1], v[0], by), __builtin_amdgcn_alignbyte(v[2], v[1], by),
+                   __builtin_amdgcn_alignbyte(v[3], v[2], by), __builtin_amdgcn_alignbyte(0x7F7F7F7Fu, v[3], by)};
   };
   auto store_scales = [&](int g) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      *reinterpret_cast<u32x4_t*>(sscale + (g & 1) * C::kScaleBytes + (t + i * C::kWaves * kWave) * 16) = transpose4(sreg[i]);
+    const u32x4_t v = g > 0 && 16 * g + 16 > groups ? align_scales(sreg) : sreg;
+    *reinterpret_cast<u32x4_t*>(sscale + (g & 1) * C::kScaleBytes + t * 16) = transpose4(v);
   };
 
   const int wm = wave / C::WN, wn = wave % C::WN;
@@ -200,95 +244,143 @@ __device__ __forceinline__ void matmul_tile(uint8_t* smem, const uint8_t* ac, co
 #pragma unroll
     for (int j = 0; j < C::NJ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  const int full = groups / 16;   // groups of four whole stages
-  if (full) load_scales(0);
-  else load_last_scales(0);
+  if (groups >= 16) load_scales(0);
+  else load_few_scales();
   store_scales(0);
 #pragma unroll
-  for (int d = 0; d < kRing - 1; ++d) issue(d, d);
+  for (int j = 0; j < C::kCopies; ++j) issue(0, 0, j);
 
+  // A stage has two MFMA steps of 128 K, each two lists: the wave's upper and
+  // lower row blocks.  Behind each MFMA stands a share of the LDS reads of the
+  // list after it (and, early in the stage, of the next stage's copies), so
+  // that no run of reads holds an MFMA up; the last list of a stage runs after
+  // the next stage's barrier, over that stage's first reads.  Before the first
+  // stage its operands are zeros with scales of 2^0.
+  constexpr int kHalf = C::MI / 2, kM = kHalf * C::NJ;
+  static_assert(C::MI % 2 == 0 && kM >= C::NJ + kHalf && kM >= C::kCopies, "a list has room for its reads and copies");
   uint32_t sa[C::MI], sb[C::NJ];
-  auto run_stage = [&](auto jc, int g) {
-    constexpr int j4 = decltype(jc)::value;
-    const int s = 4 * g + j4;
-    // this wave's copies of stage s have landed (two stages' copies came after
-    // them; a scale load among those only makes the wait stricter) and its
-    // LDS accesses are done; the barrier extends both to every wave
-    MOE_WAIT_VM(2 * C::kCopies);
+  u32x4_t fa[C::MI], fb[2][C::NJ];
+#pragma unroll
+  for (int i = 0; i < C::MI; ++i) {
+    fa[i] = u32x4_t{0, 0, 0, 0};
+    sa[i] = 0x7F7F7F7Fu;
+  }
+#pragma unroll
+  for (int j = 0; j < C::NJ; ++j) {
+    fb[0][j] = fb[1][j] = u32x4_t{0, 0, 0, 0};
+    sb[j] = 0x7F7F7F7Fu;
+  }
+  auto run_stage = [&](auto pc, int g) {   // stage p of pair g
+    constexpr int p = decltype(pc)::value;
+    // this wave's copies of the stage have landed and its LDS accesses are
+    // done; the barrier extends both to every wave
+    MOE_WAIT_VM(0);
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (j4 == 0 && g + 1 < full) load_scales(g + 1);
-    issue((j4 + kRing - 1) % kRing, s + kRing - 1);
-    if (j4 == 0) {
-      const uint8_t* sc = sscale + (g & 1) * C::kScaleBytes + q * 4;
+    const uint8_t* buf = smem + p * C::kStageBytes;
+    const uint8_t* sc = sscale + (g & 1) * C::kScaleBytes + q * 4;
+    unrolled<4>([&](auto hc) {
+      // list h - 1 (h = 0: the previous stage's last) over the operands of list h
+      constexpr int h = decltype(hc)::value, k = h / 2;
+      constexpr int pk = (2 * p + (h + 1) / 2 + 3) % 4;   // the step of the list that multiplies, in its pair
+      constexpr int pb = pk % 2, lo = (h + 1) % 2;
+      const uint8_t* at = buf + swz(4 * k + q, rl) * 16;
+      unrolled<kM>([&](auto mc) {
+        constexpr int m = decltype(mc)::value, i = lo * kHalf + m / C::NJ, j = m % C::NJ;
+        acc[i][j] = mfma_fp4_sel<pk>(fb[pb][j], fa[i], acc[i][j], sb[j], sa[i]);
+        if constexpr (h % 2 == 0) {          // B and the upper blocks of step k
+          if constexpr (m < C::NJ) {
+            fb[k][m] = *reinterpret_cast<const u32x4_t*>(at + (brow + 16 * m) * 128);
+          } else if constexpr (m < C::NJ + kHalf) {
+            constexpr int r = m - C::NJ;
+            fa[r] = *reinterpret_cast<const u32x4_t*>(at + (arow + 16 * r) * 128);
+            if constexpr (p == 0 && h == 0) sa[r] = *reinterpret_cast<const uint32_t*>(sc + (arow + 16 * r) * 16);
+          }
+        } else if constexpr (m < kHalf) {    // its lower blocks
+          constexpr int r = kHalf + m;
+          fa[r] = *reinterpret_cast<const u32x4_t*>(at + (arow + 16 * r) * 128);
+          if constexpr (p == 0 && h == 1) sa[r] = *reinterpret_cast<const uint32_t*>(sc + (arow + 16 * r) * 16);
+        }
+        if constexpr (h == 0 && m < C::kCopies) issue(1 - p, 2 * g + p + 1, m);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      if constexpr (p == 0 && h == 0) {
 #pragma unroll
-      for (int i = 0; i < C::MI; ++i) sa[i] = *reinterpret_cast<const uint32_t*>(sc + (arow + 16 * i) * 16);
-#pragma unroll
-      for (int j = 0; j < C::NJ; ++j) sb[j] = *reinterpret_cast<const uint32_t*>(sc + (brow + 16 * j) * 16);
-    }
-    const uint8_t* buf = smem + j4 * C::kStageBytes;
-    u32x4_t fb[C::NJ], fa[C::MI];
-#pragma unroll
-    for (int j = 0; j < C::NJ; ++j)
-      fb[j] = *reinterpret_cast<const u32x4_t*>(buf + (brow + 16 * j) * 64 + swz4(q, rl) * 16);
-#pragma unroll
-    for (int i = 0; i < C::MI; ++i)
-      fa[i] = *reinterpret_cast<const u32x4_t*>(buf + (arow + 16 * i) * 64 + swz4(q, rl) * 16);
-#pragma unroll
-    for (int i = 0; i < C::MI; ++i)
-#pragma unroll
-      for (int j = 0; j < C::NJ; ++j) acc[i][j] = mfma_fp4_sel<j4>(fb[j], fa[i], acc[i][j], sb[j], sa[i]);
-    if (j4 == 3 && g + 1 < full) store_scales(g + 1);
-    // the stage's MFMAs stay in their stage (left free, the compiler collects
-    // several stages' operands first and spills)
+        for (int j = 0; j < C::NJ; ++j) sb[j] = *reinterpret_cast<const uint32_t*>(sc + (brow + 16 * j) * 16);
+        load_scales(g + 1);
+      }
+    });
 #pragma unroll
     for (int i = 0; i < C::MI; ++i)
 #pragma unroll
       for (int j = 0; j < C::NJ; ++j) pin(acc[i][j][0]);
+    if constexpr (p == 1) store_scales(g + 1);   // after the last pair: into the half no one reads
   };
-  for (int g = 0; g < full; ++g) {
+  for (int g = 0; g < pairs; ++g) {
     run_stage(std::integral_constant<int, 0>{}, g);
     run_stage(std::integral_constant<int, 1>{}, g);
-    run_stage(std::integral_constant<int, 2>{}, g);
-    run_stage(std::integral_constant<int, 3>{}, g);
   }
-  if (4 * full < stages) {   // K is not a multiple of 512
-    if (full) {
-      load_last_scales(full);
-      store_scales(full);
-    }
-    run_stage(std::integral_constant<int, 0>{}, full);
-    if (4 * full + 1 < stages) run_stage(std::integral_constant<int, 1>{}, full);
-    if (4 * full + 2 < stages) run_stage(std::integral_constant<int, 2>{}, full);
-    if (4 * full + 3 < stages) run_stage(std::integral_constant<int, 3>{}, full);
-  }
+  unrolled<kM>([&](auto mc) {   // the last list of the last stage
+    constexpr int m = decltype(mc)::value, i = kHalf + m / C::NJ, j = m % C::NJ;
+    acc[i][j] = mfma_fp4_sel<3>(fb[1][j], fa[i], acc[i][j], sb[j], sa[i]);
+  });
   MOE_WAIT_VM(0);   // the copies past the end still write LDS
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();   // every wave is done reading the ring
+  asm volatile("" ::: "memory");
 
-  // lane holds row rl, columns 4q .. 4q + 3 of each 16 x 16 block
+  // Lane holds row rl, columns 4q .. 4q + 3 of each 16 x 16 block.  Where rows
+  // of the output are 16-byte aligned, the wave's blocks pass through its part
+  // of the ring, 32 rows at a time, and leave as whole rows of 16-byte chunks
+  // (permuted by chunk ^ row for the banks); else every element by itself.
+  constexpr int kSize = F32 ? 4 : 2, kRowBytes = C::NJ * 16 * kSize, kChunks = kRowBytes / 16;
+  constexpr int kMask = kChunks < 16 ? kChunks - 1 : 15;
+  static_assert(C::kWaves * 32 * kRowBytes <= C::kSmem && 64 % kChunks == 0, "two blocks of every wave fit");
+  const bool rows_aligned = N % (16 / kSize) == 0;
+  uint8_t* const stg = smem + wave * (32 * kRowBytes);
+  const int mw = wm * (16 * C::MI), nw = wn * (16 * C::NJ);
+  if (rows_aligned) {
 #pragma unroll
-  for (int i = 0; i < C::MI; ++i) {
-    const int m = wm * (16 * C::MI) + 16 * i + rl;
-    if (m >= mrows) continue;
+    for (int i = 0; i < C::MI; i += 2) {
 #pragma unroll
-    for (int j = 0; j < C::NJ; ++j) {
-      const int n = wn * (16 * C::NJ) + 16 * j + 4 * q;
-      const size_t at = (size_t)(m0 + m) * N + n0 + n;
-      if (!F32 && N % 4 == 0) {
-        if (n < nrows)
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
-              make_uint2(f32_to_bf16_rne(acc[i][j][0]) | ((uint32_t)f32_to_bf16_rne(acc[i][j][1]) << 16),
-                         f32_to_bf16_rne(acc[i][j][2]) | ((uint32_t)f32_to_bf16_rne(acc[i][j][3]) << 16));
-      } else {
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (n + e >= nrows) break;
-          if (F32) static_cast<float*>(out)[at + e] = acc[i][j][e];
-          else static_cast<uint16_t*>(out)[at + e] = f32_to_bf16_rne(acc[i][j][e]);
+        for (int j = 0; j < C::NJ; ++j) {
+          const f32x4_t v = acc[i + h][j];
+          uint8_t* const at = stg + (16 * h + rl) * kRowBytes;
+          if constexpr (F32)
+            *reinterpret_cast<f32x4_t*>(at + ((4 * j + q) ^ (rl & kMask)) * 16) = v;
+          else
+            *reinterpret_cast<uint2*>(at + ((2 * j + (q >> 1)) ^ (rl & kMask)) * 16 + 8 * (q & 1)) =
+                make_uint2(f32_to_bf16_rne(v[0]) | ((uint32_t)f32_to_bf16_rne(v[1]) << 16),
+                           f32_to_bf16_rne(v[2]) | ((uint32_t)f32_to_bf16_rne(v[3]) << 16));
         }
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int k = 0; k < kChunks / 2; ++k) {   // 64 / kChunks rows at a time
+        const int r = k * (64 / kChunks) + lane / kChunks, c = lane % kChunks;
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(stg + r * kRowBytes + ((c ^ (r & kMask)) * 16));
+        const int m = mw + 16 * i + r, n = nw + c * (16 / kSize);
+        if (m < mrows && n < nrows)
+          *reinterpret_cast<u32x4_t*>(static_cast<uint8_t*>(out) + ((size_t)(m0 + m) * N + n0 + n) * kSize) = v;
       }
+      asm volatile("" ::: "memory");
     }
+    return;
   }
+#pragma unroll
+  for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+    for (int j = 0; j < C::NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int m = mw + 16 * i + rl, n = nw + 16 * j + 4 * q + e;
+        if (m >= mrows || n >= nrows) continue;
+        const size_t at = (size_t)(m0 + m) * N + n0 + n;
+        if constexpr (F32) static_cast<float*>(out)[at] = acc[i][j][e];
+        else static_cast<uint16_t*>(out)[at] = f32_to_bf16_rne(acc[i][j][e]);
+      }
 }
 
 template <class C, bool F32>
@@ -312,16 +404,46 @@ hipError_t launch_tiles(const uint8_t* ac, const uint8_t* as, const uint8_t* bc,
 }
 
 using Mx256 = MxShape<256, 256, 2, 4>;
+using Mx128 = MxShape<128, 128, 2, 2>;
+
+template <int MT>
+hipError_t launch_rows(const uint8_t* ac, const uint8_t* as, const uint8_t* bc, const uint8_t* bs, int M, int N, int K,
+                       bool f32, void* out, hipStream_t stream) {
+  const dim3 grid((N + 15) / 16, (M + 16 * MT - 1) / (16 * MT)), block(kSplit * kWave);
+  if (f32)
+    hipLaunchKernelGGL((matmul_mxfp4_rows<MT, true>), grid, block, 0, stream, ac, as, bc, bs, M, N, K / 32, out);
+  else
+    hipLaunchKernelGGL((matmul_mxfp4_rows<MT, false>), grid, block, 0, stream, ac, as, bc, bs, M, N, K / 32, out);
+  return hipGetLastError();
+}
 
 }  // namespace
 
 hipError_t launch_mxfp4_matmul(const uint8_t* ac, const uint8_t* as, const uint8_t* bc, const uint8_t* bs, int M, int N,
                                int K, bool f32, void* out, hipStream_t stream) {
-  if (M > 128) return launch_tiles<Mx256>(ac, as, bc, bs, M, N, K, f32, out, stream);
-  const dim3 grid((N + 15) / 16, (M + 15) / 16);
-  if (f32) hipLaunchKernelGGL(matmul_mxfp4<true>, grid, dim3(kSplit * kWave), 0, stream, ac, as, bc, bs, M, N, K / 32, out);
-  else hipLaunchKernelGGL(matmul_mxfp4<false>, grid, dim3(kSplit * kWave), 0, stream, ac, as, bc, bs, M, N, K / 32, out);
-  return hipGetLastError();
+  // Row blocks per workgroup of the streaming kernel: the fewest whose
+  // workgroups still fit one to a CU (K 7168 to 4096 columns, 32 rows: 14.5,
+  // 11.3, 12.9 us with 1, 2, 4; K 4096 to 512, 64 rows: 5.5, 7.3, 10.9).
+  const int nb = (N + 15) / 16, mb = (M + 15) / 16;
+  const int mt = mb == 1 || nb * mb <= 256 ? 1 : mb == 2 || nb * ((mb + 1) / 2) <= 256 ? 2 : 4;
+  // It reads mt + 1 row blocks of K/2 bytes per workgroup from the L2s at about
+  // 4.6 TB/s; up to 256 tiles of 128 x 128 take about 5 us and 0.45 us per 256
+  // K.  The two meet where the count below does (K 7168 to 4096 columns: 48
+  // rows 15.7 against 17.9 us, 96 rows 29.2 against 18.3; K 2048 to 7168: 32
+  // rows 7.5 against 8.5, 48 rows 10.5 against 8.8).
+  const long long blocks = (long long)nb * ((mb + mt - 1) / mt) * (mt + 1);
+  if (blocks <= 1100 + 1600000 / K) {
+    if (mt == 1) return launch_rows<1>(ac, as, bc, bs, M, N, K, f32, out, stream);
+    if (mt == 2) return launch_rows<2>(ac, as, bc, bs, M, N, K, f32, out, stream);
+    return launch_rows<4>(ac, as, bc, bs, M, N, K, f32, out, stream);
+  }
+  // 256 x 256 once they fill most of the 256 CUs: half the copies per product
+  // (K 7168 to 4096 columns: 2048 rows, 128 large tiles, 49 against 43 us;
+  // 4096 rows, 256 of them, 62 against 84; K 2048 to 7168: 2048 rows, 224 of
+  // them, 24.4 against 28.9).
+  if ((long long)((M + 255) / 256) * ((N + 255) / 256) >= 192)
+    return launch_tiles<Mx256>(ac, as, bc, bs, M, N, K, f32, out, stream);
+  return launch_tiles<Mx128>(ac, as, bc, bs, M, N, K, f32, out, stream);
 }
 
 }  // namespace moe
