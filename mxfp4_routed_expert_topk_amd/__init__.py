@@ -345,8 +345,8 @@ def _need_shape(t, name: str, dtype, shape, like):
     """Raise MoeError(MOE_ERR_ARG) unless `t` is a contiguous tensor of `dtype`
     and exactly `shape` on the device of the tensor `like`."""
     import torch
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == like.device \
-            and t.is_contiguous():
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape \
+            and t.get_device() == like.get_device() and t.is_contiguous():
         return
     if not isinstance(t, torch.Tensor):
         raise _arg_error(f"{name} must be a torch.Tensor, got {type(t).__name__}")
@@ -369,7 +369,7 @@ def _rows(t, name: str, dtypes, cols: Optional[int], like):
         raise _arg_error(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
         raise _arg_error(f"{name} must be [rows, {'cols' if cols is None else cols}], got shape {tuple(t.shape)}")
-    if like is not None and t.device != like.device:
+    if like is not None and t.get_device() != like.get_device():
         raise _arg_error(f"{name} must be on {like.device}, got {t.device}")
     if t.is_contiguous():
         return t.shape[1]
@@ -381,16 +381,16 @@ def _rows(t, name: str, dtypes, cols: Optional[int], like):
 
 def _apart(out, name: str, *inputs):
     """Raise MoeError(MOE_ERR_ARG) if the memory of the contiguous `out` and of
-    an input overlap; inputs are given as (name, tensor), with their strides
-    descending."""
+    an input overlap; inputs are given as (name, tensor), each contiguous or a
+    matrix of contiguous rows."""
     lo = out.data_ptr()
-    hi = lo + out.numel() * out.element_size()
+    hi = lo + out.nbytes
     for other, t in inputs:
         at = t.data_ptr()
-        if at >= hi or lo == hi or t.numel() == 0:
-            continue
-        if at + ((t.shape[0] - 1) * t.stride(0) + t[0].numel()) * t.element_size() > lo:
-            raise _arg_error(f"{name} must not overlap {other}")
+        if at < hi and at + t.nbytes > lo or at < lo and not t.is_contiguous() and t.numel() and \
+                at + ((t.shape[0] - 1) * t.stride(0) + t.shape[1]) * t.element_size() > lo:
+            if lo != hi and t.numel():
+                raise _arg_error(f"{name} must not overlap {other}")
 
 
 def _new(shape, dtype, like, stream):
@@ -408,19 +408,18 @@ def _launch(fn, args, like, stream, tensors):
     device, with that device current.  On a given stream the tensors' memory is
     kept from other use until the stream has passed this point."""
     import torch
-    device = like.device
-    if device.type != "cuda":
-        raise _arg_error(f"tensors must be on a GPU, got {device}")
-    index = device.index
+    index = like.get_device()
+    if index < 0:
+        raise _arg_error(f"tensors must be on a GPU, got {like.device}")
     if stream is None:
         # the address behind torch.cuda.current_stream(index), without the
         # 2.7 us of building the Stream object
         at = torch._C._cuda_getCurrentRawStream(index)
-    elif stream.device != device:
-        raise _arg_error(f"stream is of {stream.device}, the tensors are on {device}")
+    elif stream.device != like.device:
+        raise _arg_error(f"stream is of {stream.device}, the tensors are on {like.device}")
     else:
         at = stream.cuda_stream
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         status = fn(*args, at)
     else:
         with torch.cuda.device(index):
@@ -457,16 +456,17 @@ def mxfp4_quantize(x, codes=None, scales=None, stream=None):
     return codes, scales
 
 
-def _mxfp4_operand(codes, scales, name: str, like):
+def _mxfp4_operand(codes, scales, codes_name: str, scales_name: str, like):
     """(rows, K) of an MXFP4 operand, its tensors checked."""
     import torch
     if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
-        raise _arg_error(f"{name}codes must be a 2-D torch.Tensor [rows, cols/2]")
-    rows, half = codes.shape
-    _need_shape(codes, f"{name}codes", torch.uint8, (rows, half), codes if like is None else like)
+        raise _arg_error(f"{codes_name} must be a 2-D torch.Tensor [rows, cols/2]")
+    shape = codes.shape
+    rows, half = shape
+    _need_shape(codes, codes_name, torch.uint8, shape, like)
     if half == 0 or half % 16:
-        raise MoeError(MOE_ERR_SHAPE, f"{name}codes must have a positive multiple of 16 columns, got {half}")
-    _need_shape(scales, f"{name}scales", torch.uint8, (rows, half // 16), codes)
+        raise MoeError(MOE_ERR_SHAPE, f"{codes_name} must have a positive multiple of 16 columns, got {half}")
+    _need_shape(scales, scales_name, torch.uint8, (rows, half // 16), like)
     return rows, 2 * half
 
 
@@ -475,8 +475,10 @@ def _float_out(out, name: str, shape, dtype, like, stream, *inputs):
     one checked against shape, dtype and the inputs' memory."""
     import torch
     if out is None:
-        dtype = torch.bfloat16 if dtype is None else dtype
-        code = _dtype_code(dtype, f"{name}_dtype" if name != "out" else "dtype")
+        if dtype is None:
+            dtype, code = torch.bfloat16, MOE_BF16
+        else:
+            code = _dtype_code(dtype, "dtype" if name == "out" else name + "_dtype")
         return _new(shape, dtype, like, stream), code
     code = _dtype_code(getattr(out, "dtype", None) if dtype is None else dtype, name)
     _need_shape(out, name, out.dtype if dtype is None else dtype, shape, like)
@@ -487,7 +489,7 @@ def _float_out(out, name: str, shape, dtype, like, stream, *inputs):
 def mxfp4_dequantize(codes, scales, dtype=None, out=None, stream=None):
     """The values [rows, cols] that codes [rows, cols/2] and scales [rows, cols/32]
     stand for, in bf16 (default) or fp32, exact (moe_mxfp4_dequantize)."""
-    rows, cols = _mxfp4_operand(codes, scales, "", None)
+    rows, cols = _mxfp4_operand(codes, scales, "codes", "scales", codes)
     out, code = _float_out(out, "out", (rows, cols), dtype, codes, stream, ("codes", codes), ("scales", scales))
     _launch(load_library().moe_mxfp4_dequantize,
             (codes.data_ptr(), scales.data_ptr(), rows, cols, code, out.data_ptr()), codes, stream,
@@ -498,8 +500,8 @@ def mxfp4_dequantize(codes, scales, dtype=None, out=None, stream=None):
 def mxfp4_matmul(a_codes, a_scales, b_codes, b_scales, dtype=None, out=None, stream=None):
     """A B^T [m, n] of two MXFP4 matrices A [m, k] and B [n, k], summed in fp32 and
     rounded once to bf16 (default) or left in fp32 (moe_mxfp4_matmul)."""
-    m, k = _mxfp4_operand(a_codes, a_scales, "a_", None)
-    n, kb = _mxfp4_operand(b_codes, b_scales, "b_", a_codes)
+    m, k = _mxfp4_operand(a_codes, a_scales, "a_codes", "a_scales", a_codes)
+    n, kb = _mxfp4_operand(b_codes, b_scales, "b_codes", "b_scales", a_codes)
     if kb != k:
         raise MoeError(MOE_ERR_SHAPE, f"A has {k} columns and B {kb}")
     out, code = _float_out(out, "out", (m, n), dtype, a_codes, stream, ("a_codes", a_codes), ("a_scales", a_scales),

@@ -69,7 +69,8 @@ __device__ __forceinline__ s16x4_t read_crossed(const uint8_t* __restrict__ p) {
 // One operand's tile of B rows (plain) or columns (crossed), `count` of them
 // live, over `length` of the reduction; `base` is its first element and `ld`
 // the elements from one memory row to the next.
-template <bool CROSSED, int B, int WAVES, int STEP>
+// NT: read past the caches.
+template <bool CROSSED, int B, int WAVES, int STEP, bool NT>
 struct Operand {
   static constexpr int kBytes = B * STEP * 2;
   static constexpr int kCopies = kBytes / 1024 / WAVES;   // copies per wave and stage
@@ -109,7 +110,7 @@ struct Operand {
     const __amdgpu_buffer_rsrc_t r =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + skip), (short)0, kMaxRange, kRsrcWord3);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)(buf + (wave + WAVES * j) * 1024), 16,
-                                             red[j] + s * STEP < length ? off[j] : kPastEnd, 0, 0, 0);
+                                             red[j] + s * STEP < length ? off[j] : kPastEnd, 0, 0, NT ? 2 : 0);
   }
 
   // MFMA operand of 32-row block b, 16-deep step k, from a staged tile
@@ -192,9 +193,11 @@ struct RowTiles {
 // W waves as WM x WN.  A wave's 32-row blocks are every WM-th one, so that the
 // blocks past a tile's last row, which are skipped, are spread over the waves;
 // its 32-column blocks lie side by side.
-// NP and NQ tiles of the rings; PER_CU workgroups fit a CU.
-template <int BM_, int BN_, int WM_, int WN_, int STEP_, int NP_, int NQ_, int PER_CU_>
+// NP and NQ tiles of the rings; PER_CU workgroups fit a CU.  NT: Q is read by
+// one workgroup only and passes the caches by.
+template <int BM_, int BN_, int WM_, int WN_, int STEP_, int NP_, int NQ_, int PER_CU_, bool NT_ = false>
 struct Shape {
+  static constexpr bool NT = NT_;
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STEP = STEP_, NP = NP_, NQ = NQ_;
   static constexpr int kWaves = WM * WN, kPerCU = PER_CU_;
   static constexpr int MI = BM / WM / 32, NJ = BN / WN / 32;
@@ -205,11 +208,11 @@ struct Shape {
 // The K loop over a wave's first LIVE row blocks.
 template <class C, bool PX, bool QX, int LIVE>
 struct Reduce {
-  static __device__ __forceinline__ void run(uint8_t* smem, const Operand<PX, C::BM, C::kWaves, C::STEP>& op,
-                                             const Operand<QX, C::BN, C::kWaves, C::STEP>& oq, int stages, int wm, int wn,
+  static __device__ __forceinline__ void run(uint8_t* smem, const Operand<PX, C::BM, C::kWaves, C::STEP, false>& op,
+                                             const Operand<QX, C::BN, C::kWaves, C::STEP, C::NT>& oq, int stages, int wm, int wn,
                                              int lane, f32x16_t (&acc)[C::MI][C::NJ]) {
-    using P = Operand<PX, C::BM, C::kWaves, C::STEP>;
-    using Q = Operand<QX, C::BN, C::kWaves, C::STEP>;
+    using P = Operand<PX, C::BM, C::kWaves, C::STEP, false>;
+    using Q = Operand<QX, C::BN, C::kWaves, C::STEP, C::NT>;
     constexpr int kG = P::kCopies + Q::kCopies;
     // Stage s issues P of stage s + NP - 1 and Q of stage s + NQ - 1 into the
     // tiles that stage s - 1 has read; the stages before 0 fill the rings.
@@ -293,8 +296,8 @@ template <class C, bool PX, bool QX, bool F32, bool STREAM>
 __device__ __forceinline__ void tile_product(uint8_t* smem, const uint16_t* p, long long ldp, const uint16_t* q,
                                              long long ldq, int rows, int cols, int length, void* out, long long ldo) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  using P = Operand<PX, C::BM, C::kWaves, C::STEP>;
-  using Q = Operand<QX, C::BN, C::kWaves, C::STEP>;
+  using P = Operand<PX, C::BM, C::kWaves, C::STEP, false>;
+  using Q = Operand<QX, C::BN, C::kWaves, C::STEP, C::NT>;
   const P op(p, ldp, rows, length, wave, lane);
   const Q oq(q, ldq, cols, length, wave, lane);
   const int wm = wave / C::WN, wn = wave % C::WN;
@@ -307,7 +310,7 @@ __device__ __forceinline__ void tile_product(uint8_t* smem, const uint16_t* p, l
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-  static_assert(C::MI == 2 || C::MI == 4, "cases below");
+  static_assert(C::MI == 1 || C::MI == 2 || C::MI == 4, "cases below");
   const int blocks = (rows + 31) / 32, live = (blocks - wm + C::WM - 1) / C::WM;   // this wave's
   if (live >= C::MI) Reduce<C, PX, QX, C::MI>::run(smem, op, oq, stages, wm, wn, lane, acc);
   else if (C::MI > 3 && live == 3) Reduce<C, PX, QX, C::MI - 1>::run(smem, op, oq, stages, wm, wn, lane, acc);
@@ -451,20 +454,23 @@ long long items_per_xcd(const GroupedArgs& a, int bm, const Deal& d) {
   return ((long long)a.rows / bm + std::min(a.groups, a.rows) + turns - 1) / turns * d.share;
 }
 
-#ifndef ROWS_SHAPE
-#define ROWS_SHAPE 256, 256, 2, 4, 64, 2, 3, 1
-#endif
-#ifndef DW_SHAPE
-#define DW_SHAPE 256, 256, 2, 4, 64, 2, 3, 1
-#endif
-using RowsShape = Shape<ROWS_SHAPE>;
-using DwShape = Shape<DW_SHAPE>;
+using Large = Shape<256, 256, 2, 4, 64, 2, 3, 1>;
+template <bool NT>
+using Middle = Shape<128, 128, 2, 2, 64, 2, 3, 2, NT>;
+template <bool NT>
+using Small = Shape<64, 128, 1, 4, 64, 3, 3, 2, NT>;
 
-}  // namespace
+// items there will be, about: half the groups end in a partial tile
+template <class C>
+long long items(const GroupedArgs& a, int cols) {
+  return ((long long)a.rows / C::BM + (std::min(a.groups, a.rows) + 1) / 2) * ((cols + C::BN - 1) / C::BN);
+}
 
-hipError_t launch_grouped_forward(const GroupedArgs& a, const void* x, int64_t ldx, void* y, hipStream_t stream) {
-  using C = RowsShape;
-  const Deal d = deal((a.n + C::BN - 1) / C::BN);
+template <class C>
+hipError_t launch_forward(const GroupedArgs& a, const void* x, int64_t ldx, void* y, hipStream_t stream) {
+  // a weight read once is best read beside its neighbours: one share
+  const int slices = (a.n + C::BN - 1) / C::BN;
+  const Deal d = C::NT ? Deal{slices, 1, slices} : deal(slices);
   hipLaunchKernelGGL((grouped_forward<C>), dim3((unsigned)(items_per_xcd(a, C::BM, d) * kXcds)),
                      dim3(C::kWaves * kWave), 0, stream, static_cast<const uint16_t*>(x), ldx,
                      static_cast<const uint16_t*>(a.w), a.offsets, a.rows, a.groups, a.n, a.k, d,
@@ -472,17 +478,15 @@ hipError_t launch_grouped_forward(const GroupedArgs& a, const void* x, int64_t l
   return hipGetLastError();
 }
 
-hipError_t launch_grouped_backward(const GroupedArgs& a, const void* dy, int64_t lddy, const void* x, int64_t ldx,
-                                   void* dx, bool f32, void* dw, hipStream_t stream) {
-  using C = DwShape;
-  BackwardArgs b{static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(a.w),
-                 lddy, ldx, a.offsets, a.rows, a.groups, a.n, a.k, static_cast<uint16_t*>(dx), dw, deal((a.k + C::BN - 1) / C::BN), 0, 0};
-  if (dx) b.dx_items = (int)items_per_xcd(a, C::BM, b.dx_deal);
-  if (dw)
-    b.dw_items = (int)(((long long)a.groups * ((a.n + C::BM - 1) / C::BM) * ((a.k + C::BN - 1) / C::BN) + kXcds - 1) / kXcds);
+template <class C>
+hipError_t launch_backward(const GroupedArgs& a, BackwardArgs b, bool f32, hipStream_t stream) {
+  b.dx_deal = deal((a.k + C::BN - 1) / C::BN);
+  b.dx_items = b.dx ? (int)items_per_xcd(a, C::BM, b.dx_deal) : 0;
+  const long long dw_tiles = (long long)a.groups * ((a.n + C::BM - 1) / C::BM) * ((a.k + C::BN - 1) / C::BN);
+  b.dw_items = b.dw ? (int)((dw_tiles + kXcds - 1) / kXcds) : 0;
   if (b.dx_items + b.dw_items == 0) return hipSuccess;
   // dw beyond the L2s' 32 MB leaves nothing there to read again and would
-  // push dy and x out: streamed
+  // push dy and x out: streamed (3.76 GB: 1259 -> 1091 us)
   const bool stream_out = (size_t)a.groups * a.n * a.k * (f32 ? 4 : 2) > kL2Bytes;
   auto run = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)(b.dx_items + b.dw_items) * kXcds), dim3(C::kWaves * kWave), 0, stream, b);
@@ -490,6 +494,39 @@ hipError_t launch_grouped_backward(const GroupedArgs& a, const void* dy, int64_t
   if (f32) run(stream_out ? grouped_backward<C, true, true> : grouped_backward<C, true, false>);
   else run(stream_out ? grouped_backward<C, false, true> : grouped_backward<C, false, false>);
   return hipGetLastError();
+}
+
+}  // namespace
+
+// Tile by the rows a group has on average (64 groups, 7168 -> 4096, us with
+// 64-, 128- and 256-row tiles): few rows stream the weights, which two
+// workgroups per CU, non-temporal, do best (16 rows each: 552, 557, 615; at 224
+// groups of 2.7 rows, 2048 -> 7168: 927, 978, 1165), but a group of more rows
+// than a tile reads them again (32 rows each 574, 577, 625, Zipf-skewed 734,
+// 668, 709; 64 each 905, 624, 655, skewed 995, 809, 728; 128 each 1572, 944,
+// 729).  Grids that would leave CUs idle take the next smaller tile (600 rows
+// in 8 groups, 768 -> 1024: 9.4, 10.9, 14.2).
+hipError_t launch_grouped_forward(const GroupedArgs& a, const void* x, int64_t ldx, void* y, hipStream_t stream) {
+  const long long rows = a.rows;
+  if (rows <= 16LL * a.groups) return launch_forward<Small<true>>(a, x, ldx, y, stream);
+  if (rows <= 40LL * a.groups && items<Middle<true>>(a, a.n) >= 256)
+    return launch_forward<Middle<true>>(a, x, ldx, y, stream);
+  if (rows > 40LL * a.groups && items<Large>(a, a.n) >= 256) return launch_forward<Large>(a, x, ldx, y, stream);
+  if (items<Middle<false>>(a, a.n) >= 256) return launch_forward<Middle<false>>(a, x, ldx, y, stream);
+  return launch_forward<Small<false>>(a, x, ldx, y, stream);
+}
+
+// 256 x 256 tiles where they fill the CUs (32 groups of 384 rows, 4096 x 7168:
+// 2000 us against 2575 with 128 x 128), else 128 x 128 (8 groups of 75 rows,
+// 768 x 1024: 22.4 against 13.7).
+hipError_t launch_grouped_backward(const GroupedArgs& a, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                   void* dx, bool f32, void* dw, hipStream_t stream) {
+  const BackwardArgs b{static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(x),
+                       static_cast<const uint16_t*>(a.w), lddy, ldx, a.offsets, a.rows, a.groups, a.n, a.k,
+                       static_cast<uint16_t*>(dx), dw, {}, 0, 0};
+  const long long dw_tiles = (long long)a.groups * ((a.n + 255) / 256) * ((a.k + 255) / 256);
+  const bool large = dw ? dw_tiles >= 256 : items<Large>(a, a.k) >= 256 && a.rows > 40LL * a.groups;
+  return large ? launch_backward<Large>(a, b, f32, stream) : launch_backward<Middle<false>>(a, b, f32, stream);
 }
 
 }  // namespace moe

@@ -135,7 +135,8 @@ def mx_operand(rng, rows, k, low=126, high=129):
 
 MATMUL_SIZES = [(1, 1, 32), (1, 16, 64), (2, 17, 96), (16, 16, 128), (17, 33, 160), (1, 4096, 1024), (5, 100, 2048),
                 (33, 257, 288), (64, 64, 512), (65, 130, 544), (128, 128, 256), (130, 250, 1056), (256, 256, 768),
-                (257, 511, 800), (300, 1000, 2048), (513, 264, 4096), (700, 300, 96), (1, 129, 4128), (37, 384, 1376)]
+                (257, 511, 800), (300, 1000, 2048), (513, 264, 4096), (700, 300, 96), (1, 129, 4128), (37, 384, 1376),
+                (3585, 3601, 160), (3401, 3704, 1056)]
 
 
 @pytest.mark.parametrize("m,n,k", MATMUL_SIZES)
@@ -217,6 +218,11 @@ GROUPED = [   # counts, n, k, rows before and behind the groups
     ([2] * 70, 72, 96, 0, 0),
     ([1, 0] * 64 + [9], 128, 64, 0, 2),
     ([513, 40], 520, 1032, 0, 7),
+    # enough columns for every tile shape: 256 rows forward, 128 with few rows a group, 128 with many
+    ([300, 0, 257], 16392, 72, 0, 3),
+    ([20] * 10, 5512, 136, 1, 1),
+    ([100, 60], 16392, 40, 0, 0),
+    ([130, 0, 7, 260, 33], 2000, 1800, 2, 2),   # 256 x 256 tiles backward
 ]
 
 
