@@ -47,7 +47,6 @@ typedef __attribute__((address_space(3))) void lds_void_t;
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 
 constexpr uint32_t kPastEnd = 0x80000000u;     // beyond every buffer resource below
-constexpr size_t kL2Bytes = 32u << 20;         // eight of 4 MB
 constexpr int kMaxRange = 0x7FFFFFFF;          // bytes a resource covers
 
 // vmcnt <= n and lgkmcnt 0

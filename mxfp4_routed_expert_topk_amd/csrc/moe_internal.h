@@ -42,6 +42,7 @@ constexpr int kMaxTopK = 32;          // largest top-k a plan accepts
 // Work counters of the prefill FC kernels: one per XCD chunk of the work list,
 // eight for FC1 then eight for FC2.
 constexpr int kXcds = 8;
+constexpr size_t kL2Bytes = 32u << 20;   // the XCDs' L2s, 4 MB each
 constexpr int kSchedCounters = 2 * kXcds;
 
 struct MatLayout {

@@ -110,7 +110,7 @@ def test_quantize_rows_of_a_wider_matrix(dtype, pad):
 
 
 @pytest.mark.parametrize("dtype", [BF, torch.float32])
-@pytest.mark.parametrize("rows,cols", [(1, 32), (8, 256), (333, 2048)])
+@pytest.mark.parametrize("rows,cols", [(1, 32), (8, 256), (333, 2048), (2080, 8192)])
 def test_dequantize_is_exact(rows, cols, dtype):
     """Every byte 0..255 occurs: 0 is 2^-127, 254 overflows for codes 4 and 6, 255 is NaN."""
     rng = np.random.default_rng(rows)
