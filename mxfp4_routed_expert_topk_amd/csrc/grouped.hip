@@ -46,6 +46,7 @@ typedef short s16x8_t __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void lds_void_t;
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 
+constexpr int kCusPerXcd = 32;
 constexpr uint32_t kPastEnd = 0x80000000u;     // beyond every buffer resource below
 constexpr int kMaxRange = 0x7FFFFFFF;          // bytes a resource covers
 
@@ -81,35 +82,41 @@ struct Operand {
   long long ld;
   int length;
   int wave;
-  uint32_t off[kCopies];   // byte offset of this lane's chunk at stage 0 (kPastEnd: not live)
-  int red[kCopies];        // reduction index of its first value at stage 0
+  // Copies of a wave lie 8 kRows or more staged rows apart, so a lane's chunk is
+  // the same in all of them.  Plain: each copy has its own memory row; crossed:
+  // the same columns of rows that lie kApart apart.
+  static constexpr int kPerRow = CROSSED ? kChunks : STEP / 8;   // chunks per staged row
+  static constexpr int kRows = 64 / kPerRow;                     // staged rows per copy
+  static constexpr int kApart = kRows * WAVES;
+  static_assert(kApart % 16 == 0 || (CROSSED && kApart % 4 == 0) || kCopies == 1, "the permutation repeats");
+  static constexpr int kOffs = CROSSED ? 1 : kCopies;
+  uint32_t off[kOffs];     // byte offset of this lane's chunk at stage 0 (kPastEnd: not live)
+  int red;                 // reduction index of its first value at stage 0 (of copy 0)
 
   __device__ __forceinline__ Operand(const uint16_t* b, long long l, int count, int len, int w, int lane)
       : base(b), ld(l), length(len), wave(w) {
+    const int r = kRows * wave + lane / kPerRow;
+    if constexpr (CROSSED) {
+      const int c = (lane % kPerRow) ^ ((r & 3) << 2);
+      red = r;
+      off[0] = 8 * c < count ? (uint32_t)((long long)r * ld * 2) + 16 * c : kPastEnd;
+    } else {
+      const int c = swz<STEP>(lane % kPerRow, r);
+      red = 8 * c;
 #pragma unroll
-    for (int j = 0; j < kCopies; ++j) {
-      const int i = wave + WAVES * j;
-      if constexpr (!CROSSED) {
-        constexpr int kPerRow = STEP / 8;     // chunks
-        const int r = 64 / kPerRow * i + lane / kPerRow, c = swz<STEP>(lane % kPerRow, r);
-        red[j] = 8 * c;
-        off[j] = r < count ? (uint32_t)((long long)r * ld * 2) + 16 * c : kPastEnd;
-      } else {
-        constexpr int kRows = 64 / kChunks;   // staged rows per copy
-        const int r = kRows * i + lane / kChunks, c = (lane % kChunks) ^ ((r & 3) << 2);
-        red[j] = r;
-        off[j] = 8 * c < count ? (uint32_t)((long long)r * ld * 2) + 16 * c : kPastEnd;
-      }
+      for (int j = 0; j < kCopies; ++j)
+        off[j] = r + kApart * j < count ? (uint32_t)((long long)(r + kApart * j) * ld * 2) + 16 * c : kPastEnd;
     }
   }
 
   // copy j of stage s into `buf`
   __device__ __forceinline__ void issue(uint8_t* buf, int s, int j) const {
-    const long long skip = (long long)s * STEP * (CROSSED ? ld : 1);
+    const long long skip = CROSSED ? ((long long)s * STEP + kApart * j) * ld : (long long)s * STEP;
     const __amdgpu_buffer_rsrc_t r =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + skip), (short)0, kMaxRange, kRsrcWord3);
+    const int at = red + s * STEP + (CROSSED ? kApart * j : 0);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)(buf + (wave + WAVES * j) * 1024), 16,
-                                             red[j] + s * STEP < length ? off[j] : kPastEnd, 0, 0, NT ? 2 : 0);
+                                             at < length ? off[CROSSED ? 0 : j] : kPastEnd, 0, 0, NT ? 2 : 0);
   }
 
   // MFMA operand of 32-row block b, 16-deep step k, from a staged tile
@@ -204,24 +211,40 @@ struct Shape {
   static_assert(NQ >= NP && NP >= 2 && kPerCU * kSmem <= 160 * 1024, "rings fit");
 };
 
-// The K loop over a wave's first LIVE row blocks.
-template <class C, bool PX, bool QX, int LIVE>
-struct Reduce {
-  static __device__ __forceinline__ void run(uint8_t* smem, const Operand<PX, C::BM, C::kWaves, C::STEP, false>& op,
-                                             const Operand<QX, C::BN, C::kWaves, C::STEP, C::NT>& oq, int stages, int wm, int wn,
-                                             int lane, f32x16_t (&acc)[C::MI][C::NJ]) {
-    using P = Operand<PX, C::BM, C::kWaves, C::STEP, false>;
-    using Q = Operand<QX, C::BN, C::kWaves, C::STEP, C::NT>;
-    constexpr int kG = P::kCopies + Q::kCopies;
-    // Stage s issues P of stage s + NP - 1 and Q of stage s + NQ - 1 into the
-    // tiles that stage s - 1 has read; the stages before 0 fill the rings.
-    uint8_t* const ring_q = smem;
+// The operands of a tile in shape C.
+template <class C, bool PX, bool QX>
+struct Operands {
+  using P = Operand<PX, C::BM, C::kWaves, C::STEP, false>;
+  using Q = Operand<QX, C::BN, C::kWaves, C::STEP, C::NT>;
+  P p;
+  Q q;
+  // Stage s issues P of stage s + NP - 1 and Q of stage s + NQ - 1 into the
+  // tiles that stage s - 1 has read; the stages before 0 fill the rings.
+  __device__ __forceinline__ void fill(uint8_t* smem) const {
     uint8_t* const ring_p = smem + C::NQ * Q::kBytes;
     unrolled<C::NQ - 1>([&](auto d) {
       constexpr int v = decltype(d)::value, sp = v - (C::NQ - C::NP);
-      if constexpr (sp >= 0) unrolled<P::kCopies>([&](auto c) { op.issue(ring_p + sp * P::kBytes, sp, c); });
-      unrolled<Q::kCopies>([&](auto c) { oq.issue(ring_q + v * Q::kBytes, v, c); });
+      if constexpr (sp >= 0) unrolled<P::kCopies>([&](auto c) { p.issue(ring_p + sp * P::kBytes, sp, c); });
+      unrolled<Q::kCopies>([&](auto c) { q.issue(smem + v * Q::kBytes, v, c); });
     });
+  }
+};
+
+// Stores of a full tile's epilogue that a K loop's first wait may leave in
+// flight (they follow the fill it waits for).
+constexpr int kLater = 32;
+
+// The K loop over a wave's first LIVE row blocks, the rings filled.  later: the
+// wave has issued kLater stores or more since the fill.
+template <class C, bool PX, bool QX, int LIVE>
+struct Reduce {
+  static __device__ __forceinline__ void run(uint8_t* smem, const Operands<C, PX, QX>& o, int stages, int wm, int wn,
+                                             int lane, bool later, f32x16_t (&acc)[C::MI][C::NJ]) {
+    using P = typename Operands<C, PX, QX>::P;
+    using Q = typename Operands<C, PX, QX>::Q;
+    constexpr int kG = P::kCopies + Q::kCopies;
+    uint8_t* const ring_q = smem;
+    uint8_t* const ring_p = smem + C::NQ * Q::kBytes;
 
     // A stage has STEP / 16 steps, each a list of LIVE x NJ MFMAs.  Behind
     // each MFMA stands a share of the LDS reads of the step after it and of
@@ -245,7 +268,9 @@ struct Reduce {
       // this wave's copies of stage s have landed (what was issued after them
       // may be in flight) and its reads of stage s - 1 are done; the barrier
       // extends both to every wave
-      MOE_WAIT_VM((C::NP - 2) * kG + (C::NQ > C::NP ? Q::kCopies : 0));
+      constexpr int kAfter = (C::NP - 2) * kG + (C::NQ > C::NP ? Q::kCopies : 0);
+      if (s == 0 && later) MOE_WAIT_VM(kAfter + kLater);
+      else MOE_WAIT_VM(kAfter);
       asm volatile("" ::: "memory");
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
@@ -255,8 +280,8 @@ struct Reduce {
       uint8_t* const to_p = ring_p + (ip ? ip - 1 : C::NP - 1) * P::kBytes;
       auto copy = [&](auto c) {
         constexpr int i = decltype(c)::value;
-        if constexpr (i < P::kCopies) op.issue(to_p, s + C::NP - 1, i);
-        else oq.issue(to_q, s + C::NQ - 1, i - P::kCopies);
+        if constexpr (i < P::kCopies) o.p.issue(to_p, s + C::NP - 1, i);
+        else o.q.issue(to_q, s + C::NQ - 1, i - P::kCopies);
       };
       unrolled<kSteps>([&](auto kc) {
         // the MFMAs of the step before (the last one of stage s - 1 first) over the reads of step k
@@ -289,48 +314,61 @@ struct Reduce {
   }
 };
 
-// One output tile: rows 0..rows-1, columns 0..cols-1 from `out` on.  STREAM:
-// the output passes the caches by.
-template <class C, bool PX, bool QX, bool F32, bool STREAM>
-__device__ __forceinline__ void tile_product(uint8_t* smem, const uint16_t* p, long long ldp, const uint16_t* q,
-                                             long long ldq, int rows, int cols, int length, void* out, long long ldo) {
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  using P = Operand<PX, C::BM, C::kWaves, C::STEP, false>;
-  using Q = Operand<QX, C::BN, C::kWaves, C::STEP, C::NT>;
-  const P op(p, ldp, rows, length, wave, lane);
-  const Q oq(q, ldq, cols, length, wave, lane);
+// The product of a tile with `rows` live rows: the K loop with the wave's share
+// of the live row blocks.
+template <class C, bool PX, bool QX>
+__device__ __forceinline__ void multiply(uint8_t* smem, const Operands<C, PX, QX>& o, int rows, int length, int wave,
+                                         int lane, bool later, f32x16_t (&acc)[C::MI][C::NJ]) {
   const int wm = wave / C::WN, wn = wave % C::WN;
   const int stages = (length + C::STEP - 1) / C::STEP;
-  f32x16_t acc[C::MI][C::NJ];
 #pragma unroll
   for (int i = 0; i < C::MI; ++i)
 #pragma unroll
     for (int j = 0; j < C::NJ; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-
   static_assert(C::MI == 1 || C::MI == 2 || C::MI == 4, "cases below");
   const int blocks = (rows + 31) / 32, live = (blocks - wm + C::WM - 1) / C::WM;   // this wave's
-  if (live >= C::MI) Reduce<C, PX, QX, C::MI>::run(smem, op, oq, stages, wm, wn, lane, acc);
-  else if (C::MI > 3 && live == 3) Reduce<C, PX, QX, C::MI - 1>::run(smem, op, oq, stages, wm, wn, lane, acc);
-  else if (C::MI > 2 && live == 2) Reduce<C, PX, QX, 2>::run(smem, op, oq, stages, wm, wn, lane, acc);
-  else if (live == 1) Reduce<C, PX, QX, 1>::run(smem, op, oq, stages, wm, wn, lane, acc);
-  else Reduce<C, PX, QX, 0>::run(smem, op, oq, stages, wm, wn, lane, acc);
+  if (live >= C::MI) Reduce<C, PX, QX, C::MI>::run(smem, o, stages, wm, wn, lane, later, acc);
+  else if (C::MI > 3 && live == 3) Reduce<C, PX, QX, C::MI - 1>::run(smem, o, stages, wm, wn, lane, later, acc);
+  else if (C::MI > 2 && live == 2) Reduce<C, PX, QX, 2>::run(smem, o, stages, wm, wn, lane, later, acc);
+  else if (live == 1) Reduce<C, PX, QX, 1>::run(smem, o, stages, wm, wn, lane, later, acc);
+  else Reduce<C, PX, QX, 0>::run(smem, o, stages, wm, wn, lane, later, acc);
+}
 
-  // 32x32 D layout with Q first: lane holds output row l%32, columns
-  // 8 t + 4 (l/32) + [0, 4).  The wave's blocks pass through its own part of
-  // the rings, 32 rows at a time, and leave as whole rows, 16 bytes a lane:
-  // stored from the MFMA layout a row's line would be written in four parts
-  // (non-temporal stores of such parts took dw from 1.4 to 4.4 ms).  Chunks
-  // are permuted by chunk ^ row, for the banks.  The barrier finds every wave
-  // done reading the rings.
+// Workgroup barrier after a K loop: every wave is done reading the rings.
+__device__ __forceinline__ void rings_free() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+}
+
+// Stores a tile: rows 0..rows-1, columns 0..cols-1 from `out` on.  STREAM: the
+// output passes the caches by.
+//   32x32 D layout with Q first: lane holds output row l%32, columns
+// 8 t + 4 (l/32) + [0, 4).  The wave's blocks pass through LDS (the rings' last
+// tiles, which a fill leaves alone), 32 rows at a time, and leave as whole
+// rows, 16 bytes a lane: stored from the MFMA layout a row's line would be
+// written in four parts (non-temporal stores of such parts took dw from 1.4 to
+// 4.4 ms).  Chunks are permuted by chunk ^ row, for the banks.
+template <class C, bool F32, bool STREAM>
+__device__ __forceinline__ void store_tile(uint8_t* smem, const f32x16_t (&acc)[C::MI][C::NJ], int rows, int cols,
+                                           int wave, int lane, void* out, long long ldo) {
+  // the addresses below are made anew for every tile: kept across a K loop in
+  // registers (they do not change with it), they would be spilled
+  asm volatile("" : "+v"(lane));
+  const int wm = wave / C::WN, wn = wave % C::WN;
   constexpr int kSize = F32 ? 4 : 2, kRowBytes = C::NJ * 32 * kSize, kChunks = kRowBytes / 16;
   constexpr int kMask = kChunks < 16 ? kChunks - 1 : 15;
-  static_assert(C::kWaves * 32 * kRowBytes <= C::kSmem && 64 % kChunks == 0, "a block of every wave fits");
-  uint8_t* const stg = smem + wave * (32 * kRowBytes);
+  constexpr int kShift = kRowBytes >= 256 ? 0 : kRowBytes == 128 ? 1 : 2;   // rows side by side in the banks
+  auto place = [](int r, int c) { return (c ^ ((r >> kShift) & kMask)) * 16; };   // chunk c of row r
+  constexpr int kHalf = C::kWaves / 2, kQ = C::BN * C::STEP * 2, kP = C::BM * C::STEP * 2;   // waves, tile bytes
+  static_assert(kHalf * 32 * kRowBytes <= kQ && kHalf * 32 * kRowBytes <= kP * C::NP / 2 && 64 % kChunks == 0,
+                "a block of every wave fits");
+  static_assert(C::MI * kChunks / 2 <= kLater || !F32, "stores of a full tile");
+  // the last Q tile, and from the end of the P tiles down
+  uint8_t* const stg = smem + (wave < kHalf ? (C::NQ - 1) * kQ + wave * (32 * kRowBytes)
+                                            : C::kSmem - (wave - kHalf + 1) * (32 * kRowBytes));
   const int h = lane >> 5, rl = lane & 31;
 #pragma unroll
   for (int i = 0; i < C::MI; ++i) {
@@ -343,19 +381,18 @@ __device__ __forceinline__ void tile_product(uint8_t* smem, const uint16_t* p, l
         const f32x16_t& a = acc[i][j];
         uint8_t* const at = stg + rl * kRowBytes;
         if constexpr (F32) {
-          *reinterpret_cast<float4*>(at + (((8 * j + 2 * t + h) ^ (rl & kMask)) * 16)) =
+          *reinterpret_cast<float4*>(at + place(rl, 8 * j + 2 * t + h)) =
               make_float4(a[4 * t], a[4 * t + 1], a[4 * t + 2], a[4 * t + 3]);
         } else {
-          *reinterpret_cast<uint2*>(at + (((4 * j + t) ^ (rl & kMask)) * 16) + 8 * h) =
-              make_uint2(f32_to_bf16_rne(a[4 * t]) | ((uint32_t)f32_to_bf16_rne(a[4 * t + 1]) << 16),
-                         f32_to_bf16_rne(a[4 * t + 2]) | ((uint32_t)f32_to_bf16_rne(a[4 * t + 3]) << 16));
+          *reinterpret_cast<uint2*>(at + place(rl, 4 * j + t) + 8 * h) =
+              make_uint2(bf16_pair(a[4 * t], a[4 * t + 1]), bf16_pair(a[4 * t + 2], a[4 * t + 3]));
         }
       }
     asm volatile("" ::: "memory");
 #pragma unroll
     for (int k = 0; k < kChunks / 2; ++k) {   // 64 / kChunks rows at a time
       const int r = k * (64 / kChunks) + lane / kChunks, c = lane % kChunks;
-      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(stg + r * kRowBytes + ((c ^ (r & kMask)) * 16));
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(stg + r * kRowBytes + place(r, c));
       const int col = wn * (C::NJ * 32) + c * (16 / kSize);
       u32x4_t* const to = reinterpret_cast<u32x4_t*>(static_cast<uint8_t*>(out) + ((long long)(r0 + r) * ldo + col) * kSize);
       if (r0 + r < rows && col < cols) {   // cols is a multiple of 8
@@ -393,9 +430,16 @@ __device__ __forceinline__ void rows_item(uint8_t* smem, const uint16_t* p, long
   const Tile t = tiles.place(tile);
   const int c0 = slice * C::BN;
   const uint16_t* we = w + (size_t)t.e * cols * length;
-  tile_product<C, false, QX, false, false>(smem, p + (long long)t.row0 * ldp, ldp,
-                                           QX ? we + c0 : we + (size_t)c0 * length, QX ? cols : length, t.rows,
-                                           min(C::BN, cols - c0), length, out + (long long)t.row0 * cols + c0, cols);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int live_cols = min(C::BN, cols - c0);
+  using O = Operands<C, false, QX>;
+  const O o = {typename O::P(p + (long long)t.row0 * ldp, ldp, t.rows, length, wave, lane),
+               typename O::Q(QX ? we + c0 : we + (size_t)c0 * length, QX ? cols : length, live_cols, length, wave, lane)};
+  f32x16_t acc[C::MI][C::NJ];
+  o.fill(smem);
+  multiply(smem, o, t.rows, length, wave, lane, false, acc);
+  rings_free();
+  store_tile<C, false, false>(smem, acc, t.rows, live_cols, wave, lane, out + (long long)t.row0 * cols + c0, cols);
 }
 
 // y = x w_e^T
@@ -416,35 +460,82 @@ struct BackwardArgs {
   void* dw;
   Deal dx_deal;
   int dx_items, dw_items;   // per XCD (dx: at most)
+  int dw_groups;            // workgroups that share an XCD's dw items
 };
 
-// Both gradients in one launch, an XCD's dw tiles and then its dx items.
+// Tile `id` of dw: a group's tiles in bands of eight tile rows, whose
+// concurrent ones share their columns of dy and x.
+struct DwTile {
+  int e, n0, k0, lo, length, rows, cols;
+};
+template <class C>
+__device__ __forceinline__ DwTile dw_tile(const BackwardArgs& a, int id) {
+  const int mtiles = (a.n + C::BM - 1) / C::BM, ntiles = (a.k + C::BN - 1) / C::BN, per = mtiles * ntiles;
+  DwTile t;
+  t.e = id / per;
+  const int j = id - t.e * per;
+  constexpr int kBand = 8;
+  const int band = j / (kBand * ntiles), in = j - band * kBand * ntiles, high = min(kBand, mtiles - band * kBand);
+  t.n0 = (band * kBand + in % high) * C::BM;
+  t.k0 = in / high * C::BN;
+  t.lo = min(max(a.offsets[t.e], 0), a.rows);
+  t.length = min(max(a.offsets[t.e + 1], t.lo), a.rows) - t.lo;
+  t.rows = min(C::BM, a.n - t.n0);
+  t.cols = min(C::BN, a.k - t.k0);
+  return t;
+}
+
+// dw: workgroup i of its XCD's `stride` takes tiles i, i + stride, .. of the
+// XCD's share.  A tile is short (384 rows are six stages) and its output large
+// (256 KB in fp32), so the next tile's rings are filled before this one is
+// stored: the fill's latency and the stores overlap.
+template <class C, bool F32, bool STREAM>
+__device__ __forceinline__ void dw_share(uint8_t* smem, const BackwardArgs& a, int xcd, int i, int stride) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int per = ((a.n + C::BM - 1) / C::BM) * ((a.k + C::BN - 1) / C::BN);
+  const int end = min((xcd + 1) * a.dw_items, a.groups * per);
+  int id = xcd * a.dw_items + i;
+  if (id >= end) return;
+  using O = Operands<C, true, true>;
+  auto operands = [&](const DwTile& t) {
+    return O{typename O::P(a.dy + (long long)t.lo * a.lddy + t.n0, a.lddy, t.rows, t.length, wave, lane),
+             typename O::Q(a.x + (long long)t.lo * a.ldx + t.k0, a.ldx, t.cols, t.length, wave, lane)};
+  };
+  DwTile t = dw_tile<C>(a, id);
+  O o = operands(t);
+  o.fill(smem);
+  bool later = false;
+  for (;;) {
+    f32x16_t acc[C::MI][C::NJ];
+    multiply(smem, o, t.rows, t.length, wave, lane, later, acc);
+    rings_free();
+    id += stride;
+    const DwTile done = t;
+    if (id < end) {
+      t = dw_tile<C>(a, id);
+      o = operands(t);
+      o.fill(smem);
+    }
+    const size_t at = ((size_t)done.e * a.n + done.n0) * a.k + done.k0;
+    void* to = F32 ? static_cast<void*>(static_cast<float*>(a.dw) + at) : static_cast<void*>(static_cast<uint16_t*>(a.dw) + at);
+    store_tile<C, F32, STREAM>(smem, acc, done.rows, done.cols, wave, lane, to, a.k);
+    if (id >= end) return;
+    // every store of a full tile was issued, so the next K loop's first wait need not cover them
+    later = F32 && C::MI * C::NJ * 4 >= kLater && done.rows == C::BM && done.cols == C::BN;
+  }
+}
+
+// Both gradients in one launch, an XCD's dw workgroups and then its dx items.
 // (Mixed in proportion, so that some CUs would write while others multiply,
 // 32 experts x 4096 x 7168 with 12288 rows took 2033 us; dw first 1977.)
 template <class C, bool F32, bool STREAM>
 __global__ __launch_bounds__(C::kWaves* kWave, C::kPerCU* C::kWaves / 4) void grouped_backward(BackwardArgs a) {
   __shared__ __align__(1024) uint8_t smem[C::kSmem];
   const int xcd = blockIdx.x % kXcds, i = blockIdx.x / kXcds;
-  if (i >= a.dw_items) {
+  if (i < a.dw_groups) dw_share<C, F32, STREAM>(smem, a, xcd, i, a.dw_groups);
+  else
     rows_item<C, true>(smem, a.dy, a.lddy, a.w, a.offsets, a.rows, a.groups, a.k, a.n, a.dx_deal, a.dx, xcd,
-                       i - a.dw_items);
-    return;
-  }
-  // XCD x takes the x-th eighth of the dw tiles: a group's tiles in bands of
-  // eight tile rows, whose concurrent ones share their columns of dy and x
-  const int mtiles = (a.n + C::BM - 1) / C::BM, ntiles = (a.k + C::BN - 1) / C::BN, per = mtiles * ntiles;
-  const int id = xcd * a.dw_items + i;
-  const int e = id / per, j = id - e * per;
-  if (e >= a.groups) return;
-  constexpr int kBand = 8;
-  const int band = j / (kBand * ntiles), in = j - band * kBand * ntiles, high = min(kBand, mtiles - band * kBand);
-  const int n0 = (band * kBand + in % high) * C::BM, k0 = in / high * C::BN;
-  const int lo = min(max(a.offsets[e], 0), a.rows), hi = min(max(a.offsets[e + 1], lo), a.rows);
-  const size_t at = ((size_t)e * a.n + n0) * a.k + k0;
-  void* o = F32 ? static_cast<void*>(static_cast<float*>(a.dw) + at) : static_cast<void*>(static_cast<uint16_t*>(a.dw) + at);
-  tile_product<C, true, true, F32, STREAM>(smem, a.dy + (long long)lo * a.lddy + n0, a.lddy,
-                                           a.x + (long long)lo * a.ldx + k0, a.ldx, min(C::BM, a.n - n0),
-                                           min(C::BN, a.k - k0), hi - lo, o, a.k);
+                       i - a.dw_groups);
 }
 
 // items per XCD there can be with row tiles of bm rows
@@ -483,12 +574,13 @@ hipError_t launch_backward(const GroupedArgs& a, BackwardArgs b, bool f32, hipSt
   b.dx_items = b.dx ? (int)items_per_xcd(a, C::BM, b.dx_deal) : 0;
   const long long dw_tiles = (long long)a.groups * ((a.n + C::BM - 1) / C::BM) * ((a.k + C::BN - 1) / C::BN);
   b.dw_items = b.dw ? (int)((dw_tiles + kXcds - 1) / kXcds) : 0;
+  b.dw_groups = std::min(b.dw_items, kCusPerXcd * C::kPerCU);   // as many as run at once
   if (b.dx_items + b.dw_items == 0) return hipSuccess;
   // dw beyond the L2s' 32 MB leaves nothing there to read again and would
   // push dy and x out: streamed (3.76 GB: 1259 -> 1091 us)
   const bool stream_out = (size_t)a.groups * a.n * a.k * (f32 ? 4 : 2) > kL2Bytes;
   auto run = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(b.dx_items + b.dw_items) * kXcds), dim3(C::kWaves * kWave), 0, stream, b);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(b.dx_items + b.dw_groups) * kXcds), dim3(C::kWaves * kWave), 0, stream, b);
   };
   if (f32) run(stream_out ? grouped_backward<C, true, true> : grouped_backward<C, true, false>);
   else run(stream_out ? grouped_backward<C, false, true> : grouped_backward<C, false, false>);
@@ -522,7 +614,7 @@ hipError_t launch_grouped_backward(const GroupedArgs& a, const void* dy, int64_t
                                    void* dx, bool f32, void* dw, hipStream_t stream) {
   const BackwardArgs b{static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(x),
                        static_cast<const uint16_t*>(a.w), lddy, ldx, a.offsets, a.rows, a.groups, a.n, a.k,
-                       static_cast<uint16_t*>(dx), dw, {}, 0, 0};
+                       static_cast<uint16_t*>(dx), dw, {}, 0, 0, 0};
   const long long dw_tiles = (long long)a.groups * ((a.n + 255) / 256) * ((a.k + 255) / 256);
   const bool large = dw ? dw_tiles >= 256 : items<Large>(a, a.k) >= 256 && a.rows > 40LL * a.groups;
   return large ? launch_backward<Large>(a, b, f32, stream) : launch_backward<Middle<false>>(a, b, f32, stream);

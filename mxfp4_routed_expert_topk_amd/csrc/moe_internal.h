@@ -251,6 +251,13 @@ __device__ __forceinline__ uint16_t f32_to_bf16_rne(float f) {
   return (uint16_t)(u >> 16);
 }
 
+// Two fp32 -> bf16 bits (a in bits 15:0), nearest even, on v_cvt_pk_bf16_f32:
+// the results of f32_to_bf16_rne in one instruction for two values.
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  const bf16x2_t v = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
 // silu(z) = z / (1 + e^-z) in fp32, the quotient on the hardware reciprocal
 // (at most 1 ulp; h is rounded to bf16 or requantised to E4M3 right after).
 // z -> -inf gives -0 (1/inf = 0), NaN stays NaN.  Measured 1 % faster in the

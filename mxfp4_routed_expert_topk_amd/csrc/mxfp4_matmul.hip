@@ -98,8 +98,7 @@ __global__ __launch_bounds__(kSplit* kWave) void matmul_mxfp4_rows(const uint8_t
     if (n >= N) return;
     if constexpr (F32) *reinterpret_cast<f32x4_t*>(static_cast<float*>(out) + at) = v;
     else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
-        make_uint2(f32_to_bf16_rne(v[0]) | ((uint32_t)f32_to_bf16_rne(v[1]) << 16),
-                   f32_to_bf16_rne(v[2]) | ((uint32_t)f32_to_bf16_rne(v[3]) << 16));
+        make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
     return;
   }
 #pragma unroll
@@ -336,6 +335,8 @@ __device__ __forceinline__ void matmul_tile(uint8_t* smem, const uint8_t* ac, co
   // (permuted by chunk ^ row for the banks); else every element by itself.
   constexpr int kSize = F32 ? 4 : 2, kRowBytes = C::NJ * 16 * kSize, kChunks = kRowBytes / 16;
   constexpr int kMask = kChunks < 16 ? kChunks - 1 : 15;
+  constexpr int kShift = kRowBytes >= 256 ? 0 : 1;   // rows side by side in the banks
+  auto place = [](int r, int c) { return (c ^ ((r >> kShift) & kMask)) * 16; };   // chunk c of row r
   static_assert(C::kWaves * 32 * kRowBytes <= C::kSmem && 64 % kChunks == 0, "two blocks of every wave fit");
   const bool rows_aligned = N % (16 / kSize) == 0;
   uint8_t* const stg = smem + wave * (32 * kRowBytes);
@@ -350,17 +351,16 @@ __device__ __forceinline__ void matmul_tile(uint8_t* smem, const uint8_t* ac, co
           const f32x4_t v = acc[i + h][j];
           uint8_t* const at = stg + (16 * h + rl) * kRowBytes;
           if constexpr (F32)
-            *reinterpret_cast<f32x4_t*>(at + ((4 * j + q) ^ (rl & kMask)) * 16) = v;
+            *reinterpret_cast<f32x4_t*>(at + place(rl, 4 * j + q)) = v;
           else
-            *reinterpret_cast<uint2*>(at + ((2 * j + (q >> 1)) ^ (rl & kMask)) * 16 + 8 * (q & 1)) =
-                make_uint2(f32_to_bf16_rne(v[0]) | ((uint32_t)f32_to_bf16_rne(v[1]) << 16),
-                           f32_to_bf16_rne(v[2]) | ((uint32_t)f32_to_bf16_rne(v[3]) << 16));
+            *reinterpret_cast<uint2*>(at + place(rl, 2 * j + (q >> 1)) + 8 * (q & 1)) =
+                make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
         }
       asm volatile("" ::: "memory");
 #pragma unroll
       for (int k = 0; k < kChunks / 2; ++k) {   // 64 / kChunks rows at a time
         const int r = k * (64 / kChunks) + lane / kChunks, c = lane % kChunks;
-        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(stg + r * kRowBytes + ((c ^ (r & kMask)) * 16));
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(stg + r * kRowBytes + place(r, c));
         const int m = mw + 16 * i + r, n = nw + c * (16 / kSize);
         if (m < mrows && n < nrows)
           *reinterpret_cast<u32x4_t*>(static_cast<uint8_t*>(out) + ((size_t)(m0 + m) * N + n0 + n) * kSize) = v;
