@@ -256,7 +256,7 @@ struct Reduce {
     constexpr int kSteps = C::STEP / 16;
     static_assert(kSteps % 2 == 0, "two operand sets in turn");
     constexpr int kM = LIVE * C::NJ, kR = LIVE + C::NJ;   // MFMAs and operands of a step
-    constexpr int kAhead = kM > 0 ? (4 * kR + 3 * kM - 1) / (3 * kM) : 0;   // operands read behind an MFMA: done by 3/4 of them
+    constexpr int kM3 = kM ? 3 * kM : 1, kAhead = kM ? (4 * kR + kM3 - 1) / kM3 : 0;   // operands read behind an MFMA: done by 3/4 of them
     constexpr int kRows = LIVE ? LIVE : 1;
     bf16x8_t fp[2][kRows], fq[2][C::NJ];
 #pragma unroll
@@ -363,10 +363,10 @@ __device__ __forceinline__ void store_tile(uint8_t* smem, const f32x16_t (&acc)[
   constexpr int kShift = kRowBytes >= 256 ? 0 : kRowBytes == 128 ? 1 : 2;   // rows side by side in the banks
   auto place = [](int r, int c) { return (c ^ ((r >> kShift) & kMask)) * 16; };   // chunk c of row r
   constexpr int kHalf = C::kWaves / 2, kQ = C::BN * C::STEP * 2, kP = C::BM * C::STEP * 2;   // waves, tile bytes
-  static_assert(kHalf * 32 * kRowBytes <= kQ && kHalf * 32 * kRowBytes <= kP * C::NP / 2 && 64 % kChunks == 0,
+  static_assert(kHalf * 32 * kRowBytes <= kQ && kHalf * 32 * kRowBytes <= kP && 64 % kChunks == 0,
                 "a block of every wave fits");
   static_assert(C::MI * kChunks / 2 <= kLater || !F32, "stores of a full tile");
-  // the last Q tile, and from the end of the P tiles down
+  // the last Q tile, and the end of the last P tile
   uint8_t* const stg = smem + (wave < kHalf ? (C::NQ - 1) * kQ + wave * (32 * kRowBytes)
                                             : C::kSmem - (wave - kHalf + 1) * (32 * kRowBytes));
   const int h = lane >> 5, rl = lane & 31;

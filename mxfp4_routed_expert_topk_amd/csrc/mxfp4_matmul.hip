@@ -427,20 +427,21 @@ hipError_t launch_mxfp4_matmul(const uint8_t* ac, const uint8_t* as, const uint8
   const int nb = (N + 15) / 16, mb = (M + 15) / 16;
   const int mt = mb == 1 || nb * mb <= 256 ? 1 : mb == 2 || nb * ((mb + 1) / 2) <= 256 ? 2 : 4;
   // It reads mt + 1 row blocks of K/2 bytes per workgroup from the L2s at about
-  // 4.6 TB/s; up to 256 tiles of 128 x 128 take about 5 us and 0.45 us per 256
-  // K.  The two meet where the count below does (K 7168 to 4096 columns: 48
-  // rows 15.7 against 17.9 us, 96 rows 29.2 against 18.3; K 2048 to 7168: 32
-  // rows 7.5 against 8.5, 48 rows 10.5 against 8.8).
+  // 4.6 TB/s; up to 256 tiles of 128 x 128 take about 4.5 us and 0.4 us per 256
+  // K.  The two meet about where the count below does (K 7168 to 4096 columns:
+  // 32 rows 11.3 against 16.5 us, 48 rows 15.5 against 16.5, 64 rows 17.9
+  // against 16.5; K 2048 to 7168: 17 rows 5.9 against 6.9, 48 rows 10.5 against
+  // 7.0; K 480 to 2048: 256 rows 4.3 against 5.2).
   const long long blocks = (long long)nb * ((mb + mt - 1) / mt) * (mt + 1);
-  if (blocks <= 1100 + 1600000 / K) {
+  if (blocks <= 900 + 800000 / K) {
     if (mt == 1) return launch_rows<1>(ac, as, bc, bs, M, N, K, f32, out, stream);
     if (mt == 2) return launch_rows<2>(ac, as, bc, bs, M, N, K, f32, out, stream);
     return launch_rows<4>(ac, as, bc, bs, M, N, K, f32, out, stream);
   }
   // 256 x 256 once they fill most of the 256 CUs: half the copies per product
-  // (K 7168 to 4096 columns: 2048 rows, 128 large tiles, 49 against 43 us;
-  // 4096 rows, 256 of them, 62 against 84; K 2048 to 7168: 2048 rows, 224 of
-  // them, 24.4 against 28.9).
+  // (K 7168 to 4096 columns: 2048 rows, 128 large tiles, 49 against 41 us;
+  // 4096 rows, 256 of them, 59 against 84; K 2048 to 7168: 2048 rows, 224 of
+  // them, 20.8 against 28.9).
   if ((long long)((M + 255) / 256) * ((N + 255) / 256) >= 192)
     return launch_tiles<Mx256>(ac, as, bc, bs, M, N, K, f32, out, stream);
   return launch_tiles<Mx128>(ac, as, bc, bs, M, N, K, f32, out, stream);

@@ -24,6 +24,14 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPerLane = 8;              // elements per lane: one dword of codes
+// A launch holds fewer than 2^32 threads; a lane past kMaxBlocks workgroups'
+// takes its turn in a loop.
+constexpr long long kMaxBlocks = 1 << 23;
+
+unsigned blocks_for(long long lanes) {
+  const long long b = (lanes + kThreads - 1) / kThreads;
+  return (unsigned)(b < kMaxBlocks ? b : kMaxBlocks);
+}
 
 __device__ __forceinline__ void load8(const uint16_t* p, uint32_t (&v)[8]) {
   const uint4 w = *reinterpret_cast<const uint4*>(p);
@@ -46,30 +54,31 @@ template <class T, bool STRIDED>
 __global__ __launch_bounds__(kThreads) void quant_mxfp4(const T* __restrict__ x, long long lanes, int lanes_per_row,
                                                         long long ld, uint32_t* __restrict__ codes,
                                                         uint8_t* __restrict__ scales) {
-  const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= lanes) return;                // whole blocks: lanes is a multiple of 4
-  long long at = i * kPerLane;
-  if constexpr (STRIDED) {
-    const long long row = i / lanes_per_row;
-    at = row * ld + (i - row * lanes_per_row) * kPerLane;
-  }
-  uint32_t v[8];
-  load8(x + at, v);
-  uint32_t amax = 0;                     // as bits: a NaN ranks above every finite value
+  // a block's four lanes stay together: lanes and the stride are multiples of 4
+  for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < lanes; i += (long long)gridDim.x * kThreads) {
+    long long at = i * kPerLane;
+    if constexpr (STRIDED) {
+      const long long row = i / lanes_per_row;
+      at = row * ld + (i - row * lanes_per_row) * kPerLane;
+    }
+    uint32_t v[8];
+    load8(x + at, v);
+    uint32_t amax = 0;                     // as bits: a NaN ranks above every finite value
 #pragma unroll
-  for (int j = 0; j < 8; ++j) amax = max(amax, v[j] & 0x7FFFFFFFu);
-  amax = max(amax, (uint32_t)__shfl_xor((int)amax, 1, kWave));
-  amax = max(amax, (uint32_t)__shfl_xor((int)amax, 2, kWave));
-  const bool bad = amax >= 0x7F800000u;
-  const int byte = max((int)(amax >> 23) - 2, 2);
-  const float scale = __uint_as_float((uint32_t)byte << 23);
-  uint32_t c = 0;
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(v[0]), __uint_as_float(v[1]), scale, 0);
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(v[2]), __uint_as_float(v[3]), scale, 1);
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(v[4]), __uint_as_float(v[5]), scale, 2);
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(v[6]), __uint_as_float(v[7]), scale, 3);
-  codes[i] = bad ? 0u : c;
-  if ((threadIdx.x & 3) == 0) scales[i >> 2] = bad ? 0xFFu : (uint8_t)byte;
+    for (int j = 0; j < 8; ++j) amax = max(amax, v[j] & 0x7FFFFFFFu);
+    amax = max(amax, (uint32_t)__shfl_xor((int)amax, 1, kWave));
+    amax = max(amax, (uint32_t)__shfl_xor((int)amax, 2, kWave));
+    const bool bad = amax >= 0x7F800000u;
+    const int byte = max((int)(amax >> 23) - 2, 2);
+    const float scale = __uint_as_float((uint32_t)byte << 23);
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(v[0]), __uint_as_float(v[1]), scale, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(v[2]), __uint_as_float(v[3]), scale, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(v[4]), __uint_as_float(v[5]), scale, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(v[6]), __uint_as_float(v[7]), scale, 3);
+    codes[i] = bad ? 0u : c;
+    if ((threadIdx.x & 3) == 0) scales[i >> 2] = bad ? 0xFFu : (uint8_t)byte;
+  }
 }
 
 // E8M0 byte -> its value: 2^(b-127) (byte 0 is the subnormal 2^-127), NaN for 0xFF.
@@ -87,32 +96,32 @@ __global__ __launch_bounds__(kThreads) void dequant_mxfp4(const uint8_t* __restr
                                                           const uint8_t* __restrict__ scales, long long lanes,
                                                           uint4* __restrict__ out) {
   constexpr int kN = F32 ? 4 : 8;        // elements per lane
-  const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= lanes) return;
-  uint32_t c;
-  if constexpr (F32) c = reinterpret_cast<const uint16_t*>(codes)[i];
-  else c = reinterpret_cast<const uint32_t*>(codes)[i];
-  const float s = e8m0_value(scales[i / (32 / kN)]);
-  typedef float f32x2_t __attribute__((ext_vector_type(2)));
-  typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-  uint32_t v[kN];
-  auto pair = [&](int j, f32x2_t p) {
-    v[2 * j] = __float_as_uint(p[0] * s);
-    v[2 * j + 1] = __float_as_uint(p[1] * s);
-  };
-  pair(0, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0));
-  pair(1, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1));
-  u32x4_t o;
-  if constexpr (F32) {
-    o = u32x4_t{v[0], v[1], v[2], v[3]};
-  } else {
-    pair(2, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2));
-    pair(3, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3));
+  for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < lanes; i += (long long)gridDim.x * kThreads) {
+    uint32_t c;
+    if constexpr (F32) c = reinterpret_cast<const uint16_t*>(codes)[i];
+    else c = reinterpret_cast<const uint32_t*>(codes)[i];
+    const float s = e8m0_value(scales[i / (32 / kN)]);
+    typedef float f32x2_t __attribute__((ext_vector_type(2)));
+    typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+    uint32_t v[kN];
+    auto pair = [&](int j, f32x2_t p) {
+      v[2 * j] = __float_as_uint(p[0] * s);
+      v[2 * j + 1] = __float_as_uint(p[1] * s);
+    };
+    pair(0, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0));
+    pair(1, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1));
+    u32x4_t o;
+    if constexpr (F32) {
+      o = u32x4_t{v[0], v[1], v[2], v[3]};
+    } else {
+      pair(2, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2));
+      pair(3, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = (v[2 * j] >> 16) | (v[2 * j + 1] & 0xFFFF0000u);
+      for (int j = 0; j < 4; ++j) o[j] = (v[2 * j] >> 16) | (v[2 * j + 1] & 0xFFFF0000u);
+    }
+    if constexpr (STREAM) __builtin_nontemporal_store(o, reinterpret_cast<u32x4_t*>(out) + i);
+    else reinterpret_cast<u32x4_t*>(out)[i] = o;
   }
-  if constexpr (STREAM) __builtin_nontemporal_store(o, reinterpret_cast<u32x4_t*>(out) + i);
-  else reinterpret_cast<u32x4_t*>(out)[i] = o;
 }
 
 }  // namespace
@@ -120,7 +129,7 @@ __global__ __launch_bounds__(kThreads) void dequant_mxfp4(const uint8_t* __restr
 hipError_t launch_mxfp4_quantize(const void* x, bool f32, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
                                  uint8_t* scales, hipStream_t stream) {
   const long long per_row = cols / kPerLane, lanes = rows * per_row;
-  const dim3 grid((unsigned)((lanes + kThreads - 1) / kThreads));
+  const dim3 grid(blocks_for(lanes));
   uint32_t* const c = reinterpret_cast<uint32_t*>(codes);
   auto run = [&](auto* src) {
     using T = std::remove_pointer_t<decltype(src)>;
@@ -139,7 +148,7 @@ hipError_t launch_mxfp4_quantize(const void* x, bool f32, int64_t rows, int64_t 
 hipError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, bool f32,
                                    void* out, hipStream_t stream) {
   const long long lanes = rows * cols / (f32 ? 4 : 8);
-  const dim3 grid((unsigned)((lanes + kThreads - 1) / kThreads));
+  const dim3 grid(blocks_for(lanes));
   const bool stream_out = lanes * 16 > (long long)kL2Bytes;
   auto run = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, codes, scales, lanes, static_cast<uint4*>(out));

@@ -136,7 +136,9 @@ def mx_operand(rng, rows, k, low=126, high=129):
 MATMUL_SIZES = [(1, 1, 32), (1, 16, 64), (2, 17, 96), (16, 16, 128), (17, 33, 160), (1, 4096, 1024), (5, 100, 2048),
                 (33, 257, 288), (64, 64, 512), (65, 130, 544), (128, 128, 256), (130, 250, 1056), (256, 256, 768),
                 (257, 511, 800), (300, 1000, 2048), (513, 264, 4096), (700, 300, 96), (1, 129, 4128), (37, 384, 1376),
-                (3585, 3601, 160), (3401, 3704, 1056)]
+                (3585, 3601, 160), (3401, 3704, 1056),   # 256 x 256 tiles
+                (1500, 1201, 1056), (1500, 1208, 800), (1500, 1204, 352), (2000, 640, 512),   # 128 x 128
+                (17, 4101, 160), (50, 2101, 1056), (64, 2100, 2048)]   # two and four row blocks a workgroup
 
 
 @pytest.mark.parametrize("m,n,k", MATMUL_SIZES)
