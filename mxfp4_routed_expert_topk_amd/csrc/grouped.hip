@@ -257,6 +257,11 @@ struct Reduce {
     static_assert(kSteps % 2 == 0, "two operand sets in turn");
     constexpr int kM = LIVE * C::NJ, kR = LIVE + C::NJ;   // MFMAs and operands of a step
     constexpr int kM3 = kM ? 3 * kM : 1, kAhead = kM ? (4 * kR + kM3 - 1) / kM3 : 0;   // operands read behind an MFMA: done by 3/4 of them
+    // The copies stand in a stage's first quarter (P, needed one stage on) and
+    // third quarter (Q): 1495 us for eight groups of 4096 x 4096 x 7168, 1504
+    // with all of them in the first half, 1526 in the first quarter.  P's come
+    // first, as the wait below counts.
+    constexpr int kQuarter = kSteps * kM / 4;
     constexpr int kRows = LIVE ? LIVE : 1;
     bf16x8_t fp[2][kRows], fq[2][C::NJ];
 #pragma unroll
@@ -295,8 +300,10 @@ struct Reduce {
             else if constexpr (r <= C::NJ) fq[then][r ? r - 1 : 0] = Q::read(bq, wn * C::NJ + (r ? r - 1 : 0), k, lane);
             else if constexpr (r < kR) fp[then][r - C::NJ] = P::read(bp, (r - C::NJ) * C::WM + wm, k, lane);
           });
-          unrolled<kG>([&](auto c) {   // over the stage's first half: P is needed one stage on
-            if constexpr (decltype(c)::value * (kSteps / 2) * kM / kG == k * kM + m) copy(c);
+          unrolled<kG>([&](auto cc) {
+            constexpr int c = decltype(cc)::value, q = c - P::kCopies;
+            constexpr int at = q < 0 ? c * kQuarter / P::kCopies : 2 * kQuarter + q * kQuarter / Q::kCopies;
+            if constexpr (at == k * kM + m) copy(cc);
           });
           __builtin_amdgcn_sched_barrier(0);
         });
