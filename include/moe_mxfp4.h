@@ -231,7 +231,9 @@ moe_status moe_router_topk(const float* logits, int32_t num_tokens, int32_t num_
                            int32_t top_k, int32_t* topk_ids, float* topk_weights,
                            hipStream_t stream);
 
-/* Element type of a floating tensor of the entries below. */
+/* Element type of a floating tensor of the entries below.  Their pointers are
+ * 16-byte aligned, but for scales (any address) and offsets (4 bytes), so that
+ * a range of rows or of groups can be taken from a larger tensor. */
 typedef enum { MOE_BF16 = 0, MOE_F32 = 1 } moe_dtype;
 
 /* MXFP4 quantisation of a matrix x [rows, cols] (cols a multiple of 32): the
@@ -243,8 +245,8 @@ typedef enum { MOE_BF16 = 0, MOE_F32 = 1 } moe_dtype;
  * bytes are 2..252, which a plan accepts for either activation type.  A block
  * that holds a NaN or an infinity gets byte 0xFF and codes 0 (a plan refuses
  * it by name).
- *   x      [rows, cols] of `dtype`, rows ldx elements apart (ldx >= cols, 16
- *          bytes a multiple of)
+ *   x      [rows, cols] of `dtype`, rows ldx >= cols elements apart, each row
+ *          16-byte aligned
  *   codes  [rows, cols/2] u8, element 2j in bits 3:0;  scales [rows, cols/32] u8
  * rows <= 2^24; rows = 0 is a no-op.  Enqueue-only. */
 moe_status moe_mxfp4_quantize(const void* x, int32_t dtype, int32_t rows, int32_t cols, int64_t ldx,
@@ -276,7 +278,9 @@ moe_status moe_mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, con
  *   offsets [num_groups + 1] int32 in device memory: group e's rows are
  *           offsets[e] .. offsets[e+1] - 1; nondecreasing, within [0, rows]
  *           (values outside are clamped there and a decreasing pair counts as
- *           an empty group, so no offset reaches outside the tensors)
+ *           an empty group, so no offset reaches outside the tensors; a row
+ *           that decreasing offsets give to two groups gets either's output
+ *           or is left as it was)
  *   out     [rows, n] bf16: out_r = w_e x_r, summed in fp32 and rounded once;
  *           rows outside every group are not written
  * n and k multiples of 8 in [8, 65536], num_groups <= 4096, rows <= 2^24, row

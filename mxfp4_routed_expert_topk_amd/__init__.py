@@ -525,7 +525,8 @@ def grouped_matmul(x, w, offsets, out=None, stream=None):
     """out [rows, n] bf16 with out[r] = w[e] @ x[r] for offsets[e] <= r < offsets[e+1]
     (moe_grouped_matmul): x [rows, k] bf16 (its rows contiguous), w [num_groups, n, k]
     bf16, offsets [num_groups + 1] int32 on the device, as Plan.route gives them.
-    Rows outside every group are left as they were (undefined in a new `out`)."""
+    Rows outside every group are left as they were (undefined in a new `out`).
+    No autograd graph is recorded: grouped_matmul_backward gives the gradients."""
     import torch
     groups, n, k = _grouped(w, offsets)
     ld = _rows(x, "x", (torch.bfloat16,), k, w)
@@ -564,8 +565,8 @@ def grouped_matmul_backward(dy, x, w, offsets, dx=None, dw=None, dw_dtype=None, 
                               ("offsets", offsets))
         x_at, dw_at = x.data_ptr(), dw.data_ptr()
         used += [x, dw]
-    else:
-        dw = None
+    elif dw is not None:
+        raise _arg_error("dw is given, but need_dw is False")
     if need_dx:
         if dx is None:
             dx = _new((rows, k), torch.bfloat16, w, stream)
@@ -576,8 +577,8 @@ def grouped_matmul_backward(dy, x, w, offsets, dx=None, dw=None, dw_dtype=None, 
                 _apart(dx, "dx", ("x", x), ("dw", dw))
         dx_at = dx.data_ptr()
         used.append(dx)
-    else:
-        dx = None
+    elif dx is not None:
+        raise _arg_error("dx is given, but need_dx is False")
     _launch(load_library().moe_grouped_matmul_backward,
             (dy.data_ptr(), lddy, x_at, ldx, w.data_ptr(), offsets.data_ptr(), rows, groups, n, k, dx_at, dw_at, code),
             w, stream, used)

@@ -615,8 +615,8 @@ hipError_t launch_grouped_forward(const GroupedArgs& a, const void* x, int64_t l
 }
 
 // 256 x 256 tiles where they fill the CUs (32 groups of 384 rows, 4096 x 7168:
-// 2000 us against 2575 with 128 x 128), else 128 x 128 (8 groups of 75 rows,
-// 768 x 1024: 22.4 against 13.7).
+// 2010 us against 2390 with 128 x 128), else 128 x 128 (8 groups of 75 rows,
+// 768 x 1024: 19.1 against 11.7).
 hipError_t launch_grouped_backward(const GroupedArgs& a, const void* dy, int64_t lddy, const void* x, int64_t ldx,
                                    void* dx, bool f32, void* dw, hipStream_t stream) {
   const BackwardArgs b{static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(x),

@@ -114,10 +114,10 @@ __global__ __launch_bounds__(kSplit* kWave) void matmul_mxfp4_rows(const uint8_t
 // One stage is 256 K: 128 bytes of codes per row, whole cache lines, copied
 // global -> LDS by buffer_load ... lds (8 rows per wave instruction) into one
 // of two buffers while the other multiplies.  (With 128 K a stage, half lines,
-// the copies took 62 us against 59 at 4096 x 4096 x 7168.)  The eight 16-byte chunks of a staged row are permuted
-// by chunk ^ (row & 7) ^ ((row >> 3) & 1): the sixteen rows of a
-// quarter-wave's ds_read_b128 then cover all 64 banks once.  Copies past an
-// edge get an out-of-range offset and write zeros.
+// the copies took 62 us against 59 at 4096 x 4096 x 7168.)  The eight 16-byte
+// chunks of a staged row are permuted by chunk ^ (row & 7) ^ ((row >> 3) & 1):
+// the sixteen rows of a quarter-wave's ds_read_b128 then cover all 64 banks
+// once.  Copies past an edge get an out-of-range offset and write zeros.
 // A pair of stages (512 K) has 16 scale bytes per row.  Thread t loads those
 // of row t one pair ahead, transposes them to four dwords (dword q: the bytes
 // of blocks q, q + 4, q + 8, q + 12, that is lane quarter q's scales of the
@@ -194,7 +194,7 @@ __device__ __forceinline__ void matmul_tile(uint8_t* smem, const uint8_t* ac, co
     const bool in = 8 * s + chunk_of < groups;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         j < kCopiesA ? ra : rb, (lds_void_t*)(smem + slot * C::kStageBytes + (wave + C::kWaves * j) * 1024), 16,
-        in ? off[j] : kPastEnd, s < 2 * pairs ? s * 128 : 0, 0, 0);
+        in ? off[j] : kPastEnd, 8 * s < groups ? s * 128 : 0, 0, 0);   // never past the resource by itself
   };
   // scales: thread t's row of the staged ones (a wave's are all A's or all B's)
   const bool of_a = wave < C::BM / kWave;

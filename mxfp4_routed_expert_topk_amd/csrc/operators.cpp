@@ -18,17 +18,20 @@ constexpr int32_t kMaxMatmulDim = 1 << 19;
 constexpr int32_t kMaxMatmulK = 1 << 16;
 constexpr int64_t kMaxLd = 1 << 20;
 
+// Scale bytes are read and written one by one or by unaligned loads, offsets
+// one by one: a range of rows or of groups may start anywhere.
 struct Ptr {
   const char* name;
   const void* p;
+  unsigned align = 16;
 };
 
 template <int N>
 moe_status check_ptrs(const Ptr (&ptrs)[N]) {
   for (const Ptr& q : ptrs) {
     if (!q.p) return fail(MOE_ERR_ARG, "%s is null", q.name);
-    if (reinterpret_cast<uintptr_t>(q.p) & 15u)
-      return fail(MOE_ERR_ALIGN, "%s must be 16-byte aligned, got %p", q.name, q.p);
+    if (reinterpret_cast<uintptr_t>(q.p) % q.align)
+      return fail(MOE_ERR_ALIGN, "%s must be %u-byte aligned, got %p", q.name, q.align, q.p);
   }
   return MOE_OK;
 }
@@ -78,7 +81,7 @@ moe_status moe_mxfp4_quantize(const void* x, int32_t dtype, int32_t rows, int32_
   if (ldx < cols || ldx % unit)
     return fail(MOE_ERR_SHAPE, "ldx must be a multiple of %d of at least cols=%d, got %lld", unit, cols, (long long)ldx);
   if (rows == 0) return ok();
-  if (moe_status s = check_ptrs({{"x", x}, {"codes", codes}, {"scales", scales}})) return s;
+  if (moe_status s = check_ptrs({{"x", x}, {"codes", codes}, {"scales", scales, 1}})) return s;
   const hipError_t e = moe::launch_mxfp4_quantize(x, dtype == MOE_F32, rows, cols, ldx, codes, scales, stream);
   return e == hipSuccess ? ok() : hip_fail(e, "mxfp4 quantise launch");
 }
@@ -88,7 +91,7 @@ moe_status moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int
   if (moe_status s = check_dtype("dtype", dtype)) return s;
   if (moe_status s = check_matrix(rows, cols)) return s;
   if (rows == 0) return ok();
-  if (moe_status s = check_ptrs({{"codes", codes}, {"scales", scales}, {"out", out}})) return s;
+  if (moe_status s = check_ptrs({{"codes", codes}, {"scales", scales, 1}, {"out", out}})) return s;
   const hipError_t e = moe::launch_mxfp4_dequantize(codes, scales, rows, cols, dtype == MOE_F32, out, stream);
   return e == hipSuccess ? ok() : hip_fail(e, "mxfp4 dequantise launch");
 }
@@ -103,8 +106,8 @@ moe_status moe_mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, con
   if (k < 32 || k > kMaxMatmulK || k % 32)
     return fail(MOE_ERR_SHAPE, "k must be a multiple of 32 in [32, %d], got %d", kMaxMatmulK, k);
   if (m == 0 || n == 0) return ok();
-  if (moe_status s = check_ptrs({{"a_codes", a_codes}, {"a_scales", a_scales}, {"b_codes", b_codes},
-                                 {"b_scales", b_scales}, {"out", out}}))
+  if (moe_status s = check_ptrs({{"a_codes", a_codes}, {"a_scales", a_scales, 1}, {"b_codes", b_codes},
+                                 {"b_scales", b_scales, 1}, {"out", out}}))
     return s;
   const hipError_t e =
       moe::launch_mxfp4_matmul(a_codes, a_scales, b_codes, b_scales, m, n, k, dtype == MOE_F32, out, stream);
@@ -116,7 +119,7 @@ moe_status moe_grouped_matmul(const uint16_t* x, int64_t ldx, const uint16_t* w,
   if (moe_status s = check_grouped(rows, num_groups, n, k)) return s;
   if (moe_status s = check_ld("ldx", ldx, k)) return s;
   if (rows == 0 || num_groups == 0) return ok();
-  if (moe_status s = check_ptrs({{"x", x}, {"w", w}, {"offsets", offsets}, {"out", out}})) return s;
+  if (moe_status s = check_ptrs({{"x", x}, {"w", w}, {"offsets", offsets, 4}, {"out", out}})) return s;
   const hipError_t e = moe::launch_grouped_forward({w, offsets, rows, num_groups, n, k}, x, ldx, out, stream);
   return e == hipSuccess ? ok() : hip_fail(e, "grouped matmul launch");
 }
@@ -131,7 +134,7 @@ moe_status moe_grouped_matmul_backward(const uint16_t* dy, int64_t lddy, const u
   if (moe_status s = check_ld("ldx", ldx, k)) return s;
   if (rows == 0) dx = nullptr;   // no rows to write
   if (num_groups == 0 || (!dx && !dw)) return ok();
-  if (moe_status s = check_ptrs({{"offsets", offsets}})) return s;
+  if (moe_status s = check_ptrs({{"offsets", offsets, 4}})) return s;
   if (rows > 0)   // without rows every weight gradient is zero and nothing is read
     if (moe_status s = check_ptrs({{"dy", dy}})) return s;
   if (dx)

@@ -380,6 +380,127 @@ def test_grouped_empty_calls():
     assert moe.mxfp4_matmul(codes, scales, codes, scales).shape == (0, 0)
 
 
+@pytest.mark.parametrize("m,n,k", [(20, 300, 1056), (700, 300, 96), (1500, 1204, 352), (3401, 3704, 544)])
+def test_mxfp4_rows_of_larger_matrices(m, n, k):
+    """A range of rows: its scales may start at any address."""
+    rng = np.random.default_rng(k)
+    full = [up(t) for t in (*mx_operand(rng, m + 5, k), *mx_operand(rng, n + 6, k))]
+    part = [t[c:] for t, c in zip(full, (5, 5, 3, 3))]
+    part[2:] = [t[:n] for t in part[2:]]
+    assert any(t.data_ptr() % 16 for t in part)
+    own = [t.clone() for t in part]
+    assert torch.equal(moe.mxfp4_matmul(*part), moe.mxfp4_matmul(*own))
+    assert torch.equal(moe.mxfp4_dequantize(*part[:2]), moe.mxfp4_dequantize(*own[:2]))
+    x = moe.mxfp4_dequantize(*own[:2])
+    full[0].zero_(), full[1].zero_()
+    moe.mxfp4_quantize(x, codes=part[0], scales=part[1])
+    want = moe.mxfp4_quantize(x)
+    assert torch.equal(part[0], want[0]) and torch.equal(part[1], want[1])
+    assert not full[0][:5].any() and not full[1][:5].any()
+
+
+def test_grouped_range_of_groups():
+    """Some of the groups, their offsets as they lie in the whole array: the others' rows are left."""
+    off, x, dy, w = grouped_case([30, 70, 0, 41, 9], 136, 200, 2, 3, 6)
+    X, DY, W, O = up(x, BF), up(dy, BF), up(w, BF), up(off)
+    whole = moe.grouped_matmul(X, W, O), *moe.grouped_matmul_backward(DY, X, W, O)
+    lo, hi = off[1], off[4]
+    y, dx = torch.full_like(whole[0], 7.0), torch.full_like(whole[1], 7.0)
+    moe.grouped_matmul(X, W[1:4], O[1:5], out=y)
+    _, dw = moe.grouped_matmul_backward(DY, X, W[1:4], O[1:5], dx=dx)
+    for got, ref in ((y, whole[0]), (dx, whole[1])):
+        assert torch.equal(got[lo:hi], ref[lo:hi]) and bool((got[:lo] == 7).all()) and bool((got[hi:] == 7).all())
+    assert torch.equal(dw, whole[2][1:4])
+
+
+# ------------------------------------------------------------------ beyond 32 bits
+# Tensors of more than 2^31 elements (and 2^32 bytes), of which the calls use the
+# far end; elsewhere rows belong to no group or hold zeros.
+def far_rows(rows, cols, used):
+    """bf16 [rows, cols], uninitialised but for small integers in the last `used` rows."""
+    t = torch.empty((rows, cols), dtype=BF, device=dev())
+    a = ints(np.random.default_rng(rows + cols), (used, cols))
+    t[rows - used:] = up(a, BF)
+    return t, a
+
+
+def test_quantize_and_dequantize_far_rows():
+    # 2^24 + 32 rows of 1024: more lanes than one launch has threads
+    rows, cols = (1 << 24), 1024 + 32
+    x = torch.zeros((rows, cols), dtype=BF, device=dev())
+    tail = up(ints(np.random.default_rng(0), (70, cols)), BF)
+    x[-70:] = tail
+    codes, scales = moe.mxfp4_quantize(x)
+    del x
+    want = moe.mxfp4_quantize(tail)
+    assert torch.equal(codes[-70:], want[0]) and torch.equal(scales[-70:], want[1])
+    assert not codes[-80:-70].any() and bool((scales[-80:-70] == 2).all())
+    for dtype in (BF, torch.float32):
+        assert torch.equal(moe.mxfp4_dequantize(codes, scales, dtype=dtype)[-70:], moe.mxfp4_dequantize(*want, dtype=dtype))
+
+
+def test_quantize_far_strided_rows():
+    x, a = far_rows(300000, 8192, 40)      # 2.4e9 elements
+    codes, scales = moe.mxfp4_quantize(x[:, 64:128])
+    want = moe.mxfp4_quantize(up(a[:, 64:128], BF))
+    assert torch.equal(codes[-40:], want[0]) and torch.equal(scales[-40:], want[1])
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+def test_matmul_far_outputs(dtype):
+    m, n = 50000, 50001                    # 2.5e9 outputs; rows are not 16-byte aligned
+    g = torch.Generator(device=dev()).manual_seed(1)
+    a, b = (torch.randint(0, 256, (r, 32), dtype=torch.uint8, device=dev(), generator=g) for r in (m, n))
+    sa, sb = (torch.full((r, 2), 127, dtype=torch.uint8, device=dev()) for r in (m, n))
+    out = moe.mxfp4_matmul(a, sa, b, sb, dtype=dtype)
+    av, bv = (moe.mxfp4_dequantize(t, s, dtype=torch.float32).double() for t, s in ((a[-300:], sa[-300:]), (b, sb)))
+    # sums of 64 multiples of 1/4 of at most 36: exact in fp32
+    assert torch.equal(out[-300:], (av @ bv.t()).to(dtype))
+    del out
+    out = moe.mxfp4_matmul(b, sb, a, sa, dtype=dtype)      # 16-byte rows
+    assert torch.equal(out[-300:].t(), (moe.mxfp4_dequantize(a, sa, dtype=torch.float32).double() @ bv[-300:].t()).to(dtype))
+
+
+def test_grouped_far_rows():
+    rows, n, k, used = 340000, 7168, 264, 700
+    off = up(np.array([rows - used, rows - 300, rows - 300, rows], np.int32))
+    split = [0, used - 300, used - 300, used]
+    dy, a = far_rows(rows, n, used)        # 2.4e9 elements
+    w = ints(np.random.default_rng(2), (3, n, k))
+    W = up(w, BF)
+    dx, dw = moe.grouped_matmul_backward(dy, torch.ones((rows, k), dtype=BF, device=dev()), W, off)
+    np.testing.assert_array_equal(f64(dx[-used:]), bf16_rounded(np.concatenate([a[:400] @ w[0], a[400:] @ w[2]])))
+    np.testing.assert_array_equal(f64(dw), np.stack([a[i:j].T @ np.ones((j - i, k)) for i, j in zip(split, split[1:])]))
+    # the forward product's far input, and its far output
+    wt = np.ascontiguousarray(w.transpose(0, 2, 1))
+    y = moe.grouped_matmul(dy, up(wt, BF), off)
+    np.testing.assert_array_equal(f64(y[-used:]), f64(dx[-used:]))
+    del y, dx
+    x, a = far_rows(rows, k, used)
+    y = moe.grouped_matmul(x, W, off, out=dy)
+    np.testing.assert_array_equal(f64(y[-used:]), bf16_rounded(np.concatenate([a[:400] @ w[0].T, a[400:] @ w[2].T])))
+
+
+def test_grouped_far_groups():
+    groups, n, k, rows = 1160, 1024, 2048, 90        # 2.4e9 weights
+    off = np.zeros(groups + 1, np.int32)
+    off[-2:] = 50, rows
+    rng = np.random.default_rng(3)
+    x, dy, w = ints(rng, (rows, k)), ints(rng, (rows, n)), ints(rng, (2, n, k))
+    W = torch.empty((groups, n, k), dtype=BF, device=dev())
+    W[-2:] = up(w, BF)
+    args = up(dy, BF), up(x, BF), W, up(off)
+    y = f64(moe.grouped_matmul(args[1], W, args[3]))
+    np.testing.assert_array_equal(y, bf16_rounded(np.concatenate([x[:50] @ w[0].T, x[50:] @ w[1].T])))
+    for dtype in (torch.float32, BF):
+        dx, dw = moe.grouped_matmul_backward(*args, dw_dtype=dtype)
+        np.testing.assert_array_equal(f64(dx), bf16_rounded(np.concatenate([dy[:50] @ w[0], dy[50:] @ w[1]])))
+        for e, (lo, hi) in ((-2, (0, 50)), (-1, (50, rows))):
+            want = dy[lo:hi].T @ x[lo:hi]
+            np.testing.assert_array_equal(f64(dw[e]), want if dtype == torch.float32 else bf16_rounded(want))
+        assert not dw[:-2].any()
+
+
 # ------------------------------------------------------------------ streams, graphs, and all of them together
 def test_on_another_stream():
     off, x, dy, w = grouped_case([100, 28], 128, 192, 0, 0, 3)

@@ -36,7 +36,8 @@ P = 64   # a pointer that is aligned and never read
     ((P, 1, 4, 64, 66, P, P, None), 2, "ldx must be a multiple of 4"),
     ((None, 0, 4, 64, 64, P, P, None), 1, "x is null"),
     ((P, 0, 4, 64, 64, P + 4, P, None), 3, "codes must be 16-byte aligned"),
-    ((P, 0, 4, 64, 64, P, P + 1, None), 3, "scales must be 16-byte aligned"),
+    ((P, 0, 4, 64, 64, P, None, None), 1, "scales is null"),
+    ((P + 8, 0, 4, 64, 64, P, P + 1, None), 3, "x must be 16-byte aligned"),
 ])
 def test_quantize_refusals(lib, args, status, needle):
     refused(lib, "moe_mxfp4_quantize", args, status, needle)
@@ -61,7 +62,7 @@ def test_dequantize_refusals(lib, args, status, needle):
     ((P, P, P, P, 4, 4, 0, 0, P, None), 2, "k must be a multiple of 32"),
     ((P, P, P, P, 4, 4, 65568, 0, P, None), 2, "k must be a multiple of 32"),
     ((P, P, None, P, 4, 4, 64, 0, P, None), 1, "b_codes is null"),
-    ((P, P + 2, P, P, 4, 4, 64, 0, P, None), 3, "a_scales must be 16-byte aligned"),
+    ((P, P + 1, P + 2, P, 4, 4, 64, 0, P, None), 3, "b_codes must be 16-byte aligned"),
 ])
 def test_matmul_refusals(lib, args, status, needle):
     refused(lib, "moe_mxfp4_matmul", args, status, needle)
@@ -80,7 +81,7 @@ def test_matmul_refusals(lib, args, status, needle):
     ((P, 68, P, P, 4, 2, 16, 64, P, None), 2, "ldx must be a multiple of 8"),
     ((P, (1 << 20) + 8, P, P, 4, 2, 16, 64, P, None), 2, "ldx must be"),
     ((P, 64, None, P, 4, 2, 16, 64, P, None), 1, "w is null"),
-    ((P, 64, P, P + 4, 4, 2, 16, 64, P, None), 3, "offsets must be 16-byte aligned"),
+    ((P, 64, P, P + 2, 4, 2, 16, 64, P, None), 3, "offsets must be 4-byte aligned"),
 ])
 def test_grouped_matmul_refusals(lib, args, status, needle):
     refused(lib, "moe_grouped_matmul", args, status, needle)
@@ -157,6 +158,10 @@ def z(*shape, dtype=BF):
      "dw_dtype must be"),
     (lambda: moe.grouped_matmul_backward(z(4, 16), z(4, 64), z(2, 16, 64), z(3, dtype=I32), dx=z(3, 64)), 1,
      "dx must have shape (4, 64)"),
+    (lambda: moe.grouped_matmul_backward(z(4, 16), z(4, 64), z(2, 16, 64), z(3, dtype=I32), dx=z(4, 64), need_dx=False),
+     1, "dx is given, but need_dx is False"),
+    (lambda: moe.grouped_matmul_backward(z(4, 16), None, z(2, 16, 64), z(3, dtype=I32), dw=z(2, 16, 64), need_dw=False),
+     1, "dw is given, but need_dw is False"),
 ])
 def test_binding_refusals(lib, call, status, needle):
     with pytest.raises(moe.MoeError) as ei:
