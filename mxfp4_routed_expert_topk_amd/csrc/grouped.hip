@@ -4,7 +4,7 @@
 //   forward    y_r  = w_e x_r                       reduction over K
 //   dx         dx_r = dy_r w_e                      reduction over N
 //   dw         dw_e = sum over e's rows dy_r x_r^T  reduction over the rows
-// One tile kernel on v_mfma_f32_32x32x16_bf16 serves the three: an output tile
+// One tile kernel on v_mfma_f32_16x16x32_bf16 serves the three: an output tile
 // of BM x BN is the product of a row operand P (output rows) and a column
 // operand Q (output columns).  An operand
 // lies in memory either along its reduction ("plain": x and w forward, dy for
@@ -24,10 +24,11 @@
 //     chunks are permuted by swz below, which spreads a quarter-wave's
 //     ds_read_b128 over all 64 banks;
 //   crossed tile: STEP rows (the reduction) of BM or BN columns whose 64-byte
-//     units are permuted by unit ^ (row & 3): the four rows a transposed read
-//     takes lie in four different units, again all 64 banks.
+//     units are permuted by unit ^ (row & 3) and whose halves of a unit by
+//     (row >> 3) & 1: the eight rows that half a wave's transposed read takes
+//     lie in eight different halves, again all 64 banks.
 // Both operands number the reduction alike, so every output is one fp32 sum
-// in ascending order of 16 values an MFMA, whatever the tile.
+// in ascending order of 32 values an MFMA, whatever the tile.
 //
 // Q is the instruction's first operand: a lane then ends with four
 // consecutive columns of one output row, stored together.
@@ -39,7 +40,6 @@
 namespace moe {
 namespace {
 
-typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x8_t __attribute__((ext_vector_type(8)));
@@ -88,7 +88,7 @@ struct Operand {
   static constexpr int kPerRow = CROSSED ? kChunks : STEP / 8;   // chunks per staged row
   static constexpr int kRows = 64 / kPerRow;                     // staged rows per copy
   static constexpr int kApart = kRows * WAVES;
-  static_assert(kApart % 16 == 0 || (CROSSED && kApart % 4 == 0) || kCopies == 1, "the permutation repeats");
+  static_assert(kApart % 16 == 0 || kCopies == 1, "the permutation repeats");
   static constexpr int kOffs = CROSSED ? 1 : kCopies;
   uint32_t off[kOffs];     // byte offset of this lane's chunk at stage 0 (kPastEnd: not live)
   int red;                 // reduction index of its first value at stage 0 (of copy 0)
@@ -97,7 +97,7 @@ struct Operand {
       : base(b), ld(l), length(len), wave(w) {
     const int r = kRows * wave + lane / kPerRow;
     if constexpr (CROSSED) {
-      const int c = (lane % kPerRow) ^ ((r & 3) << 2);
+      const int c = (lane % kPerRow) ^ ((r & 3) << 2) ^ (((r >> 3) & 1) << 1);
       red = r;
       off[0] = 8 * c < count ? (uint32_t)((long long)r * ld * 2) + 16 * c : kPastEnd;
     } else {
@@ -119,17 +119,15 @@ struct Operand {
                                              at < length ? off[CROSSED ? 0 : j] : kPastEnd, 0, 0, NT ? 2 : 0);
   }
 
-  // MFMA operand of 32-row block b, 16-deep step k, from a staged tile
+  // MFMA operand of 16-row block b, 32-deep step k, from a staged tile
   static __device__ __forceinline__ bf16x8_t read(const uint8_t* buf, int b, int k, int lane) {
-    const int h = lane >> 5;
+    const int i = lane & 15, q = lane >> 4;   // row and the step's q-th eight values
     if constexpr (!CROSSED) {
-      const int r = lane & 31;
-      return *reinterpret_cast<const bf16x8_t*>(buf + (b * 32 + r) * (2 * STEP) + swz<STEP>(2 * k + h, r) * 16);
+      return *reinterpret_cast<const bf16x8_t*>(buf + (b * 16 + i) * (2 * STEP) + swz<STEP>(4 * k + q, i) * 16);
     } else {
       // lane i of 16 points at row i/4 and columns 4 (i%4).. of a 4 x 16 block
-      const int i = lane & 15, g = (lane >> 4) & 1;
-      const uint8_t* p = buf + (16 * k + 8 * h + (i >> 2)) * (B * 2) + ((b ^ (i >> 2)) * 4 + 2 * g + ((i >> 1) & 1)) * 16 +
-                         (i & 1) * 8;
+      const uint8_t* p = buf + (32 * k + 8 * q + (i >> 2)) * (B * 2) +
+                         (((b >> 1) ^ (i >> 2)) * 4 + 2 * ((b ^ q) & 1) + ((i >> 1) & 1)) * 16 + (i & 1) * 8;
       const s16x4_t lo = read_crossed(p), hi = read_crossed(p + 4 * (B * 2));
       const s16x8_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
       return __builtin_bit_cast(bf16x8_t, v);
@@ -239,35 +237,34 @@ constexpr int kLater = 32;
 template <class C, bool PX, bool QX, int LIVE>
 struct Reduce {
   static __device__ __forceinline__ void run(uint8_t* smem, const Operands<C, PX, QX>& o, int stages, int wm, int wn,
-                                             int lane, bool later, f32x16_t (&acc)[C::MI][C::NJ]) {
+                                             int lane, bool later, f32x4_t (&acc)[2 * C::MI][2 * C::NJ]) {
     using P = typename Operands<C, PX, QX>::P;
     using Q = typename Operands<C, PX, QX>::Q;
     constexpr int kG = P::kCopies + Q::kCopies;
     uint8_t* const ring_q = smem;
     uint8_t* const ring_p = smem + C::NQ * Q::kBytes;
 
-    // A stage has STEP / 16 steps, each a list of LIVE x NJ MFMAs.  Behind
-    // each MFMA stands a share of the LDS reads of the step after it and of
-    // the global copies: a run of reads would fill the LDS queue from eight
-    // waves at once and hold up the MFMAs behind it.  A stage's last list
-    // therefore runs after the next stage's barrier, over that stage's first
-    // reads.  Before the first stage its operands are zeros (0 * 0 leaves the
-    // accumulators at +0).
-    constexpr int kSteps = C::STEP / 16;
-    static_assert(kSteps % 2 == 0, "two operand sets in turn");
-    constexpr int kM = LIVE * C::NJ, kR = LIVE + C::NJ;   // MFMAs and operands of a step
-    constexpr int kM3 = kM ? 3 * kM : 1, kAhead = kM ? (4 * kR + kM3 - 1) / kM3 : 0;   // operands read behind an MFMA: done by 3/4 of them
+    // A stage has STEP / 32 steps, each two lists of MFMAs: the upper and the
+    // lower half of the wave's live 16-row blocks.  Behind each MFMA stands a
+    // share of the LDS reads of the list after it and of the global copies: a
+    // run of reads would fill the LDS queue from eight waves at once and hold
+    // up the MFMAs behind it.  A stage's last list therefore runs after the
+    // next stage's barrier, over that stage's first reads.  Before the first
+    // stage its operands are zeros (0 * 0 leaves the accumulators at +0).
+    constexpr int kSteps = C::STEP / 32;
+    static_assert(kSteps % 2 == 0, "two sets of Q operands in turn");
+    constexpr int kH = LIVE, kB = 2 * C::NJ, kM = kH * kB;   // P and Q blocks and MFMAs of a list
     // The copies stand in a stage's first quarter (P, needed one stage on) and
     // third quarter (Q): 1495 us for eight groups of 4096 x 4096 x 7168, 1504
     // with all of them in the first half, 1526 in the first quarter.  P's come
     // first, as the wait below counts.
-    constexpr int kQuarter = kSteps * kM / 4;
-    constexpr int kRows = LIVE ? LIVE : 1;
-    bf16x8_t fp[2][kRows], fq[2][C::NJ];
+    constexpr int kQuarter = 2 * kSteps * kM / 4;
+    constexpr int kRows = LIVE ? 2 * LIVE : 1;
+    bf16x8_t fp[kRows], fq[2][kB];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) fp[1][i] = bf16x8_t{};
+    for (int i = 0; i < kRows; ++i) fp[i] = bf16x8_t{};
 #pragma unroll
-    for (int j = 0; j < C::NJ; ++j) fq[1][j] = bf16x8_t{};
+    for (int j = 0; j < kB; ++j) fq[1][j] = bf16x8_t{};
     int iq = 0, ip = 0;   // stage s's tiles
     for (int s = 0; s < stages; ++s) {
       // this wave's copies of stage s have landed (what was issued after them
@@ -283,39 +280,46 @@ struct Reduce {
       const uint8_t* bp = ring_p + ip * P::kBytes;
       uint8_t* const to_q = ring_q + (iq ? iq - 1 : C::NQ - 1) * Q::kBytes;
       uint8_t* const to_p = ring_p + (ip ? ip - 1 : C::NP - 1) * P::kBytes;
+      auto row_block = [&](int i) { return 2 * ((i >> 1) * C::WM + wm) + (i & 1); };   // of the tile
       auto copy = [&](auto c) {
         constexpr int i = decltype(c)::value;
         if constexpr (i < P::kCopies) o.p.issue(to_p, s + C::NP - 1, i);
         else o.q.issue(to_q, s + C::NQ - 1, i - P::kCopies);
       };
-      unrolled<kSteps>([&](auto kc) {
-        // the MFMAs of the step before (the last one of stage s - 1 first) over the reads of step k
-        constexpr int k = decltype(kc)::value, now = (k + 1) % 2, then = k % 2;
+      unrolled<2 * kSteps>([&](auto hc) {
+        // the MFMAs of the list before (the last one of stage s - 1 first) over the reads of list h
+        constexpr int h = decltype(hc)::value, k = h / 2, half = h % 2;
+        constexpr int before = half ? k : (k + kSteps - 1) % kSteps;   // its step
+        constexpr int kR = half ? kH : kH + kB;                        // reads, over 3/4 of the MFMAs
         unrolled<kM>([&](auto mc) {
-          constexpr int m = decltype(mc)::value, i = m / C::NJ, j = m % C::NJ;
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fq[now][j], fp[now][i], acc[i][j], 0, 0, 0);
-          unrolled<kAhead>([&](auto rc) {   // q0, p0, the other q's, the other p's
-            constexpr int r = m * kAhead + decltype(rc)::value;
-            if constexpr (r == 1) fp[then][0] = P::read(bp, wm, k, lane);
-            else if constexpr (r <= C::NJ) fq[then][r ? r - 1 : 0] = Q::read(bq, wn * C::NJ + (r ? r - 1 : 0), k, lane);
-            else if constexpr (r < kR) fp[then][r - C::NJ] = P::read(bp, (r - C::NJ) * C::WM + wm, k, lane);
+          constexpr int m = decltype(mc)::value, i = (1 - half) * kH + m / kB, j = m % kB;
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[before % 2][j], fp[i], acc[i][j], 0, 0, 0);
+          unrolled<kR>([&](auto rc) {   // q0, p0, the other q's, the other p's
+            constexpr int r = decltype(rc)::value;
+            if constexpr (r * 3 * kM / (4 * kR) == m) {
+              constexpr int p = half ? r : r == 1 ? 0 : r - kB, q = r ? r - 1 : 0;
+              if constexpr (half || r == 1 || r > kB)
+                fp[half * kH + p] = P::read(bp, row_block(half * kH + p), k, lane);
+              else
+                fq[k % 2][q] = Q::read(bq, wn * kB + q, k, lane);
+            }
           });
           unrolled<kG>([&](auto cc) {
             constexpr int c = decltype(cc)::value, q = c - P::kCopies;
             constexpr int at = q < 0 ? c * kQuarter / P::kCopies : 2 * kQuarter + q * kQuarter / Q::kCopies;
-            if constexpr (at == k * kM + m) copy(cc);
+            if constexpr (at == h * kM + m) copy(cc);
           });
           __builtin_amdgcn_sched_barrier(0);
         });
       });
       if constexpr (LIVE == 0) unrolled<kG>([&](auto c) { copy(c); });
-      unrolled<kM>([&](auto m) { pin(acc[decltype(m)::value / C::NJ][decltype(m)::value % C::NJ][0]); });
+      unrolled<2 * kM>([&](auto m) { pin(acc[decltype(m)::value / kB][decltype(m)::value % kB][0]); });
       iq = iq + 1 == C::NQ ? 0 : iq + 1;
       ip = ip + 1 == C::NP ? 0 : ip + 1;
     }
     unrolled<kM>([&](auto mc) {
-      constexpr int m = decltype(mc)::value, i = m / C::NJ, j = m % C::NJ;
-      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fq[1][j], fp[1][i], acc[i][j], 0, 0, 0);
+      constexpr int m = decltype(mc)::value, i = kH + m / kB, j = m % kB;
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[1][j], fp[i], acc[i][j], 0, 0, 0);
     });
     MOE_WAIT_VM(0);   // the copies past the end still write LDS
   }
@@ -325,15 +329,13 @@ struct Reduce {
 // of the live row blocks.
 template <class C, bool PX, bool QX>
 __device__ __forceinline__ void multiply(uint8_t* smem, const Operands<C, PX, QX>& o, int rows, int length, int wave,
-                                         int lane, bool later, f32x16_t (&acc)[C::MI][C::NJ]) {
+                                         int lane, bool later, f32x4_t (&acc)[2 * C::MI][2 * C::NJ]) {
   const int wm = wave / C::WN, wn = wave % C::WN;
   const int stages = (length + C::STEP - 1) / C::STEP;
 #pragma unroll
-  for (int i = 0; i < C::MI; ++i)
+  for (int i = 0; i < 2 * C::MI; ++i)
 #pragma unroll
-    for (int j = 0; j < C::NJ; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    for (int j = 0; j < 2 * C::NJ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   static_assert(C::MI == 1 || C::MI == 2 || C::MI == 4, "cases below");
   const int blocks = (rows + 31) / 32, live = (blocks - wm + C::WM - 1) / C::WM;   // this wave's
   if (live >= C::MI) Reduce<C, PX, QX, C::MI>::run(smem, o, stages, wm, wn, lane, later, acc);
@@ -352,14 +354,14 @@ __device__ __forceinline__ void rings_free() {
 
 // Stores a tile: rows 0..rows-1, columns 0..cols-1 from `out` on.  STREAM: the
 // output passes the caches by.
-//   32x32 D layout with Q first: lane holds output row l%32, columns
-// 8 t + 4 (l/32) + [0, 4).  The wave's blocks pass through LDS (the rings' last
+//   16x16 D layout with Q first: lane holds output row l%16, columns
+// 4 (l/16) + [0, 4).  The wave's blocks pass through LDS (the rings' last
 // tiles, which a fill leaves alone), 32 rows at a time, and leave as whole
 // rows, 16 bytes a lane: stored from the MFMA layout a row's line would be
 // written in four parts (non-temporal stores of such parts took dw from 1.4 to
 // 4.4 ms).  Chunks are permuted by chunk ^ row, for the banks.
 template <class C, bool F32, bool STREAM>
-__device__ __forceinline__ void store_tile(uint8_t* smem, const f32x16_t (&acc)[C::MI][C::NJ], int rows, int cols,
+__device__ __forceinline__ void store_tile(uint8_t* smem, const f32x4_t (&acc)[2 * C::MI][2 * C::NJ], int rows, int cols,
                                            int wave, int lane, void* out, long long ldo) {
   // the addresses below are made anew for every tile: kept across a K loop in
   // registers (they do not change with it), they would be spilled
@@ -376,24 +378,21 @@ __device__ __forceinline__ void store_tile(uint8_t* smem, const f32x16_t (&acc)[
   // the last Q tile, and the end of the last P tile
   uint8_t* const stg = smem + (wave < kHalf ? (C::NQ - 1) * kQ + wave * (32 * kRowBytes)
                                             : C::kSmem - (wave - kHalf + 1) * (32 * kRowBytes));
-  const int h = lane >> 5, rl = lane & 31;
+  const int q = lane >> 4;
 #pragma unroll
   for (int i = 0; i < C::MI; ++i) {
     const int r0 = (i * C::WM + wm) * 32;
     if (r0 >= rows) break;
 #pragma unroll
-    for (int j = 0; j < C::NJ; ++j)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const f32x16_t& a = acc[i][j];
-        uint8_t* const at = stg + rl * kRowBytes;
-        if constexpr (F32) {
-          *reinterpret_cast<float4*>(at + place(rl, 8 * j + 2 * t + h)) =
-              make_float4(a[4 * t], a[4 * t + 1], a[4 * t + 2], a[4 * t + 3]);
-        } else {
-          *reinterpret_cast<uint2*>(at + place(rl, 4 * j + t) + 8 * h) =
-              make_uint2(bf16_pair(a[4 * t], a[4 * t + 1]), bf16_pair(a[4 * t + 2], a[4 * t + 3]));
-        }
+      for (int j = 0; j < 2 * C::NJ; ++j) {
+        const f32x4_t& a = acc[2 * i + h][j];
+        const int r = 16 * h + (lane & 15);
+        uint8_t* const at = stg + r * kRowBytes;
+        if constexpr (F32) *reinterpret_cast<f32x4_t*>(at + place(r, 4 * j + q)) = a;
+        else *reinterpret_cast<uint2*>(at + place(r, 2 * j + (q >> 1)) + 8 * (q & 1)) =
+            make_uint2(bf16_pair(a[0], a[1]), bf16_pair(a[2], a[3]));
       }
     asm volatile("" ::: "memory");
 #pragma unroll
@@ -442,7 +441,7 @@ __device__ __forceinline__ void rows_item(uint8_t* smem, const uint16_t* p, long
   using O = Operands<C, false, QX>;
   const O o = {typename O::P(p + (long long)t.row0 * ldp, ldp, t.rows, length, wave, lane),
                typename O::Q(QX ? we + c0 : we + (size_t)c0 * length, QX ? cols : length, live_cols, length, wave, lane)};
-  f32x16_t acc[C::MI][C::NJ];
+  f32x4_t acc[2 * C::MI][2 * C::NJ];
   o.fill(smem);
   multiply(smem, o, t.rows, length, wave, lane, false, acc);
   rings_free();
@@ -513,7 +512,7 @@ __device__ __forceinline__ void dw_share(uint8_t* smem, const BackwardArgs& a, i
   o.fill(smem);
   bool later = false;
   for (;;) {
-    f32x16_t acc[C::MI][C::NJ];
+    f32x4_t acc[2 * C::MI][2 * C::NJ];
     multiply(smem, o, t.rows, t.length, wave, lane, later, acc);
     rings_free();
     id += stride;
