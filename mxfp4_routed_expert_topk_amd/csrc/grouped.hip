@@ -429,7 +429,9 @@ __device__ __forceinline__ void rows_item(uint8_t* smem, const uint16_t* p, long
                                           const int32_t* offsets, int rows, int groups, int cols, int length, Deal d,
                                           uint16_t* out, int xcd, int i) {
   const int turn = i / d.share, slice = xcd % d.parts * d.share + i - turn * d.share;
-  const int tile = turn * (kXcds / d.parts) + xcd / d.parts;
+  // a turn's tiles go round: groups of 1.5 tiles would else give one XCD the
+  // full and another the half ones (dx of 32 groups of 384 rows: 821 -> 720 us)
+  const int turns = kXcds / d.parts, tile = turn * turns + (xcd / d.parts + turn) % turns;
   if (slice >= d.slices) return;
   const RowTiles tiles(offsets, groups, rows, C::BM, threadIdx.x & 63);
   if (tile >= tiles.total) return;
@@ -614,7 +616,7 @@ hipError_t launch_grouped_forward(const GroupedArgs& a, const void* x, int64_t l
 }
 
 // 256 x 256 tiles where they fill the CUs (32 groups of 384 rows, 4096 x 7168:
-// 2010 us against 2390 with 128 x 128), else 128 x 128 (8 groups of 75 rows,
+// 1870 us against 2390 with 128 x 128), else 128 x 128 (8 groups of 75 rows,
 // 768 x 1024: 19.1 against 11.7).
 hipError_t launch_grouped_backward(const GroupedArgs& a, const void* dy, int64_t lddy, const void* x, int64_t ldx,
                                    void* dx, bool f32, void* dw, hipStream_t stream) {
