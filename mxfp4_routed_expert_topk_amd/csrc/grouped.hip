@@ -20,9 +20,12 @@
 // the group, reduction past its length, columns past the matrix) get an
 // out-of-range offset, for which the copy writes zeros: no other group's row,
 // NaN or not, enters a sum.
-//   plain tile: rows of STEP reduction values (128 bytes or 64) whose 16-byte
-//     chunks are permuted by swz below, which spreads a quarter-wave's
-//     ds_read_b128 over all 64 banks;
+//   plain tile: rows of STEP reduction values (128 bytes, half the banks) whose
+//     16-byte chunks are permuted by chunk ^ (row >> 1).  The sixteen lanes that
+//     ds_read_b128 serves at once are eight rows of one chunk and the other
+//     eight of its neighbour (lanes 0-3, 12-15, 20-27): the eight even rows
+//     then take all eight places, and the odd ones.  (chunk ^ row ^ (row >> 3)
+//     is right for lanes in order only: every read took twice the cycles.)
 //   crossed tile: STEP rows (the reduction) of BM or BN columns whose 64-byte
 //     units are permuted by unit ^ (row & 3) and whose halves of a unit by
 //     (row >> 3) & 1: the eight rows that half a wave's transposed read takes
@@ -53,11 +56,8 @@ constexpr int kMaxRange = 0x7FFFFFFF;          // bytes a resource covers
 // vmcnt <= n and lgkmcnt 0
 #define MOE_WAIT_VM(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (7 << 4) | ((((n) >> 4) & 3) << 14))
 
-// LDS place of 16-byte chunk c in a plain tile's row r of STEP values.
-template <int STEP>
-__device__ __forceinline__ int swz(int c, int r) {
-  return STEP == 64 ? c ^ (r & 7) ^ ((r >> 3) & 1) : c ^ ((r >> 2) & 3);
-}
+// LDS place of 16-byte chunk c in a plain tile's row r.
+__device__ __forceinline__ int swz(int c, int r) { return c ^ ((r >> 1) & 7); }
 
 // Four reduction values of one column (see Operand::read).  The __restrict__
 // matters: without alias information on the read the compiler takes it to
@@ -101,7 +101,7 @@ struct Operand {
       red = r;
       off[0] = 8 * c < count ? (uint32_t)((long long)r * ld * 2) + 16 * c : kPastEnd;
     } else {
-      const int c = swz<STEP>(lane % kPerRow, r);
+      const int c = swz(lane % kPerRow, r);
       red = 8 * c;
 #pragma unroll
       for (int j = 0; j < kCopies; ++j)
@@ -123,7 +123,7 @@ struct Operand {
   static __device__ __forceinline__ bf16x8_t read(const uint8_t* buf, int b, int k, int lane) {
     const int i = lane & 15, q = lane >> 4;   // row and the step's q-th eight values
     if constexpr (!CROSSED) {
-      return *reinterpret_cast<const bf16x8_t*>(buf + (b * 16 + i) * (2 * STEP) + swz<STEP>(4 * k + q, i) * 16);
+      return *reinterpret_cast<const bf16x8_t*>(buf + (b * 16 + i) * (2 * STEP) + swz(4 * k + q, i) * 16);
     } else {
       // lane i of 16 points at row i/4 and columns 4 (i%4).. of a 4 x 16 block
       const uint8_t* p = buf + (32 * k + 8 * q + (i >> 2)) * (B * 2) +

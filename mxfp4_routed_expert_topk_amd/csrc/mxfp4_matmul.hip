@@ -115,8 +115,9 @@ __global__ __launch_bounds__(kSplit* kWave) void matmul_mxfp4_rows(const uint8_t
 // global -> LDS by buffer_load ... lds (8 rows per wave instruction) into one
 // of two buffers while the other multiplies.  (With 128 K a stage, half lines,
 // the copies took 62 us against 59 at 4096 x 4096 x 7168.)  The eight 16-byte
-// chunks of a staged row are permuted by chunk ^ (row & 7) ^ ((row >> 3) & 1):
-// the sixteen rows of a quarter-wave's ds_read_b128 then cover all 64 banks
+// chunks of a staged row are permuted by chunk ^ (row >> 1): the sixteen lanes
+// that ds_read_b128 serves at once, eight rows of one chunk and the other eight
+// of its neighbour (lanes 0-3, 12-15, 20-27), then cover all 64 banks
 // once.  Copies past an edge get an out-of-range offset and write zeros.
 // A pair of stages (512 K) has 16 scale bytes per row.  Thread t loads those
 // of row t one pair ahead, transposes them to four dwords (dword q: the bytes
@@ -129,7 +130,7 @@ constexpr uint32_t kPastEnd = 0x80000000u;   // beyond every buffer resource bel
 
 #define MOE_WAIT_VM(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (7 << 4) | ((((n) >> 4) & 3) << 14))
 
-__device__ __forceinline__ int swz(int c, int r) { return c ^ (r & 7) ^ ((r >> 3) & 1); }
+__device__ __forceinline__ int swz(int c, int r) { return c ^ ((r >> 1) & 7); }
 
 template <int BM_, int BN_, int WM_, int WN_>
 struct MxShape {
