@@ -204,6 +204,7 @@ struct Shape {
   static constexpr bool NT = NT_;
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STEP = STEP_, NP = NP_, NQ = NQ_;
   static constexpr int kWaves = WM * WN, kPerCU = PER_CU_;
+  static constexpr bool kAlone = kWaves * kPerCU == 4;   // a wave has its SIMD, and 512 registers, to itself
   static constexpr int MI = BM / WM / 32, NJ = BN / WN / 32;
   static constexpr int kSmem = 2 * STEP * (BM * NP + BN * NQ);
   static_assert(NQ >= NP && NP >= 2 && kPerCU * kSmem <= 160 * 1024, "rings fit");
@@ -254,10 +255,11 @@ struct Reduce {
     constexpr int kSteps = C::STEP / 32;
     static_assert(kSteps % 2 == 0, "two sets of Q operands in turn");
     constexpr int kH = LIVE, kB = 2 * C::NJ, kM = kH * kB;   // P and Q blocks and MFMAs of a list
-    // The copies stand in a stage's first quarter (P, needed one stage on) and
-    // third quarter (Q): 1495 us for eight groups of 4096 x 4096 x 7168, 1504
-    // with all of them in the first half, 1526 in the first quarter.  P's come
-    // first, as the wait below counts.
+    // With two waves a SIMD the copies stand in a stage's first quarter (P,
+    // needed one stage on) and third quarter (Q): 1431 us for eight groups of
+    // 4096 x 4096 x 7168, 1445 with all of them in the first half, 1471 over the
+    // whole stage; a wave alone takes that (1412 against 1422).  P's come first,
+    // as the wait below counts.
     constexpr int kQuarter = 2 * kSteps * kM / 4;
     constexpr int kRows = LIVE ? 2 * LIVE : 1;
     bf16x8_t fp[kRows], fq[2][kB];
@@ -265,6 +267,16 @@ struct Reduce {
     for (int i = 0; i < kRows; ++i) fp[i] = bf16x8_t{};
 #pragma unroll
     for (int j = 0; j < kB; ++j) fq[1][j] = bf16x8_t{};
+    // the accumulators stay where they are: those of a wave alone are 256, all
+    // of the AGPRs (unasked, the compiler moved them about: 2170 us for 1412)
+    auto keep = [&] {
+      unrolled<2 * kM>([&](auto mc) {
+        f32x4_t& a = acc[decltype(mc)::value / kB][decltype(mc)::value % kB];
+        if constexpr (C::kAlone) pin_agpr(a);
+        else pin(a[0]);
+      });
+    };
+    if constexpr (C::kAlone) keep();
     int iq = 0, ip = 0;   // stage s's tiles
     for (int s = 0; s < stages; ++s) {
       // this wave's copies of stage s have landed (what was issued after them
@@ -306,14 +318,16 @@ struct Reduce {
           });
           unrolled<kG>([&](auto cc) {
             constexpr int c = decltype(cc)::value, q = c - P::kCopies;
-            constexpr int at = q < 0 ? c * kQuarter / P::kCopies : 2 * kQuarter + q * kQuarter / Q::kCopies;
+            constexpr int at = C::kAlone ? c * 4 * kQuarter / kG
+                               : q < 0   ? c * kQuarter / P::kCopies
+                                         : 2 * kQuarter + q * kQuarter / Q::kCopies;
             if constexpr (at == h * kM + m) copy(cc);
           });
           __builtin_amdgcn_sched_barrier(0);
         });
       });
       if constexpr (LIVE == 0) unrolled<kG>([&](auto c) { copy(c); });
-      unrolled<2 * kM>([&](auto m) { pin(acc[decltype(m)::value / kB][decltype(m)::value % kB][0]); });
+      keep();
       iq = iq + 1 == C::NQ ? 0 : iq + 1;
       ip = ip + 1 == C::NP ? 0 : ip + 1;
     }
@@ -374,7 +388,6 @@ __device__ __forceinline__ void store_tile(uint8_t* smem, const f32x4_t (&acc)[2
   constexpr int kHalf = C::kWaves / 2, kQ = C::BN * C::STEP * 2, kP = C::BM * C::STEP * 2;   // waves, tile bytes
   static_assert(kHalf * 32 * kRowBytes <= kQ && kHalf * 32 * kRowBytes <= kP && 64 % kChunks == 0,
                 "a block of every wave fits");
-  static_assert(C::MI * kChunks / 2 <= kLater || !F32, "stores of a full tile");
   // the last Q tile, and the end of the last P tile
   uint8_t* const stg = smem + (wave < kHalf ? (C::NQ - 1) * kQ + wave * (32 * kRowBytes)
                                             : C::kSmem - (wave - kHalf + 1) * (32 * kRowBytes));
@@ -552,7 +565,8 @@ long long items_per_xcd(const GroupedArgs& a, int bm, const Deal& d) {
   return ((long long)a.rows / bm + std::min(a.groups, a.rows) + turns - 1) / turns * d.share;
 }
 
-using Large = Shape<256, 256, 2, 4, 64, 2, 3, 1>;
+template <int WN>
+using Large = Shape<256, 256, 2, WN, 64, 2, 3, 1>;
 template <bool NT>
 using Middle = Shape<128, 128, 2, 2, 64, 2, 3, 2, NT>;
 template <bool NT>
@@ -603,19 +617,23 @@ hipError_t launch_backward(const GroupedArgs& a, BackwardArgs b, bool f32, hipSt
 // groups of 2.7 rows, 2048 -> 7168: 927, 978, 1165), but a group of more rows
 // than a tile reads them again (32 rows each 574, 577, 625, Zipf-skewed 734,
 // 668, 709; 64 each 905, 624, 655, skewed 995, 809, 728; 128 each 1572, 944,
-// 729).  Grids that would leave CUs idle take the next smaller tile (600 rows
+// 729).  The 256-row tile has four waves of 128 x 128, which read two thirds of
+// what eight of 128 x 64 do from LDS (eight groups of 4096 rows, at the power
+// limit: 1412 against 1451 us).  Grids that would leave CUs idle take the next smaller tile (600 rows
 // in 8 groups, 768 -> 1024: 9.4, 10.9, 14.2).
 hipError_t launch_grouped_forward(const GroupedArgs& a, const void* x, int64_t ldx, void* y, hipStream_t stream) {
   const long long rows = a.rows;
   if (rows <= 16LL * a.groups) return launch_forward<Small<true>>(a, x, ldx, y, stream);
   if (rows <= 40LL * a.groups && items<Middle<true>>(a, a.n) >= 256)
     return launch_forward<Middle<true>>(a, x, ldx, y, stream);
-  if (rows > 40LL * a.groups && items<Large>(a, a.n) >= 256) return launch_forward<Large>(a, x, ldx, y, stream);
+  if (rows > 40LL * a.groups && items<Large<2>>(a, a.n) >= 256) return launch_forward<Large<2>>(a, x, ldx, y, stream);
   if (items<Middle<false>>(a, a.n) >= 256) return launch_forward<Middle<false>>(a, x, ldx, y, stream);
   return launch_forward<Small<false>>(a, x, ldx, y, stream);
 }
 
-// 256 x 256 tiles where they fill the CUs (32 groups of 384 rows, 4096 x 7168:
+// 256 x 256 tiles, in eight waves (four took 2038 us where eight took 1966:
+// dw's short sums and large stores leave a wave alone idle), where they fill
+// the CUs (32 groups of 384 rows, 4096 x 7168:
 // 1870 us against 2390 with 128 x 128), else 128 x 128 (8 groups of 75 rows,
 // 768 x 1024: 19.1 against 11.7).
 hipError_t launch_grouped_backward(const GroupedArgs& a, const void* dy, int64_t lddy, const void* x, int64_t ldx,
@@ -624,8 +642,8 @@ hipError_t launch_grouped_backward(const GroupedArgs& a, const void* dy, int64_t
                        static_cast<const uint16_t*>(a.w), lddy, ldx, a.offsets, a.rows, a.groups, a.n, a.k,
                        static_cast<uint16_t*>(dx), dw, {}, 0, 0, 0};
   const long long dw_tiles = (long long)a.groups * ((a.n + 255) / 256) * ((a.k + 255) / 256);
-  const bool large = dw ? dw_tiles >= 256 : items<Large>(a, a.k) >= 256 && a.rows > 40LL * a.groups;
-  return large ? launch_backward<Large>(a, b, f32, stream) : launch_backward<Middle<false>>(a, b, f32, stream);
+  const bool large = dw ? dw_tiles >= 256 : items<Large<4>>(a, a.k) >= 256 && a.rows > 40LL * a.groups;
+  return large ? launch_backward<Large<4>>(a, b, f32, stream) : launch_backward<Middle<false>>(a, b, f32, stream);
 }
 
 }  // namespace moe

@@ -217,6 +217,14 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 // operands in registers.
 __device__ __forceinline__ void pin(float v) { asm volatile("" ::"v"(v)); }
 
+// The same for an accumulator that stays in AGPRs (a constraint the host
+// compiler does not know).
+__device__ __forceinline__ void pin_agpr(f32x4_t& v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" : "+a"(v));
+#endif
+}
+
 // f(integral_constant 0) .. f(integral_constant N - 1)
 template <int N, int I = 0, class F>
 __device__ __forceinline__ void unrolled(F&& f) {
