@@ -612,15 +612,16 @@ hipError_t launch_backward(const GroupedArgs& a, BackwardArgs b, bool f32, hipSt
 }  // namespace
 
 // Tile by the rows a group has on average (64 groups, 7168 -> 4096, us with
-// 64-, 128- and 256-row tiles): few rows stream the weights, which two
-// workgroups per CU, non-temporal, do best (16 rows each: 552, 557, 615; at 224
-// groups of 2.7 rows, 2048 -> 7168: 927, 978, 1165), but a group of more rows
-// than a tile reads them again (32 rows each 574, 577, 625, Zipf-skewed 734,
-// 668, 709; 64 each 905, 624, 655, skewed 995, 809, 728; 128 each 1572, 944,
-// 729).  The 256-row tile has four waves of 128 x 128, which read two thirds of
-// what eight of 128 x 64 do from LDS (eight groups of 4096 rows, at the power
-// limit: 1412 against 1451 us).  Grids that would leave CUs idle take the next smaller tile (600 rows
-// in 8 groups, 768 -> 1024: 9.4, 10.9, 14.2).
+// 64-, 128- and 256-row tiles, the first two non-temporal): few rows stream the
+// weights, which two workgroups per CU, non-temporal, do best (16 rows each:
+// 550, 551, 612; 224 groups of 2.7 rows, 2048 -> 7168: 927, 988, 1135), but a
+// group of more rows than a tile reads them again (32 rows each 572, 578, 619,
+// Zipf-skewed 741, 681, 694; 64 each 888, 632, 640, skewed 1007, 842, 705; 128
+// each 1553, 1055, 691).  The 256-row tile has four waves of 128 x 128, which
+// read two thirds of what eight of 128 x 64 do from LDS (eight groups of 4096
+// rows, at the power limit: 1412 against 1451 us).  Grids that would leave CUs
+// idle take the next smaller tile (600 rows in 8 groups, 768 -> 1024: 8.2, 9.1,
+// 13.5).
 hipError_t launch_grouped_forward(const GroupedArgs& a, const void* x, int64_t ldx, void* y, hipStream_t stream) {
   const long long rows = a.rows;
   if (rows <= 16LL * a.groups) return launch_forward<Small<true>>(a, x, ldx, y, stream);
@@ -633,9 +634,9 @@ hipError_t launch_grouped_forward(const GroupedArgs& a, const void* x, int64_t l
 
 // 256 x 256 tiles, in eight waves (four took 2038 us where eight took 1966:
 // dw's short sums and large stores leave a wave alone idle), where they fill
-// the CUs (32 groups of 384 rows, 4096 x 7168:
-// 1870 us against 2390 with 128 x 128), else 128 x 128 (8 groups of 75 rows,
-// 768 x 1024: 19.1 against 11.7).
+// the CUs (32 groups of 384 rows, 4096 x 7168: 1870 us against 2390 with
+// 128 x 128), else 128 x 128 (8 groups of 75 rows, 768 x 1024: 19.1 against
+// 11.7).
 hipError_t launch_grouped_backward(const GroupedArgs& a, const void* dy, int64_t lddy, const void* x, int64_t ldx,
                                    void* dx, bool f32, void* dw, hipStream_t stream) {
   const BackwardArgs b{static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(x),
