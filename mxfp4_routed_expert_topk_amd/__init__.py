@@ -344,10 +344,12 @@ def _dtype_code(dtype, name: str) -> int:
 def _need_shape(t, name: str, dtype, shape, like):
     """Raise MoeError(MOE_ERR_ARG) unless `t` is a contiguous tensor of `dtype`
     and exactly `shape` on the device of the tensor `like`."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == like.get_device() and t.is_contiguous():
+            return
+    except AttributeError:   # not a tensor
+        pass
     import torch
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape \
-            and t.get_device() == like.get_device() and t.is_contiguous():
-        return
     if not isinstance(t, torch.Tensor):
         raise _arg_error(f"{name} must be a torch.Tensor, got {type(t).__name__}")
     if t.dtype != dtype:
@@ -362,6 +364,12 @@ def _need_shape(t, name: str, dtype, shape, like):
 def _rows(t, name: str, dtypes, cols: Optional[int], like):
     """The row stride (elements) of a matrix whose rows are contiguous;
     MoeError(MOE_ERR_ARG) otherwise."""
+    try:
+        if t.is_contiguous() and t.dtype in dtypes and t.dim() == 2 and (cols is None or t.shape[1] == cols) \
+                and (like is None or t.get_device() == like.get_device()):
+            return t.shape[1]
+    except AttributeError:   # not a tensor
+        pass
     import torch
     if not isinstance(t, torch.Tensor):
         raise _arg_error(f"{name} must be a torch.Tensor, got {type(t).__name__}")
@@ -371,8 +379,6 @@ def _rows(t, name: str, dtypes, cols: Optional[int], like):
         raise _arg_error(f"{name} must be [rows, {'cols' if cols is None else cols}], got shape {tuple(t.shape)}")
     if like is not None and t.get_device() != like.get_device():
         raise _arg_error(f"{name} must be on {like.device}, got {t.device}")
-    if t.is_contiguous():
-        return t.shape[1]
     row_stride, step = t.stride()
     if step != 1 and t.shape[1] > 1:
         raise _arg_error(f"the rows of {name} must be contiguous, got strides {t.stride()}")
@@ -459,10 +465,17 @@ def mxfp4_quantize(x, codes=None, scales=None, stream=None):
 def _mxfp4_operand(codes, scales, codes_name: str, scales_name: str, like):
     """(rows, K) of an MXFP4 operand, its tensors checked."""
     import torch
+    try:
+        rows, half = shape = codes.shape
+        if half and not half % 16 and codes.dtype is scales.dtype is torch.uint8 \
+                and scales.shape == (rows, half // 16) \
+                and codes.get_device() == scales.get_device() == like.get_device() \
+                and codes.is_contiguous() and scales.is_contiguous():
+            return rows, 2 * half
+    except (AttributeError, ValueError):   # not tensors, or not 2-D
+        pass
     if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
         raise _arg_error(f"{codes_name} must be a 2-D torch.Tensor [rows, cols/2]")
-    shape = codes.shape
-    rows, half = shape
     _need_shape(codes, codes_name, torch.uint8, shape, like)
     if half == 0 or half % 16:
         raise MoeError(MOE_ERR_SHAPE, f"{codes_name} must have a positive multiple of 16 columns, got {half}")
@@ -514,6 +527,13 @@ def mxfp4_matmul(a_codes, a_scales, b_codes, b_scales, dtype=None, out=None, str
 
 def _grouped(w, offsets):
     import torch
+    try:
+        groups, n, k = shape = w.shape
+        if w.dtype is torch.bfloat16 and offsets.dtype is torch.int32 and offsets.shape == (groups + 1,) \
+                and w.get_device() == offsets.get_device() and w.is_contiguous() and offsets.is_contiguous():
+            return shape
+    except (AttributeError, ValueError):   # not tensors, or w not 3-D
+        pass
     if not isinstance(w, torch.Tensor) or w.dim() != 3:
         raise _arg_error("w must be a 3-D torch.Tensor [num_groups, n, k]")
     _need_shape(w, "w", torch.bfloat16, w.shape, w)
