@@ -546,17 +546,19 @@ __device__ __forceinline__ void dw_share(uint8_t* smem, const BackwardArgs& a, i
   }
 }
 
-// Both gradients in one launch, an XCD's dw workgroups and then its dx items.
-// (Mixed in proportion, so that some CUs would write while others multiply,
-// 32 experts x 4096 x 7168 with 12288 rows took 2033 us; dw first 1977.)
-template <class C, bool F32, bool STREAM>
+// Both gradients in one launch, an XCD's dx items (tiles in shape X) and then
+// its dw workgroups, whose stores end the launch: 32 groups of 384 rows,
+// 4096 x 7168, take 1838 us, dw first 1860; 4 groups of 75 rows, 2048 x 1024,
+// 19.6 and 22.7.  (Mixed in proportion, so that some CUs would write while
+// others multiply, was no better than dw first.)
+template <class C, class X, bool F32, bool STREAM>
 __global__ __launch_bounds__(C::kWaves* kWave, C::kPerCU* C::kWaves / 4) void grouped_backward(BackwardArgs a) {
-  __shared__ __align__(1024) uint8_t smem[C::kSmem];
+  static_assert(C::kWaves == X::kWaves, "one workgroup size");
+  __shared__ __align__(1024) uint8_t smem[C::kSmem > X::kSmem ? C::kSmem : X::kSmem];
   const int xcd = blockIdx.x % kXcds, i = blockIdx.x / kXcds;
-  if (i < a.dw_groups) dw_share<C, F32, STREAM>(smem, a, xcd, i, a.dw_groups);
-  else
-    rows_item<C, true>(smem, a.dy, a.lddy, a.w, a.offsets, a.rows, a.groups, a.k, a.n, a.dx_deal, a.dx, xcd,
-                       i - a.dw_groups);
+  if (i < a.dx_items)
+    rows_item<X, true>(smem, a.dy, a.lddy, a.w, a.offsets, a.rows, a.groups, a.k, a.n, a.dx_deal, a.dx, xcd, i);
+  else dw_share<C, F32, STREAM>(smem, a, xcd, i - a.dx_items, a.dw_groups);
 }
 
 // items per XCD there can be with row tiles of bm rows
@@ -590,10 +592,10 @@ hipError_t launch_forward(const GroupedArgs& a, const void* x, int64_t ldx, void
   return hipGetLastError();
 }
 
-template <class C>
+template <class C, class X>
 hipError_t launch_backward(const GroupedArgs& a, BackwardArgs b, bool f32, hipStream_t stream) {
-  b.dx_deal = deal((a.k + C::BN - 1) / C::BN);
-  b.dx_items = b.dx ? (int)items_per_xcd(a, C::BM, b.dx_deal) : 0;
+  b.dx_deal = deal((a.k + X::BN - 1) / X::BN);
+  b.dx_items = b.dx ? (int)items_per_xcd(a, X::BM, b.dx_deal) : 0;
   const long long dw_tiles = (long long)a.groups * ((a.n + C::BM - 1) / C::BM) * ((a.k + C::BN - 1) / C::BN);
   b.dw_items = b.dw ? (int)((dw_tiles + kXcds - 1) / kXcds) : 0;
   b.dw_groups = std::min(b.dw_items, kCusPerXcd * C::kPerCU);   // as many as run at once
@@ -604,8 +606,8 @@ hipError_t launch_backward(const GroupedArgs& a, BackwardArgs b, bool f32, hipSt
   auto run = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)(b.dx_items + b.dw_groups) * kXcds), dim3(C::kWaves * kWave), 0, stream, b);
   };
-  if (f32) run(stream_out ? grouped_backward<C, true, true> : grouped_backward<C, true, false>);
-  else run(stream_out ? grouped_backward<C, false, true> : grouped_backward<C, false, false>);
+  if (f32) run(stream_out ? grouped_backward<C, X, true, true> : grouped_backward<C, X, true, false>);
+  else run(stream_out ? grouped_backward<C, X, false, true> : grouped_backward<C, X, false, false>);
   return hipGetLastError();
 }
 
@@ -636,7 +638,10 @@ hipError_t launch_grouped_forward(const GroupedArgs& a, const void* x, int64_t l
 // dw's short sums and large stores leave a wave alone idle), where they fill
 // the CUs (32 groups of 384 rows, 4096 x 7168: 1870 us against 2390 with
 // 128 x 128), else 128 x 128 (8 groups of 75 rows, 768 x 1024: 19.1 against
-// 11.7).
+// 11.7).  dx takes 64-row tiles, whose rings are deeper, where those leave CUs
+// to dw or to more of them (dx alone, 8 groups of 75 rows and of 256, 768 x
+// 1024: 7.6 against 9.6 us and 8.6 against 10.4; with dw 10.8 against 11.6, but
+// 14.9 against 13.2).
 hipError_t launch_grouped_backward(const GroupedArgs& a, const void* dy, int64_t lddy, const void* x, int64_t ldx,
                                    void* dx, bool f32, void* dw, hipStream_t stream) {
   const BackwardArgs b{static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(x),
@@ -644,7 +649,10 @@ hipError_t launch_grouped_backward(const GroupedArgs& a, const void* dy, int64_t
                        static_cast<uint16_t*>(dx), dw, {}, 0, 0, 0};
   const long long dw_tiles = (long long)a.groups * ((a.n + 255) / 256) * ((a.k + 255) / 256);
   const bool large = dw ? dw_tiles >= 256 : items<Large<4>>(a, a.k) >= 256 && a.rows > 40LL * a.groups;
-  return large ? launch_backward<Large<4>>(a, b, f32, stream) : launch_backward<Middle<false>>(a, b, f32, stream);
+  if (large) return launch_backward<Large<4>, Large<4>>(a, b, f32, stream);
+  if (items<Small<false>>(a, a.k) <= (dw ? 256 : 512))
+    return launch_backward<Middle<false>, Small<false>>(a, b, f32, stream);
+  return launch_backward<Middle<false>, Middle<false>>(a, b, f32, stream);
 }
 
 }  // namespace moe
