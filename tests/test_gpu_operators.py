@@ -225,6 +225,8 @@ GROUPED = [   # counts, n, k, rows before and behind the groups
     ([20] * 10, 5512, 136, 1, 1),
     ([100, 60], 16392, 40, 0, 0),
     ([130, 0, 7, 260, 33], 2000, 1800, 2, 2),   # 256 x 256 tiles backward
+    ([353, 417, 33, 200, 129], 9480, 136, 1, 0),   # 256 x 256 tiles forward, every number of live row blocks
+    ([700, 500, 333], 264, 2600, 0, 1),   # 128 x 128 tiles for both gradients
 ]
 
 
@@ -281,6 +283,17 @@ def test_grouped_one_gradient_only():
     only_dw = moe.grouped_matmul_backward(*args, need_dx=False)
     assert only_dx[1] is None and torch.equal(only_dx[0], dx)
     assert only_dw[0] is None and torch.equal(only_dw[1], dw)
+
+
+@pytest.mark.parametrize("counts,n,k", [([700, 500, 333], 264, 2600), ([353, 417, 33, 200, 129], 136, 9480)])
+def test_grouped_one_gradient_in_other_tiles(counts, n, k):
+    """A gradient alone may take other tiles than both: the sums are the same."""
+    off, x, dy, w = grouped_case(counts, n, k, 0, 0, 4)
+    args = [up(t, BF) for t in (dy, x, w)] + [up(off)]
+    dx, dw = moe.grouped_matmul_backward(*args)
+    assert torch.equal(moe.grouped_matmul_backward(args[0], None, args[2], args[3], need_dw=False)[0], dx)
+    assert torch.equal(moe.grouped_matmul_backward(*args, need_dx=False)[1], dw)
+    np.testing.assert_array_equal(f64(dx), bf16_rounded(oracle.grouped_matmul_backward(dy, x, w, off, np.zeros(x.shape))[0]))
 
 
 @pytest.mark.parametrize("counts,n,k", [([40, 0, 90], 256, 1024), ([700, 3, 41], 520, 2048), ([5, 0, 1, 17], 512, 7168)])
