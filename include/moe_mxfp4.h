@@ -284,23 +284,31 @@ moe_status moe_mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, con
  *   out     [rows, n] bf16: out_r = w_e x_r, summed in fp32 and rounded once;
  *           rows outside every group are not written
  * n and k multiples of 8 in [8, 65536], num_groups <= 4096, rows <= 2^24, row
- * strides multiples of 8 up to 2^20.  Enqueue-only, no workspace. */
+ * strides multiples of 8 up to 2^20.  Enqueue-only.
+ *   workspace  NULL, or device memory of moe_grouped_matmul_workspace bytes (0
+ *           for most sizes) that nothing else uses until the call has run: few
+ *           rows and columns with a long sum are then summed in parts, in a
+ *           second launch joined in order, which spreads them over the GPU */
+size_t moe_grouped_matmul_workspace(int32_t rows, int32_t num_groups, int32_t n, int32_t k);
 moe_status moe_grouped_matmul(const uint16_t* x, int64_t ldx, const uint16_t* w, const int32_t* offsets, int32_t rows,
-                              int32_t num_groups, int32_t n, int32_t k, uint16_t* out, hipStream_t stream);
+                              int32_t num_groups, int32_t n, int32_t k, uint16_t* out, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream);
 
 /* Gradients of moe_grouped_matmul for dy [rows, n] bf16 (rows lddy apart), in
- * one launch:
+ * one launch (more where a sum is split, as above):
  *   dx [rows, k] bf16 or NULL: dx_r = w_e^T dy_r; rows outside every group are
  *      not written
  *   dw [num_groups, n, k] of `dw_dtype` or NULL: dw_e = sum over e's rows of
  *      dy_r x_r^T, every element written (zero for an empty group)
  * A NULL gradient is not computed; w is read for dx only, x for dw only, and
  * either may be NULL where it is not read.  Each output is one fp32 sum in a
- * fixed order, rounded once (no atomics).  Enqueue-only, no workspace. */
+ * fixed order, rounded once (no atomics).  Enqueue-only. */
+size_t moe_grouped_matmul_backward_workspace(int32_t rows, int32_t num_groups, int32_t n, int32_t k, int32_t need_dx,
+                                             int32_t need_dw);
 moe_status moe_grouped_matmul_backward(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx,
                                        const uint16_t* w, const int32_t* offsets, int32_t rows, int32_t num_groups,
                                        int32_t n, int32_t k, uint16_t* dx, void* dw, int32_t dw_dtype,
-                                       hipStream_t stream);
+                                       void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Peak micro-benchmarks: the measured ceilings a benchmark reports its
  * kernels against beside the published peaks (the pages record each run's

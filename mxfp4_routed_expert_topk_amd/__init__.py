@@ -44,10 +44,11 @@ EXPORTS = ("moe_mxfp4_query_sizes", "moe_mxfp4_plan", "moe_mxfp4_forward", "moe_
            "moe_mxfp4_forward_fused",
            "moe_mxfp4_fused_status", "moe_mxfp4_route", "moe_mxfp4_workspace_region", "moe_mxfp8_quantize",
            "moe_router_topk", "moe_mxfp4_quantize", "moe_mxfp4_dequantize", "moe_mxfp4_matmul",
-           "moe_grouped_matmul", "moe_grouped_matmul_backward", "moe_probe_memory", "moe_probe_mfma", "moe_probe_mfma_f8f4_blocks",
+           "moe_grouped_matmul", "moe_grouped_matmul_backward", "moe_grouped_matmul_workspace",
+           "moe_grouped_matmul_backward_workspace", "moe_probe_memory", "moe_probe_mfma", "moe_probe_mfma_f8f4_blocks",
            "moe_mxfp4_set_stage_events",
            "moe_mxfp4_destroy", "moe_mxfp4_last_error")
-_STATUS_FNS = tuple(n for n in EXPORTS if n not in ("moe_mxfp4_destroy", "moe_mxfp4_last_error"))
+_STATUS_FNS = tuple(n for n in EXPORTS if n not in ("moe_mxfp4_destroy", "moe_mxfp4_last_error") and not n.endswith("_workspace"))
 
 
 class MoeError(RuntimeError):
@@ -103,8 +104,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_mxfp4_quantize.argtypes = [vp, i32, i32, i32, i64, vp, vp, vp]
     lib.moe_mxfp4_dequantize.argtypes = [vp, vp, i32, i32, i32, vp, vp]
     lib.moe_mxfp4_matmul.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp]
-    lib.moe_grouped_matmul.argtypes = [vp, i64, vp, vp, i32, i32, i32, i32, vp, vp]
-    lib.moe_grouped_matmul_backward.argtypes = [vp, i64, vp, i64, vp, vp, i32, i32, i32, i32, vp, vp, i32, vp]
+    lib.moe_grouped_matmul.argtypes = [vp, i64, vp, vp, i32, i32, i32, i32, vp, vp, sz, vp]
+    lib.moe_grouped_matmul_backward.argtypes = [vp, i64, vp, i64, vp, vp, i32, i32, i32, i32, vp, vp, i32, vp, sz, vp]
+    lib.moe_grouped_matmul_workspace.argtypes = [i32] * 4
+    lib.moe_grouped_matmul_backward_workspace.argtypes = [i32] * 6
+    lib.moe_grouped_matmul_workspace.restype = lib.moe_grouped_matmul_backward_workspace.restype = sz
     lib.moe_probe_memory.argtypes = [i32, vp, vp, sz, vp, i32, vp]
     lib.moe_probe_mfma.argtypes = [i32, i32, vp, i32, ctypes.POINTER(ctypes.c_double), vp]
     lib.moe_probe_mfma_f8f4_blocks.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp]
@@ -556,9 +560,16 @@ def grouped_matmul(x, w, offsets, out=None, stream=None):
     else:
         _need_shape(out, "out", torch.bfloat16, (rows, n), w)
         _apart(out, "out", ("x", x), ("w", w), ("offsets", offsets))
-    _launch(load_library().moe_grouped_matmul,
-            (x.data_ptr(), ld, w.data_ptr(), offsets.data_ptr(), rows, groups, n, k, out.data_ptr()), w, stream,
-            (x, w, offsets, out))
+    lib, used, space, size = load_library(), (x, w, offsets, out), None, 0
+    if k > 3000:   # a shorter sum is never split
+        size = lib.moe_grouped_matmul_workspace(rows, groups, n, k)
+        if size:
+            space = _new((size,), torch.uint8, x, stream)
+            used += (space,)
+            space = space.data_ptr()
+    _launch(lib.moe_grouped_matmul,
+            (x.data_ptr(), ld, w.data_ptr(), offsets.data_ptr(), rows, groups, n, k, out.data_ptr(), space, size), w,
+            stream, used)
     return out
 
 
@@ -599,9 +610,16 @@ def grouped_matmul_backward(dy, x, w, offsets, dx=None, dw=None, dw_dtype=None, 
         used.append(dx)
     elif dx is not None:
         raise _arg_error("dx is given, but need_dx is False")
-    _launch(load_library().moe_grouped_matmul_backward,
-            (dy.data_ptr(), lddy, x_at, ldx, w.data_ptr(), offsets.data_ptr(), rows, groups, n, k, dx_at, dw_at, code),
-            w, stream, used)
+    lib, space = load_library(), None
+    size = 0
+    if n > 3000 or rows > 3000 * groups:   # shorter sums are never split
+        size = lib.moe_grouped_matmul_backward_workspace(rows, groups, n, k, need_dx, need_dw)
+    if size:
+        used.append(_new((size,), torch.uint8, w, stream))
+        space = used[-1].data_ptr()
+    _launch(lib.moe_grouped_matmul_backward,
+            (dy.data_ptr(), lddy, x_at, ldx, w.data_ptr(), offsets.data_ptr(), rows, groups, n, k, dx_at, dw_at, code,
+             space, size), w, stream, used)
     return dx, dw
 
 

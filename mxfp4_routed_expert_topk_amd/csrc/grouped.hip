@@ -436,40 +436,105 @@ inline Deal deal(int slices) {
   return {slices, parts, (slices + parts - 1) / parts};
 }
 
-// Item i of XCD `xcd`'s list.
-template <class C, bool QX>
-__device__ __forceinline__ void rows_item(uint8_t* smem, const uint16_t* p, long long ldp, const uint16_t* w,
-                                          const int32_t* offsets, int rows, int groups, int cols, int length, Deal d,
-                                          uint16_t* out, int xcd, int i) {
-  const int turn = i / d.share, slice = xcd % d.parts * d.share + i - turn * d.share;
+// Item i of XCD `xcd`'s list: its row tile and column slice; false past the end.
+template <class C>
+__device__ __forceinline__ bool rows_place(const int32_t* offsets, int rows, int groups, const Deal& d, int xcd, int i,
+                                           Tile& t, int& slice) {
+  const int turn = i / d.share;
+  slice = xcd % d.parts * d.share + i - turn * d.share;
   // a turn's tiles go round: groups of 1.5 tiles would else give one XCD the
   // full and another the half ones (dx of 32 groups of 384 rows: 821 -> 720 us)
   const int turns = kXcds / d.parts, tile = turn * turns + (xcd / d.parts + turn) % turns;
-  if (slice >= d.slices) return;
+  if (slice >= d.slices) return false;
   const RowTiles tiles(offsets, groups, rows, C::BM, threadIdx.x & 63);
-  if (tile >= tiles.total) return;
-  const Tile t = tiles.place(tile);
-  const int c0 = slice * C::BN;
-  const uint16_t* we = w + (size_t)t.e * cols * length;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int live_cols = min(C::BN, cols - c0);
-  using O = Operands<C, false, QX>;
-  const O o = {typename O::P(p + (long long)t.row0 * ldp, ldp, t.rows, length, wave, lane),
-               typename O::Q(QX ? we + c0 : we + (size_t)c0 * length, QX ? cols : length, live_cols, length, wave, lane)};
-  f32x4_t acc[2 * C::MI][2 * C::NJ];
-  o.fill(smem);
-  multiply(smem, o, t.rows, length, wave, lane, false, acc);
-  rings_free();
-  store_tile<C, false, false>(smem, acc, t.rows, live_cols, wave, lane, out + (long long)t.row0 * cols + c0, cols);
+  if (tile >= tiles.total) return false;
+  t = tiles.place(tile);
+  return true;
+}
+
+// A reduction in `parts` parts of whole stages: part `part` of one of `length`.
+template <int STEP>
+__device__ __forceinline__ void part_range(int length, int parts, int part, int& from, int& len) {
+  const int per = ((length + STEP - 1) / STEP + parts - 1) / parts * STEP;
+  from = min(part * per, length);
+  len = min(length - from, per);
+}
+
+// SPLIT: item i / parts, the part i % parts of its reduction, to `partial`
+// [parts, rows, cols].
+template <class C, bool QX, bool SPLIT>
+struct RowsItem {
+  static __device__ __forceinline__ void run(uint8_t* smem, const uint16_t* p, long long ldp, const uint16_t* w,
+                                            const int32_t* offsets, int rows, int groups, int cols, int length, Deal d,
+                                            uint16_t* out, int parts, float* partial, int xcd, int i) {
+    Tile t;
+    int slice, from = 0, len = length;
+    const int part = SPLIT ? i % parts : 0;
+    if (!rows_place<C>(offsets, rows, groups, d, xcd, SPLIT ? i / parts : i, t, slice)) return;
+    if (SPLIT) part_range<C::STEP>(length, parts, part, from, len);
+    const int c0 = slice * C::BN;
+    const uint16_t* we = w + (size_t)t.e * cols * length + (QX ? (size_t)from * cols + c0 : (size_t)c0 * length + from);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int live_cols = min(C::BN, cols - c0);
+    using O = Operands<C, false, QX>;
+    const O o = {typename O::P(p + (long long)t.row0 * ldp + from, ldp, t.rows, len, wave, lane),
+                 typename O::Q(we, QX ? cols : length, live_cols, len, wave, lane)};
+    f32x4_t acc[2 * C::MI][2 * C::NJ];
+    o.fill(smem);
+    multiply(smem, o, t.rows, len, wave, lane, false, acc);
+    rings_free();
+    if constexpr (SPLIT)
+      store_tile<C, true, false>(smem, acc, t.rows, live_cols, wave, lane,
+                                 partial + ((size_t)part * rows + t.row0) * cols + c0, cols);
+    else
+      store_tile<C, false, false>(smem, acc, t.rows, live_cols, wave, lane, out + (long long)t.row0 * cols + c0, cols);
+  }
+};
+
+// The sum of `parts` values `stride` apart, in the parts' order.
+__device__ __forceinline__ f32x4_t join(const float* p, size_t stride, int parts) {
+  f32x4_t v = *reinterpret_cast<const f32x4_t*>(p);
+  for (int i = 1; i < parts; ++i) v += *reinterpret_cast<const f32x4_t*>(p + i * stride);
+  return v;
+}
+__device__ __forceinline__ uint2 bf16_quad(f32x4_t v) {
+  return make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+}
+
+// Joins the parts of every item of the same deal: rows outside every group are
+// left alone here too.
+template <class C>
+__global__ __launch_bounds__(C::kWaves* kWave) void grouped_join_rows(const float* partial, int parts,
+                                                                      const int32_t* offsets, int rows, int groups,
+                                                                      int cols, Deal d, uint16_t* out) {
+  Tile t;
+  int slice;
+  if (!rows_place<C>(offsets, rows, groups, d, blockIdx.x % kXcds, blockIdx.x / kXcds, t, slice)) return;
+  const int c0 = slice * C::BN, quads = min(C::BN, cols - c0) / 4;
+  for (int i = threadIdx.x; i < t.rows * quads; i += C::kWaves * kWave) {
+    const int r = i / quads;
+    const size_t at = (size_t)(t.row0 + r) * cols + c0 + 4 * (i - r * quads);
+    *reinterpret_cast<uint2*>(out + at) = bf16_quad(join(partial + at, (size_t)rows * cols, parts));
+  }
+}
+
+template <bool F32>
+__global__ __launch_bounds__(256) void grouped_join_dw(const float* partial, int parts, size_t total, void* dw) {
+  const size_t at = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (at >= total) return;   // a multiple of 64
+  const f32x4_t v = join(partial + at, total, parts);
+  if constexpr (F32) *reinterpret_cast<f32x4_t*>(static_cast<float*>(dw) + at) = v;
+  else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(dw) + at) = bf16_quad(v);
 }
 
 // y = x w_e^T
-template <class C>
+template <class C, bool SPLIT>
 __global__ __launch_bounds__(C::kWaves* kWave, C::kPerCU* C::kWaves / 4) void grouped_forward(
     const uint16_t* x, long long ldx, const uint16_t* w, const int32_t* offsets, int rows, int groups, int n, int k,
-    Deal d, uint16_t* out) {
+    Deal d, uint16_t* out, int parts, float* partial) {
   __shared__ __align__(1024) uint8_t smem[C::kSmem];
-  rows_item<C, false>(smem, x, ldx, w, offsets, rows, groups, n, k, d, out, blockIdx.x % kXcds, blockIdx.x / kXcds);
+  RowsItem<C, false, SPLIT>::run(smem, x, ldx, w, offsets, rows, groups, n, k, d, out, parts, partial, blockIdx.x % kXcds,
+                             blockIdx.x / kXcds);
 }
 
 struct BackwardArgs {
@@ -482,12 +547,14 @@ struct BackwardArgs {
   Deal dx_deal;
   int dx_items, dw_items;   // per XCD (dx: at most)
   int dw_groups;            // workgroups that share an XCD's dw items
+  int dx_parts, dw_parts;   // parts of a reduction, each a dx or dw item
+  float *dx_partial, *dw_partial;   // [parts] dx and dw in fp32
 };
 
 // Tile `id` of dw: a group's tiles in bands of eight tile rows, whose
 // concurrent ones share their columns of dy and x.
 struct DwTile {
-  int e, n0, k0, lo, length, rows, cols;
+  int e, n0, k0, lo, length, rows, cols, part;
 };
 template <class C>
 __device__ __forceinline__ DwTile dw_tile(const BackwardArgs& a, int id) {
@@ -510,11 +577,23 @@ __device__ __forceinline__ DwTile dw_tile(const BackwardArgs& a, int id) {
 // XCD's share.  A tile is short (384 rows are six stages) and its output large
 // (256 KB in fp32), so the next tile's rings are filled before this one is
 // stored: the fill's latency and the stores overlap.
-template <class C, bool F32, bool STREAM>
+template <class C, bool F32, bool STREAM, bool SPLIT>
 __device__ __forceinline__ void dw_share(uint8_t* smem, const BackwardArgs& a, int xcd, int i, int stride) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int per = ((a.n + C::BM - 1) / C::BM) * ((a.k + C::BN - 1) / C::BN);
-  const int end = min((xcd + 1) * a.dw_items, a.groups * per);
+  const int parts = SPLIT ? a.dw_parts : 1, end = min((xcd + 1) * a.dw_items, a.groups * per * parts);
+  auto tile = [&](int id) {
+    DwTile t = dw_tile<C>(a, SPLIT ? id / parts : id);
+    t.part = 0;
+    if (SPLIT) {
+      int from, len;
+      t.part = id % parts;
+      part_range<C::STEP>(t.length, parts, t.part, from, len);
+      t.lo += from;
+      t.length = len;
+    }
+    return t;
+  };
   int id = xcd * a.dw_items + i;
   if (id >= end) return;
   using O = Operands<C, true, true>;
@@ -522,7 +601,7 @@ __device__ __forceinline__ void dw_share(uint8_t* smem, const BackwardArgs& a, i
     return O{typename O::P(a.dy + (long long)t.lo * a.lddy + t.n0, a.lddy, t.rows, t.length, wave, lane),
              typename O::Q(a.x + (long long)t.lo * a.ldx + t.k0, a.ldx, t.cols, t.length, wave, lane)};
   };
-  DwTile t = dw_tile<C>(a, id);
+  DwTile t = tile(id);
   O o = operands(t);
   o.fill(smem);
   bool later = false;
@@ -533,12 +612,13 @@ __device__ __forceinline__ void dw_share(uint8_t* smem, const BackwardArgs& a, i
     id += stride;
     const DwTile done = t;
     if (id < end) {
-      t = dw_tile<C>(a, id);
+      t = tile(id);
       o = operands(t);
       o.fill(smem);
     }
-    const size_t at = ((size_t)done.e * a.n + done.n0) * a.k + done.k0;
-    void* to = F32 ? static_cast<void*>(static_cast<float*>(a.dw) + at) : static_cast<void*>(static_cast<uint16_t*>(a.dw) + at);
+    const size_t at = ((size_t)(done.part * a.groups + done.e) * a.n + done.n0) * a.k + done.k0;
+    float* const f32 = SPLIT ? a.dw_partial : static_cast<float*>(a.dw);
+    void* to = F32 ? static_cast<void*>(f32 + at) : static_cast<void*>(static_cast<uint16_t*>(a.dw) + at);
     store_tile<C, F32, STREAM>(smem, acc, done.rows, done.cols, wave, lane, to, a.k);
     if (id >= end) return;
     // every store of a full tile was issued, so the next K loop's first wait need not cover them
@@ -551,14 +631,15 @@ __device__ __forceinline__ void dw_share(uint8_t* smem, const BackwardArgs& a, i
 // 4096 x 7168, take 1838 us, dw first 1860; 4 groups of 75 rows, 2048 x 1024,
 // 19.6 and 22.7.  (Mixed in proportion, so that some CUs would write while
 // others multiply, was no better than dw first.)
-template <class C, class X, bool F32, bool STREAM>
+template <class C, class X, bool F32, bool STREAM, bool SPLIT_DX, bool SPLIT_DW>
 __global__ __launch_bounds__(C::kWaves* kWave, C::kPerCU* C::kWaves / 4) void grouped_backward(BackwardArgs a) {
   static_assert(C::kWaves == X::kWaves, "one workgroup size");
   __shared__ __align__(1024) uint8_t smem[C::kSmem > X::kSmem ? C::kSmem : X::kSmem];
   const int xcd = blockIdx.x % kXcds, i = blockIdx.x / kXcds;
   if (i < a.dx_items)
-    rows_item<X, true>(smem, a.dy, a.lddy, a.w, a.offsets, a.rows, a.groups, a.k, a.n, a.dx_deal, a.dx, xcd, i);
-  else dw_share<C, F32, STREAM>(smem, a, xcd, i - a.dx_items, a.dw_groups);
+    RowsItem<X, true, SPLIT_DX>::run(smem, a.dy, a.lddy, a.w, a.offsets, a.rows, a.groups, a.k, a.n, a.dx_deal, a.dx,
+                                 a.dx_parts, a.dx_partial, xcd, i);
+  else dw_share<C, F32, STREAM, SPLIT_DW>(smem, a, xcd, i - a.dx_items, a.dw_groups);
 }
 
 // items per XCD there can be with row tiles of bm rows
@@ -580,38 +661,101 @@ long long items(const GroupedArgs& a, int cols) {
   return ((long long)a.rows / C::BM + (std::min(a.groups, a.rows) + 1) / 2) * ((cols + C::BN - 1) / C::BN);
 }
 
+// Parts of a reduction of `stages` stages for a launch of `items` workgroups:
+// few items leave CUs idle, each taking 0.3 us a stage (dw 0.5).  The second
+// launch and the workspace cost the host 5 us, so only long sums gain (718 rows,
+// 6672 -> 64, 12 items of 105 stages: 28.9 -> 14.6 us; dw of 6566 rows, 584 x
+// 184, 10 of 103: 58 -> 19; dx of 100 rows in two groups, 4096 x 512, 8 of 64:
+// 24.9 -> 16.7), not short ones (300 rows in two groups, 2048 -> 2048, 32
+// stages: 12.7 -> 20.6) or many items, which fill the memory (10 rows in 18
+// groups, 5552 -> 2216, 90 of 87: 53 -> 60).
+int parts_for(long long items, long long stages) {
+  if (items > 64 || stages < 50) return 1;
+  return (int)std::min(stages / 8, 256 / std::max(items, 1LL));
+}
+
+struct Parts {
+  int dx = 1, dw = 1;   // dx: of the forward product's y too
+  size_t dx_floats, dw_floats;
+  size_t bytes() const { return (dx > 1 ? dx * dx_floats : 0) * 4 + (dw > 1 ? dw * dw_floats : 0) * 4; }
+};
+Parts forward_parts(const GroupedArgs& a) {
+  Parts p;
+  p.dx_floats = (size_t)a.rows * a.n;
+  p.dx = parts_for(items<Small<false>>(a, a.n), (a.k + 63) / 64);
+  return p;
+}
+Parts backward_parts(const GroupedArgs& a, bool dx, bool dw) {
+  Parts p;
+  p.dx_floats = (size_t)a.rows * a.k;
+  p.dw_floats = (size_t)a.groups * a.n * a.k;
+  if (dx) p.dx = parts_for(items<Small<false>>(a, a.k), (a.n + 63) / 64);
+  if (dw)
+    p.dw = parts_for((long long)a.groups * ((a.n + 127) / 128) * ((a.k + 127) / 128), a.rows / a.groups / 64);
+  return p;
+}
+
 template <class C>
-hipError_t launch_forward(const GroupedArgs& a, const void* x, int64_t ldx, void* y, hipStream_t stream) {
-  // a weight read once is best read beside its neighbours: one share
-  const int slices = (a.n + C::BN - 1) / C::BN;
-  const Deal d = C::NT ? Deal{slices, 1, slices} : deal(slices);
-  hipLaunchKernelGGL((grouped_forward<C>), dim3((unsigned)(items_per_xcd(a, C::BM, d) * kXcds)),
-                     dim3(C::kWaves * kWave), 0, stream, static_cast<const uint16_t*>(x), ldx,
-                     static_cast<const uint16_t*>(a.w), a.offsets, a.rows, a.groups, a.n, a.k, d,
-                     static_cast<uint16_t*>(y));
+hipError_t launch_join_rows(const GroupedArgs& a, int cols, const Deal& d, int parts, const float* partial, void* out,
+                            hipStream_t stream) {
+  hipLaunchKernelGGL((grouped_join_rows<C>), dim3((unsigned)(items_per_xcd(a, C::BM, d) * kXcds)),
+                     dim3(C::kWaves * kWave), 0, stream, partial, parts, a.offsets, a.rows, a.groups, cols, d,
+                     static_cast<uint16_t*>(out));
   return hipGetLastError();
 }
 
-template <class C, class X>
+template <class C, bool SPLIT = false>
+hipError_t launch_forward(const GroupedArgs& a, const void* x, int64_t ldx, void* y, hipStream_t stream, int parts = 1,
+                          float* partial = nullptr) {
+  // a weight read once is best read beside its neighbours: one share
+  const int slices = (a.n + C::BN - 1) / C::BN;
+  const Deal d = C::NT ? Deal{slices, 1, slices} : deal(slices);
+  hipLaunchKernelGGL((grouped_forward<C, SPLIT>), dim3((unsigned)(items_per_xcd(a, C::BM, d) * kXcds * parts)),
+                     dim3(C::kWaves * kWave), 0, stream, static_cast<const uint16_t*>(x), ldx,
+                     static_cast<const uint16_t*>(a.w), a.offsets, a.rows, a.groups, a.n, a.k, d,
+                     static_cast<uint16_t*>(y), parts, partial);
+  if (const hipError_t e = hipGetLastError()) return e;
+  return SPLIT ? launch_join_rows<C>(a, a.n, d, parts, partial, y, stream) : hipSuccess;
+}
+
+template <class C, class X, bool SPLIT_DX = false, bool SPLIT_DW = false>
 hipError_t launch_backward(const GroupedArgs& a, BackwardArgs b, bool f32, hipStream_t stream) {
   b.dx_deal = deal((a.k + X::BN - 1) / X::BN);
-  b.dx_items = b.dx ? (int)items_per_xcd(a, X::BM, b.dx_deal) : 0;
+  b.dx_items = b.dx ? (int)items_per_xcd(a, X::BM, b.dx_deal) * b.dx_parts : 0;
   const long long dw_tiles = (long long)a.groups * ((a.n + C::BM - 1) / C::BM) * ((a.k + C::BN - 1) / C::BN);
-  b.dw_items = b.dw ? (int)((dw_tiles + kXcds - 1) / kXcds) : 0;
+  b.dw_items = b.dw ? (int)((dw_tiles * b.dw_parts + kXcds - 1) / kXcds) : 0;
   b.dw_groups = std::min(b.dw_items, kCusPerXcd * C::kPerCU);   // as many as run at once
   if (b.dx_items + b.dw_items == 0) return hipSuccess;
   // dw beyond the L2s' 32 MB leaves nothing there to read again and would
   // push dy and x out: streamed (3.76 GB: 1259 -> 1091 us)
-  const bool stream_out = (size_t)a.groups * a.n * a.k * (f32 ? 4 : 2) > kL2Bytes;
+  const size_t total = (size_t)a.groups * a.n * a.k;
+  const bool stream_out = total * (f32 ? 4 : 2) > kL2Bytes;
   auto run = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)(b.dx_items + b.dw_groups) * kXcds), dim3(C::kWaves * kWave), 0, stream, b);
   };
-  if (f32) run(stream_out ? grouped_backward<C, X, true, true> : grouped_backward<C, X, true, false>);
-  else run(stream_out ? grouped_backward<C, X, false, true> : grouped_backward<C, X, false, false>);
-  return hipGetLastError();
+  if constexpr (SPLIT_DW) run(grouped_backward<C, X, true, false, SPLIT_DX, true>);
+  else if (f32)
+    run(stream_out ? grouped_backward<C, X, true, true, SPLIT_DX, false>
+                   : grouped_backward<C, X, true, false, SPLIT_DX, false>);
+  else
+    run(stream_out ? grouped_backward<C, X, false, true, SPLIT_DX, false>
+                   : grouped_backward<C, X, false, false, SPLIT_DX, false>);
+  if (const hipError_t e = hipGetLastError()) return e;
+  if constexpr (SPLIT_DX)
+    if (const hipError_t e = launch_join_rows<X>(a, a.k, b.dx_deal, b.dx_parts, b.dx_partial, b.dx, stream)) return e;
+  if constexpr (SPLIT_DW) {
+    const dim3 grid((unsigned)((total / 4 + 255) / 256));
+    if (f32) hipLaunchKernelGGL((grouped_join_dw<true>), grid, dim3(256), 0, stream, b.dw_partial, b.dw_parts, total, b.dw);
+    else hipLaunchKernelGGL((grouped_join_dw<false>), grid, dim3(256), 0, stream, b.dw_partial, b.dw_parts, total, b.dw);
+    if (const hipError_t e = hipGetLastError()) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
+
+size_t grouped_forward_workspace(const GroupedArgs& a) { return forward_parts(a).bytes(); }
+size_t grouped_backward_workspace(const GroupedArgs& a, bool dx, bool dw) { return backward_parts(a, dx, dw).bytes(); }
 
 // Tile by the rows a group has on average (64 groups, 7168 -> 4096, us with
 // 64-, 128- and 256-row tiles, the first two non-temporal): few rows stream the
@@ -624,8 +768,15 @@ hipError_t launch_backward(const GroupedArgs& a, BackwardArgs b, bool f32, hipSt
 // rows, at the power limit: 1412 against 1451 us).  Grids that would leave CUs
 // idle take the next smaller tile (600 rows in 8 groups, 768 -> 1024: 8.2, 9.1,
 // 13.5).
-hipError_t launch_grouped_forward(const GroupedArgs& a, const void* x, int64_t ldx, void* y, hipStream_t stream) {
+hipError_t launch_grouped_forward(const GroupedArgs& a, const void* x, int64_t ldx, void* y, void* workspace,
+                                  hipStream_t stream) {
   const long long rows = a.rows;
+  if (workspace) {
+    const int parts = forward_parts(a).dx;
+    float* const partial = static_cast<float*>(workspace);
+    if (parts > 1 && rows <= 16LL * a.groups) return launch_forward<Small<true>, true>(a, x, ldx, y, stream, parts, partial);
+    if (parts > 1) return launch_forward<Small<false>, true>(a, x, ldx, y, stream, parts, partial);
+  }
   if (rows <= 16LL * a.groups) return launch_forward<Small<true>>(a, x, ldx, y, stream);
   if (rows <= 40LL * a.groups && items<Middle<true>>(a, a.n) >= 256)
     return launch_forward<Middle<true>>(a, x, ldx, y, stream);
@@ -643,15 +794,27 @@ hipError_t launch_grouped_forward(const GroupedArgs& a, const void* x, int64_t l
 // 1024: 7.6 against 9.6 us and 8.6 against 10.4; with dw 10.8 against 11.6, but
 // 14.9 against 13.2).
 hipError_t launch_grouped_backward(const GroupedArgs& a, const void* dy, int64_t lddy, const void* x, int64_t ldx,
-                                   void* dx, bool f32, void* dw, hipStream_t stream) {
+                                   void* dx, bool f32, void* dw, void* workspace, hipStream_t stream) {
   const BackwardArgs b{static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(x),
                        static_cast<const uint16_t*>(a.w), lddy, ldx, a.offsets, a.rows, a.groups, a.n, a.k,
-                       static_cast<uint16_t*>(dx), dw, {}, 0, 0, 0};
+                       static_cast<uint16_t*>(dx), dw, {}, 0, 0, 0, 1, 1, nullptr, nullptr};
+  const bool small = items<Small<false>>(a, a.k) <= (dw ? 256 : 512);
+  if (workspace) {
+    const Parts p = backward_parts(a, dx, dw);
+    BackwardArgs s = b;
+    s.dx_parts = p.dx;
+    s.dw_parts = p.dw;
+    s.dx_partial = static_cast<float*>(workspace);
+    s.dw_partial = s.dx_partial + (p.dx > 1 ? p.dx * p.dx_floats : 0);
+    if (p.dx > 1 && p.dw > 1) return launch_backward<Middle<false>, Small<false>, true, true>(a, s, f32, stream);
+    if (p.dx > 1) return launch_backward<Middle<false>, Small<false>, true, false>(a, s, f32, stream);
+    if (p.dw > 1 && small) return launch_backward<Middle<false>, Small<false>, false, true>(a, s, f32, stream);
+    if (p.dw > 1) return launch_backward<Middle<false>, Middle<false>, false, true>(a, s, f32, stream);
+  }
   const long long dw_tiles = (long long)a.groups * ((a.n + 255) / 256) * ((a.k + 255) / 256);
   const bool large = dw ? dw_tiles >= 256 : items<Large<4>>(a, a.k) >= 256 && a.rows > 40LL * a.groups;
   if (large) return launch_backward<Large<4>, Large<4>>(a, b, f32, stream);
-  if (items<Small<false>>(a, a.k) <= (dw ? 256 : 512))
-    return launch_backward<Middle<false>, Small<false>>(a, b, f32, stream);
+  if (small) return launch_backward<Middle<false>, Small<false>>(a, b, f32, stream);
   return launch_backward<Middle<false>, Middle<false>>(a, b, f32, stream);
 }
 

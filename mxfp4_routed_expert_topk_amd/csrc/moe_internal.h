@@ -182,10 +182,14 @@ struct GroupedArgs {
   const int32_t* offsets;   // [groups + 1]
   int rows, groups, n, k;
 };
-hipError_t launch_grouped_forward(const GroupedArgs& a, const void* x, int64_t ldx, void* y, hipStream_t stream);
+// workspace: null (no reduction is split) or of the size that these give, 0 where no split helps
+size_t grouped_forward_workspace(const GroupedArgs& a);
+size_t grouped_backward_workspace(const GroupedArgs& a, bool dx, bool dw);
+hipError_t launch_grouped_forward(const GroupedArgs& a, const void* x, int64_t ldx, void* y, void* workspace,
+                                  hipStream_t stream);
 // dx or dw null: not computed (x null too without dw, w without dx); dx only with rows above zero
 hipError_t launch_grouped_backward(const GroupedArgs& a, const void* dy, int64_t lddy, const void* x, int64_t ldx,
-                                   void* dx, bool f32, void* dw, hipStream_t stream);
+                                   void* dx, bool f32, void* dw, void* workspace, hipStream_t stream);
 
 // Router top-k (E <= kRouterMaxExperts, k <= 32).
 constexpr int kRouterMaxExperts = 1024;

@@ -69,9 +69,28 @@ moe_status check_ld(const char* name, int64_t ld, int32_t cols) {
   return MOE_OK;
 }
 
+// a workspace may be missing (nothing is split) but not too small
+moe_status check_workspace(const void* p, size_t bytes, size_t need) {
+  if (!p || !need) return MOE_OK;
+  if (bytes < need) return fail(MOE_ERR_CAPACITY, "workspace must hold %zu bytes, got %zu", need, bytes);
+  if (reinterpret_cast<uintptr_t>(p) & 15u) return fail(MOE_ERR_ALIGN, "workspace must be 16-byte aligned, got %p", p);
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t moe_grouped_matmul_workspace(int32_t rows, int32_t num_groups, int32_t n, int32_t k) {
+  if (check_grouped(rows, num_groups, n, k) || !rows || !num_groups) return 0;
+  return moe::grouped_forward_workspace({nullptr, nullptr, rows, num_groups, n, k});
+}
+
+size_t moe_grouped_matmul_backward_workspace(int32_t rows, int32_t num_groups, int32_t n, int32_t k, int32_t need_dx,
+                                             int32_t need_dw) {
+  if (check_grouped(rows, num_groups, n, k) || !rows || !num_groups) return 0;
+  return moe::grouped_backward_workspace({nullptr, nullptr, rows, num_groups, n, k}, need_dx, need_dw);
+}
 
 moe_status moe_mxfp4_quantize(const void* x, int32_t dtype, int32_t rows, int32_t cols, int64_t ldx, uint8_t* codes,
                               uint8_t* scales, hipStream_t stream) {
@@ -115,19 +134,22 @@ moe_status moe_mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, con
 }
 
 moe_status moe_grouped_matmul(const uint16_t* x, int64_t ldx, const uint16_t* w, const int32_t* offsets, int32_t rows,
-                              int32_t num_groups, int32_t n, int32_t k, uint16_t* out, hipStream_t stream) {
+                              int32_t num_groups, int32_t n, int32_t k, uint16_t* out, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream) {
   if (moe_status s = check_grouped(rows, num_groups, n, k)) return s;
   if (moe_status s = check_ld("ldx", ldx, k)) return s;
   if (rows == 0 || num_groups == 0) return ok();
   if (moe_status s = check_ptrs({{"x", x}, {"w", w}, {"offsets", offsets, 4}, {"out", out}})) return s;
-  const hipError_t e = moe::launch_grouped_forward({w, offsets, rows, num_groups, n, k}, x, ldx, out, stream);
+  const moe::GroupedArgs a{w, offsets, rows, num_groups, n, k};
+  if (moe_status s = check_workspace(workspace, workspace_bytes, moe::grouped_forward_workspace(a))) return s;
+  const hipError_t e = moe::launch_grouped_forward(a, x, ldx, out, workspace, stream);
   return e == hipSuccess ? ok() : hip_fail(e, "grouped matmul launch");
 }
 
 moe_status moe_grouped_matmul_backward(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx,
                                        const uint16_t* w, const int32_t* offsets, int32_t rows, int32_t num_groups,
                                        int32_t n, int32_t k, uint16_t* dx, void* dw, int32_t dw_dtype,
-                                       hipStream_t stream) {
+                                       void* workspace, size_t workspace_bytes, hipStream_t stream) {
   if (moe_status s = check_dtype("dw_dtype", dw_dtype)) return s;
   if (moe_status s = check_grouped(rows, num_groups, n, k)) return s;
   if (moe_status s = check_ld("lddy", lddy, n)) return s;
@@ -144,8 +166,10 @@ moe_status moe_grouped_matmul_backward(const uint16_t* dy, int64_t lddy, const u
     if (rows > 0)
       if (moe_status s = check_ptrs({{"x", x}})) return s;
   }
-  const hipError_t e = moe::launch_grouped_backward({w, offsets, rows, num_groups, n, k}, dy, lddy, x, ldx, dx,
-                                                    dw_dtype == MOE_F32, dw, stream);
+  const moe::GroupedArgs a{w, offsets, rows, num_groups, n, k};
+  if (moe_status s = check_workspace(workspace, workspace_bytes, moe::grouped_backward_workspace(a, dx, dw))) return s;
+  const hipError_t e =
+      moe::launch_grouped_backward(a, dy, lddy, x, ldx, dx, dw_dtype == MOE_F32, dw, workspace, stream);
   return e == hipSuccess ? ok() : hip_fail(e, "grouped matmul backward launch");
 }
 

@@ -227,6 +227,12 @@ GROUPED = [   # counts, n, k, rows before and behind the groups
     ([130, 0, 7, 260, 33], 2000, 1800, 2, 2),   # 256 x 256 tiles backward
     ([353, 417, 33, 200, 129], 9480, 136, 1, 0),   # 256 x 256 tiles forward, every number of live row blocks
     ([700, 500, 333], 264, 2600, 0, 1),   # 128 x 128 tiles for both gradients
+    # long sums for few tiles, in parts: forward, forward of few rows, dw, dx, both gradients
+    ([718], 64, 6672, 1, 1),
+    ([1, 0, 3, 0, 1, 0] * 3, 264, 5552, 2, 0),
+    ([6000], 584, 184, 3, 2),
+    ([90, 0, 30], 4104, 72, 2, 1),
+    ([3300], 3208, 72, 1, 2),
 ]
 
 
@@ -283,6 +289,46 @@ def test_grouped_one_gradient_only():
     only_dw = moe.grouped_matmul_backward(*args, need_dx=False)
     assert only_dx[1] is None and torch.equal(only_dx[0], dx)
     assert only_dw[0] is None and torch.equal(only_dw[1], dw)
+
+
+@pytest.mark.parametrize("counts,n,k", [([718], 64, 6672), ([1, 0, 3] * 6, 264, 5552), ([6000, 566], 584, 184),
+                                        ([90, 30], 4104, 72), ([3300], 3208, 72)])
+def test_grouped_sums_in_parts_and_whole(counts, n, k):
+    """With and without a workspace, of sums that are exact: the same bits."""
+    off, x, dy, w = grouped_case(counts, n, k, 0, 0, 8)
+    X, DY, W, O = up(x, BF), up(dy, BF), up(w, BF), up(off)
+    lib, rows, G = moe.load_library(), len(x), len(counts)
+    assert lib.moe_grouped_matmul_workspace(rows, G, n, k) + \
+        lib.moe_grouped_matmul_backward_workspace(rows, G, n, k, 1, 1) > 0
+    y, dx, dw = torch.zeros_like(DY), torch.zeros_like(X), torch.zeros(W.shape, device=dev())
+    s = torch.cuda.current_stream().cuda_stream
+    assert lib.moe_grouped_matmul(X.data_ptr(), k, W.data_ptr(), O.data_ptr(), rows, G, n, k, y.data_ptr(), None, 0, s) == 0
+    assert lib.moe_grouped_matmul_backward(DY.data_ptr(), n, X.data_ptr(), k, W.data_ptr(), O.data_ptr(), rows, G, n, k,
+                                           dx.data_ptr(), dw.data_ptr(), moe.MOE_F32, None, 0, s) == 0
+    got = moe.grouped_matmul(X, W, O), *moe.grouped_matmul_backward(DY, X, W, O)
+    for g, t in zip(got, (y, dx, dw)):
+        assert torch.equal(g, t)
+
+
+def test_grouped_sums_in_parts_in_a_graph():
+    off, x, dy, w = grouped_case([90, 30], 4104, 72, 1, 1, 9)
+    X, DY, W, O = up(x, BF), up(dy, BF), up(w, BF), up(off)
+    wt = W.transpose(1, 2).contiguous()
+    step = lambda: (moe.grouped_matmul(DY, wt, O), *moe.grouped_matmul_backward(DY, X, W, O))
+    step()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        res = step()
+    for turn in range(3):
+        DY.copy_(up(ints(np.random.default_rng(turn), dy.shape), BF))
+        want = [t.clone() for t in step()]
+        for t in res:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for got, ref in zip(res, want):
+            lo, hi = (1, 121) if got.dim() == 2 else (0, None)   # the first and last rows are no group's
+            assert torch.equal(got[lo:hi], ref[lo:hi])
 
 
 @pytest.mark.parametrize("counts,n,k", [([700, 500, 333], 264, 2600), ([353, 417, 33, 200, 129], 136, 9480)])

@@ -69,36 +69,36 @@ def test_matmul_refusals(lib, args, status, needle):
 
 
 @pytest.mark.parametrize("args,status,needle", [
-    ((P, 64, P, P, -1, 2, 16, 64, P, None), 1, "rows must be >= 0"),
-    ((P, 64, P, P, (1 << 24) + 1, 2, 16, 64, P, None), 2, "rows must be at most"),
-    ((P, 64, P, P, 4, -1, 16, 64, P, None), 1, "num_groups must be >= 0"),
-    ((P, 64, P, P, 4, 4097, 16, 64, P, None), 2, "num_groups must be at most"),
-    ((P, 64, P, P, 4, 2, 12, 64, P, None), 2, "n must be a multiple of 8"),
-    ((P, 64, P, P, 4, 2, 0, 64, P, None), 2, "n must be a multiple of 8"),
-    ((P, 65, P, P, 4, 2, 16, 65, P, None), 2, "k must be a multiple of 8"),
-    ((P, 65544, P, P, 4, 2, 16, 65544, P, None), 2, "k must be a multiple of 8"),
-    ((P, 56, P, P, 4, 2, 16, 64, P, None), 2, "ldx must be"),
-    ((P, 68, P, P, 4, 2, 16, 64, P, None), 2, "ldx must be a multiple of 8"),
-    ((P, (1 << 20) + 8, P, P, 4, 2, 16, 64, P, None), 2, "ldx must be"),
-    ((P, 64, None, P, 4, 2, 16, 64, P, None), 1, "w is null"),
-    ((P, 64, P, P + 2, 4, 2, 16, 64, P, None), 3, "offsets must be 4-byte aligned"),
+    ((P, 64, P, P, -1, 2, 16, 64, P, None, 0, None), 1, "rows must be >= 0"),
+    ((P, 64, P, P, (1 << 24) + 1, 2, 16, 64, P, None, 0, None), 2, "rows must be at most"),
+    ((P, 64, P, P, 4, -1, 16, 64, P, None, 0, None), 1, "num_groups must be >= 0"),
+    ((P, 64, P, P, 4, 4097, 16, 64, P, None, 0, None), 2, "num_groups must be at most"),
+    ((P, 64, P, P, 4, 2, 12, 64, P, None, 0, None), 2, "n must be a multiple of 8"),
+    ((P, 64, P, P, 4, 2, 0, 64, P, None, 0, None), 2, "n must be a multiple of 8"),
+    ((P, 65, P, P, 4, 2, 16, 65, P, None, 0, None), 2, "k must be a multiple of 8"),
+    ((P, 65544, P, P, 4, 2, 16, 65544, P, None, 0, None), 2, "k must be a multiple of 8"),
+    ((P, 56, P, P, 4, 2, 16, 64, P, None, 0, None), 2, "ldx must be"),
+    ((P, 68, P, P, 4, 2, 16, 64, P, None, 0, None), 2, "ldx must be a multiple of 8"),
+    ((P, (1 << 20) + 8, P, P, 4, 2, 16, 64, P, None, 0, None), 2, "ldx must be"),
+    ((P, 64, None, P, 4, 2, 16, 64, P, None, 0, None), 1, "w is null"),
+    ((P, 64, P, P + 2, 4, 2, 16, 64, P, None, 0, None), 3, "offsets must be 4-byte aligned"),
 ])
 def test_grouped_matmul_refusals(lib, args, status, needle):
     refused(lib, "moe_grouped_matmul", args, status, needle)
 
 
 @pytest.mark.parametrize("args,status,needle", [
-    ((P, 16, P, 64, P, P, 4, 2, 16, 64, P, P, 7, None), 1, "dw_dtype must be"),
-    ((P, 8, P, 64, P, P, 4, 2, 16, 64, P, P, 0, None), 2, "lddy must be"),
-    ((P, 16, P, 56, P, P, 4, 2, 16, 64, P, P, 0, None), 2, "ldx must be"),
-    ((P, 16, P, 64, P, P, -4, 2, 16, 64, P, P, 0, None), 1, "rows must be >= 0"),
-    ((P, 16, P, 64, P, P, 4, 2, 20, 64, P, P, 0, None), 2, "n must be a multiple of 8"),
-    ((None, 16, P, 64, P, P, 4, 2, 16, 64, P, P, 0, None), 1, "dy is null"),
-    ((P, 16, None, 64, P, P, 4, 2, 16, 64, None, P, 0, None), 1, "x is null"),
-    ((P, 16, P, 64, None, P, 4, 2, 16, 64, P, None, 0, None), 1, "w is null"),
-    ((P, 16, P, 64, P, None, 4, 2, 16, 64, P, P, 0, None), 1, "offsets is null"),
-    ((P, 16, P, 64, P, P, 4, 2, 16, 64, P + 8, None, 0, None), 3, "dx must be 16-byte aligned"),
-    ((P, 16, P, 64, P, P, 4, 2, 16, 64, None, P + 2, 0, None), 3, "dw must be 16-byte aligned"),
+    ((P, 16, P, 64, P, P, 4, 2, 16, 64, P, P, 7, None, 0, None), 1, "dw_dtype must be"),
+    ((P, 8, P, 64, P, P, 4, 2, 16, 64, P, P, 0, None, 0, None), 2, "lddy must be"),
+    ((P, 16, P, 56, P, P, 4, 2, 16, 64, P, P, 0, None, 0, None), 2, "ldx must be"),
+    ((P, 16, P, 64, P, P, -4, 2, 16, 64, P, P, 0, None, 0, None), 1, "rows must be >= 0"),
+    ((P, 16, P, 64, P, P, 4, 2, 20, 64, P, P, 0, None, 0, None), 2, "n must be a multiple of 8"),
+    ((None, 16, P, 64, P, P, 4, 2, 16, 64, P, P, 0, None, 0, None), 1, "dy is null"),
+    ((P, 16, None, 64, P, P, 4, 2, 16, 64, None, P, 0, None, 0, None), 1, "x is null"),
+    ((P, 16, P, 64, None, P, 4, 2, 16, 64, P, None, 0, None, 0, None), 1, "w is null"),
+    ((P, 16, P, 64, P, None, 4, 2, 16, 64, P, P, 0, None, 0, None), 1, "offsets is null"),
+    ((P, 16, P, 64, P, P, 4, 2, 16, 64, P + 8, None, 0, None, 0, None), 3, "dx must be 16-byte aligned"),
+    ((P, 16, P, 64, P, P, 4, 2, 16, 64, None, P + 2, 0, None, 0, None), 3, "dw must be 16-byte aligned"),
 ])
 def test_grouped_backward_refusals(lib, args, status, needle):
     refused(lib, "moe_grouped_matmul_backward", args, status, needle)
@@ -109,11 +109,27 @@ def test_empty_calls_are_no_ops(lib):
     assert lib.moe_mxfp4_dequantize(None, None, 0, 64, 0, None, None) == 0
     assert lib.moe_mxfp4_matmul(None, None, None, None, 0, 5, 64, 0, None, None) == 0
     assert lib.moe_mxfp4_matmul(None, None, None, None, 5, 0, 64, 0, None, None) == 0
-    assert lib.moe_grouped_matmul(None, 64, None, None, 0, 2, 16, 64, None, None) == 0
-    assert lib.moe_grouped_matmul(None, 64, None, None, 4, 0, 16, 64, None, None) == 0
-    assert lib.moe_grouped_matmul_backward(None, 16, None, 64, None, None, 4, 0, 16, 64, None, None, 0, None) == 0
-    assert lib.moe_grouped_matmul_backward(None, 16, None, 64, None, None, 4, 2, 16, 64, None, None, 0, None) == 0
-    assert lib.moe_grouped_matmul_backward(None, 16, None, 64, None, None, 0, 2, 16, 64, P, None, 0, None) == 0
+    assert lib.moe_grouped_matmul(None, 64, None, None, 0, 2, 16, 64, None, None, 0, None) == 0
+    assert lib.moe_grouped_matmul(None, 64, None, None, 4, 0, 16, 64, None, None, 0, None) == 0
+    assert lib.moe_grouped_matmul_backward(None, 16, None, 64, None, None, 4, 0, 16, 64, None, None, 0, None, 0, None) == 0
+    assert lib.moe_grouped_matmul_backward(None, 16, None, 64, None, None, 4, 2, 16, 64, None, None, 0, None, 0, None) == 0
+    assert lib.moe_grouped_matmul_backward(None, 16, None, 64, None, None, 0, 2, 16, 64, P, None, 0, None, 0, None) == 0
+
+
+def test_grouped_workspaces(lib):
+    fwd, bwd = lib.moe_grouped_matmul_workspace, lib.moe_grouped_matmul_backward_workspace
+    # many tiles, short sums, nothing to do, sizes that the entries refuse: none
+    assert fwd(32768, 8, 4096, 7168) == fwd(32, 8, 256, 256) == fwd(0, 8, 64, 7168) == fwd(9, 0, 64, 7168) == 0
+    assert fwd(9, 2, 63, 7168) == bwd(6566, 1, 584, 184, 0, 0) == bwd(12288, 32, 4096, 7168, 1, 1) == 0
+    need = fwd(718, 1, 64, 6672)
+    assert need > 0 and need % (718 * 64 * 4) == 0       # whole fp32 copies of y
+    assert bwd(6566, 1, 584, 184, 0, 1) % (584 * 184 * 4) == 0 < bwd(6566, 1, 584, 184, 0, 1)
+    refused(lib, "moe_grouped_matmul", (P, 6672, P, P, 718, 1, 64, 6672, P, P, need - 1, None), 4,
+            f"workspace must hold {need} bytes")
+    refused(lib, "moe_grouped_matmul", (P, 6672, P, P, 718, 1, 64, 6672, P, P + 8, need, None), 3,
+            "workspace must be 16-byte aligned")
+    refused(lib, "moe_grouped_matmul_backward",
+            (P, 584, P, 184, P, P, 6566, 1, 584, 184, P, P, 0, P, 64, None), 4, "workspace must hold")
 
 
 def z(*shape, dtype=BF):
