@@ -330,10 +330,11 @@ __device__ __forceinline__ void matmul_tile(uint8_t* smem, const uint8_t* ac, co
   __builtin_amdgcn_s_barrier();   // every wave is done reading the ring
   asm volatile("" ::: "memory");
 
-  // Lane holds row rl, columns 4q .. 4q + 3 of each 16 x 16 block.  Where rows
-  // of the output are 16-byte aligned, the wave's blocks pass through its part
-  // of the ring, 32 rows at a time, and leave as whole rows of 16-byte chunks
-  // (permuted by chunk ^ row for the banks); else every element by itself.
+  // Lane holds row rl, columns 4q .. 4q + 3 of each 16 x 16 block.  The wave's
+  // blocks pass through its part of the ring, 32 rows at a time, and leave as
+  // whole rows of 16-byte chunks (permuted by chunk ^ row for the banks) or,
+  // where the output's rows are not 16-byte aligned, of single values, a row's
+  // side by side (4096 x 4097 x 1024: 36 us; from the MFMA layout 57).
   constexpr int kSize = F32 ? 4 : 2, kRowBytes = C::NJ * 16 * kSize, kChunks = kRowBytes / 16;
   constexpr int kMask = kChunks < 16 ? kChunks - 1 : 15;
   constexpr int kShift = kRowBytes >= 256 ? 0 : 1;   // rows side by side in the banks
@@ -342,22 +343,22 @@ __device__ __forceinline__ void matmul_tile(uint8_t* smem, const uint8_t* ac, co
   const bool rows_aligned = N % (16 / kSize) == 0;
   uint8_t* const stg = smem + wave * (32 * kRowBytes);
   const int mw = wm * (16 * C::MI), nw = wn * (16 * C::NJ);
-  if (rows_aligned) {
 #pragma unroll
-    for (int i = 0; i < C::MI; i += 2) {
+  for (int i = 0; i < C::MI; i += 2) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j = 0; j < C::NJ; ++j) {
-          const f32x4_t v = acc[i + h][j];
-          uint8_t* const at = stg + (16 * h + rl) * kRowBytes;
-          if constexpr (F32)
-            *reinterpret_cast<f32x4_t*>(at + place(rl, 4 * j + q)) = v;
-          else
-            *reinterpret_cast<uint2*>(at + place(rl, 2 * j + (q >> 1)) + 8 * (q & 1)) =
-                make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
-        }
-      asm volatile("" ::: "memory");
+      for (int j = 0; j < C::NJ; ++j) {
+        const f32x4_t v = acc[i + h][j];
+        uint8_t* const at = stg + (16 * h + rl) * kRowBytes;
+        if constexpr (F32)
+          *reinterpret_cast<f32x4_t*>(at + place(rl, 4 * j + q)) = v;
+        else
+          *reinterpret_cast<uint2*>(at + place(rl, 2 * j + (q >> 1)) + 8 * (q & 1)) =
+              make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+      }
+    asm volatile("" ::: "memory");
+    if (rows_aligned) {
 #pragma unroll
       for (int k = 0; k < kChunks / 2; ++k) {   // 64 / kChunks rows at a time
         const int r = k * (64 / kChunks) + lane / kChunks, c = lane % kChunks;
@@ -366,22 +367,17 @@ __device__ __forceinline__ void matmul_tile(uint8_t* smem, const uint8_t* ac, co
         if (m < mrows && n < nrows)
           *reinterpret_cast<u32x4_t*>(static_cast<uint8_t*>(out) + ((size_t)(m0 + m) * N + n0 + n) * kSize) = v;
       }
-      asm volatile("" ::: "memory");
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < C::MI; ++i)
-#pragma unroll
-    for (int j = 0; j < C::NJ; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int m = mw + 16 * i + rl, n = nw + 16 * j + 4 * q + e;
-        if (m >= mrows || n >= nrows) continue;
-        const size_t at = (size_t)(m0 + m) * N + n0 + n;
-        if constexpr (F32) static_cast<float*>(out)[at] = acc[i][j][e];
-        else static_cast<uint16_t*>(out)[at] = f32_to_bf16_rne(acc[i][j][e]);
+    } else {
+      using V = std::conditional_t<F32, float, uint16_t>;
+      static_assert(C::NJ * 16 == kWave, "a row a wave");
+      const int n = nw + lane, c = lane / (16 / kSize);
+      for (int r = 0; r < 32 && mw + 16 * i + r < mrows; ++r) {
+        const V v = *reinterpret_cast<const V*>(stg + r * kRowBytes + place(r, c) + lane % (16 / kSize) * kSize);
+        if (n < nrows) static_cast<V*>(out)[(size_t)(m0 + mw + 16 * i + r) * N + n0 + n] = v;
       }
+    }
+    asm volatile("" ::: "memory");
+  }
 }
 
 template <class C, bool F32>
