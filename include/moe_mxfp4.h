@@ -48,7 +48,7 @@ typedef enum {
   MOE_ERR_ARG = 1,          /* null pointer, bad enum, negative count */
   MOE_ERR_SHAPE = 2,        /* dimension not supported (see moe_mxfp4_config) */
   MOE_ERR_ALIGN = 3,        /* a device pointer is not 16-byte aligned */
-  MOE_ERR_CAPACITY = 4,     /* num_tokens > max_tokens */
+  MOE_ERR_CAPACITY = 4,     /* num_tokens > max_tokens, or memory too small */
   MOE_ERR_SCALE_BYTE = 5,   /* a weight scale byte is not accepted (plan) */
   MOE_ERR_WORKSPACE = 6,    /* workspace or repacked buffer too small */
   MOE_ERR_UNSUPPORTED = 7,  /* device is not gfx950 */

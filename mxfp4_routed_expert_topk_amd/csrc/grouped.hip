@@ -676,7 +676,7 @@ int parts_for(long long items, long long stages) {
 
 struct Parts {
   int dx = 1, dw = 1;   // dx: of the forward product's y too
-  size_t dx_floats, dw_floats;
+  size_t dx_floats = 0, dw_floats = 0;
   size_t bytes() const { return (dx > 1 ? dx * dx_floats : 0) * 4 + (dw > 1 ? dw * dw_floats : 0) * 4; }
 };
 Parts forward_parts(const GroupedArgs& a) {

@@ -1,6 +1,7 @@
 // C entries of the MXFP4 quantiser and product and of the grouped products:
-// argument checks before any launch, then one enqueue.  Nothing here allocates
-// or synchronises, so every call may be captured in a graph.
+// argument checks before any launch, then one enqueue (two or three where a
+// long sum is split).  Nothing here allocates or synchronises, so every call
+// may be captured in a graph.
 #include <hip/hip_runtime.h>
 
 #include "../../include/moe_mxfp4.h"
