@@ -162,6 +162,12 @@ def _need(t, name: str, dtype, rows_min: int, cols: Optional[int], device, ndim:
         raise _arg_error(f"{name} must hold at least {rows_min} elements, got {t.numel()}")
 
 
+def _too_large(**sizes):
+    """The refusal of sizes of which one is 2^31 or more: ctypes would pass its
+    low 32 bits on."""
+    return MoeError(MOE_ERR_SHAPE, "sizes must be below 2^31, got " + ", ".join(f"{n}={v}" for n, v in sizes.items()))
+
+
 def _stream(stream=None) -> int:
     import torch
     s = torch.cuda.current_stream() if stream is None else stream
@@ -308,6 +314,8 @@ def router_topk(logits, top_k, ids=None, weights=None, stream=None):
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise _arg_error("logits must be a 2-D torch.Tensor [T, num_experts]")
     T, E = logits.shape
+    if (T | E) >> 31:
+        raise _too_large(num_tokens=T, num_experts=E)
     _need(logits, "logits", torch.float32, T, E, logits.device)
     ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device) if ids is None else ids
     weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device) if weights is None else weights
@@ -322,6 +330,8 @@ def mxfp8_quantize(x_bf16, stream=None):
     if not isinstance(x_bf16, torch.Tensor) or x_bf16.dim() != 2:
         raise _arg_error("x must be a 2-D torch.Tensor [rows, cols]")
     rows, cols = x_bf16.shape
+    if (rows | cols) >> 31:
+        raise _too_large(rows=rows, cols=cols)
     _need(x_bf16, "x", torch.bfloat16, rows, cols, x_bf16.device)
     codes = torch.empty((rows, cols), dtype=torch.uint8, device=x_bf16.device)
     scales = torch.empty((rows, max(cols // 32, 0)), dtype=torch.uint8, device=x_bf16.device)
@@ -450,6 +460,8 @@ def mxfp4_quantize(x, codes=None, scales=None, stream=None):
     rows, cols = x.shape
     if cols <= 0 or cols % 32:
         raise MoeError(MOE_ERR_SHAPE, f"cols must be a positive multiple of 32, got {cols}")
+    if (rows | cols) >> 31:
+        raise _too_large(rows=rows, cols=cols)
     if codes is None:
         codes = _new((rows, cols // 2), torch.uint8, x, stream)
     else:
@@ -471,7 +483,7 @@ def _mxfp4_operand(codes, scales, codes_name: str, scales_name: str, like):
     import torch
     try:
         rows, half = shape = codes.shape
-        if half and not half % 16 and codes.dtype is scales.dtype is torch.uint8 \
+        if half and not half % 16 and not (rows | 2 * half) >> 31 and codes.dtype is scales.dtype is torch.uint8 \
                 and scales.shape == (rows, half // 16) \
                 and codes.get_device() == scales.get_device() == like.get_device() \
                 and codes.is_contiguous() and scales.is_contiguous():
@@ -484,6 +496,8 @@ def _mxfp4_operand(codes, scales, codes_name: str, scales_name: str, like):
     if half == 0 or half % 16:
         raise MoeError(MOE_ERR_SHAPE, f"{codes_name} must have a positive multiple of 16 columns, got {half}")
     _need_shape(scales, scales_name, torch.uint8, (rows, half // 16), like)
+    if (rows | 2 * half) >> 31:
+        raise _too_large(rows=rows, cols=2 * half)
     return rows, 2 * half
 
 
@@ -555,6 +569,8 @@ def grouped_matmul(x, w, offsets, out=None, stream=None):
     groups, n, k = _grouped(w, offsets)
     ld = _rows(x, "x", (torch.bfloat16,), k, w)
     rows = x.shape[0]
+    if (rows | groups | n | k) >> 31:
+        raise _too_large(rows=rows, num_groups=groups, n=n, k=k)
     if out is None:
         out = _new((rows, n), torch.bfloat16, x, stream)
     else:
@@ -584,6 +600,8 @@ def grouped_matmul_backward(dy, x, w, offsets, dx=None, dw=None, dw_dtype=None, 
     groups, n, k = _grouped(w, offsets)
     lddy = _rows(dy, "dy", (torch.bfloat16,), n, w)
     rows = dy.shape[0]
+    if (rows | groups | n | k) >> 31:
+        raise _too_large(rows=rows, num_groups=groups, n=n, k=k)
     used = [dy, w, offsets]
     ldx, code, x_at, dw_at, dx_at = k, MOE_F32, None, None, None
     if need_dw:

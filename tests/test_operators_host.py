@@ -196,3 +196,43 @@ def test_binding_refuses_overlapping_outputs(lib):
     both = z(8, 64)
     with pytest.raises(moe.MoeError, match="must be on a GPU"):
         moe.grouped_matmul(both[:4], z(2, 64, 64), z(3, dtype=I32), out=both[4:])
+
+
+BIG = 1 << 32                       # sizes reach the C entries as int32, where BIG + n would count as n
+
+
+def m(*shape, dtype=BF):
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+@pytest.mark.parametrize("call,needle", [
+    (lambda: moe.mxfp4_quantize(m(1, BIG + 32)), f"cols={BIG + 32}"),
+    (lambda: moe.mxfp4_quantize(m(BIG + 1, 32, dtype=F32)), f"rows={BIG + 1}"),
+    (lambda: moe.mxfp4_dequantize(m(1, BIG // 2 + 16, dtype=U8), m(1, BIG // 32 + 1, dtype=U8)), f"cols={BIG + 32}"),
+    (lambda: moe.mxfp4_dequantize(m(1, BIG // 4, dtype=U8), m(1, BIG // 64, dtype=U8)), f"cols={BIG // 2}"),
+    (lambda: moe.mxfp4_matmul(m(1, 16, dtype=U8), m(1, 1, dtype=U8), m(BIG + 3, 16, dtype=U8), m(BIG + 3, 1, dtype=U8)),
+     f"rows={BIG + 3}"),
+    (lambda: moe.mxfp4_matmul(*[m(1, (BIG + 64) // d, dtype=U8) for d in (2, 32, 2, 32)]), f"cols={BIG + 64}"),
+    (lambda: moe.grouped_matmul(m(BIG + 8, 8), m(1, 8, 8), m(2, dtype=I32)), f"rows={BIG + 8}"),
+    (lambda: moe.grouped_matmul(m(4, 8), m(1, BIG + 8, 8), m(2, dtype=I32)), f"n={BIG + 8}"),
+    (lambda: moe.grouped_matmul(m(4, BIG + 8), m(1, 8, BIG + 8), m(2, dtype=I32)), f"k={BIG + 8}"),
+    (lambda: moe.grouped_matmul_backward(m(BIG + 8, 8), m(BIG + 8, 8), m(1, 8, 8), m(2, dtype=I32)), f"rows={BIG + 8}"),
+    (lambda: moe.grouped_matmul_backward(m(4, 8), m(4, 8), m(BIG, 8, 8), m(BIG + 1, dtype=I32)), f"num_groups={BIG}"),
+    (lambda: moe.mxfp8_quantize(m(1, BIG + 32)), f"cols={BIG + 32}"),
+    (lambda: moe.router_topk(m(BIG + 1, 8, dtype=F32), 2), f"num_tokens={BIG + 1}"),
+])
+def test_sizes_that_no_int32_holds_are_refused(lib, call, needle):
+    with pytest.raises(moe.MoeError) as ei:
+        call()
+    assert ei.value.status == 2 and needle in ei.value.message, ei.value.message
+
+
+def test_the_largest_int32_sizes_reach_the_entries_checks(lib):
+    """Sizes that an int32 holds are refused, or not, by the entries themselves."""
+    most = (1 << 31) - 32
+    with pytest.raises(moe.MoeError, match="must be on a GPU"):
+        moe.mxfp4_quantize(m(1, most))
+    with pytest.raises(moe.MoeError, match="must be on a GPU"):
+        moe.mxfp4_dequantize(m(1, most // 2, dtype=U8), m(1, most // 32, dtype=U8))
+    with pytest.raises(moe.MoeError, match="must be on a GPU"):
+        moe.grouped_matmul(m(most, 8), m(1, 8, 8), m(2, dtype=I32))
