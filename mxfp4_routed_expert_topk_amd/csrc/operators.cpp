@@ -154,7 +154,8 @@ moe_status moe_grouped_matmul_backward(const uint16_t* dy, int64_t lddy, const u
   if (moe_status s = check_dtype("dw_dtype", dw_dtype)) return s;
   if (moe_status s = check_grouped(rows, num_groups, n, k)) return s;
   if (moe_status s = check_ld("lddy", lddy, n)) return s;
-  if (moe_status s = check_ld("ldx", ldx, k)) return s;
+  if (dw)   // x is read for dw only
+    if (moe_status s = check_ld("ldx", ldx, k)) return s;
   if (rows == 0) dx = nullptr;   // no rows to write
   if (num_groups == 0 || (!dx && !dw)) return ok();
   if (moe_status s = check_ptrs({{"offsets", offsets, 4}})) return s;

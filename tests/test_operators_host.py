@@ -236,3 +236,10 @@ def test_the_largest_int32_sizes_reach_the_entries_checks(lib):
         moe.mxfp4_dequantize(m(1, most // 2, dtype=U8), m(1, most // 32, dtype=U8))
     with pytest.raises(moe.MoeError, match="must be on a GPU"):
         moe.grouped_matmul(m(most, 8), m(1, 8, 8), m(2, dtype=I32))
+
+
+def test_the_stride_of_a_matrix_that_is_not_read_is_not_checked(lib):
+    """x is read for dw only: without dw it may be NULL, whatever ldx says."""
+    no_dw = lambda ldx: (None, 16, None, ldx, P, P, 0, 2, 16, 64, None, None, 0, None, 0, None)
+    assert [lib.moe_grouped_matmul_backward(*no_dw(ldx)) for ldx in (0, -8, 3, 64)] == [0] * 4
+    refused(lib, "moe_grouped_matmul_backward", (P, 16, P, 0, P, P, 4, 2, 16, 64, None, P, 0, None, 0, None), 2, "ldx must be")
