@@ -277,10 +277,9 @@ moe_status moe_mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, con
  *   w       [num_groups, n, k] bf16
  *   offsets [num_groups + 1] int32 in device memory: group e's rows are
  *           offsets[e] .. offsets[e+1] - 1; nondecreasing, within [0, rows]
- *           (values outside are clamped there and a decreasing pair counts as
- *           an empty group, so no offset reaches outside the tensors; a row
- *           that decreasing offsets give to two groups gets either's output
- *           or is left as it was)
+ *           (values outside are clamped there, and one that is below an
+ *           earlier one counts as that one, so no offset reaches outside the
+ *           tensors and no row belongs to two groups)
  *   out     [rows, n] bf16: out_r = w_e x_r, summed in fp32 and rounded once;
  *           rows outside every group are not written
  * n and k multiples of 8 in [8, 65536], num_groups <= 4096, rows <= 2^24, row
@@ -299,7 +298,9 @@ moe_status moe_grouped_matmul(const uint16_t* x, int64_t ldx, const uint16_t* w,
  *   dx [rows, k] bf16 or NULL: dx_r = w_e^T dy_r; rows outside every group are
  *      not written
  *   dw [num_groups, n, k] of `dw_dtype` or NULL: dw_e = sum over e's rows of
- *      dy_r x_r^T, every element written (zero for an empty group)
+ *      dy_r x_r^T, every element written (zero for an empty group).  Of
+ *      decreasing offsets each group's own two count here: a decreasing pair
+ *      is an empty group, a row between two groups' offsets is in both sums
  * A NULL gradient is not computed; w is read for dx only, x for dw only, and
  * either may be NULL where it is not read.  Each output is one fp32 sum in a
  * fixed order, rounded once (no atomics).  Enqueue-only. */

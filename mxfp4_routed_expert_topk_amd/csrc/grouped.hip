@@ -136,27 +136,47 @@ struct Operand {
 };
 
 // Row tiles (of bm rows, groups in order) and the place of one of them.
-// Offsets are clamped to [0, rows] and to their predecessor, so no offset
-// leads outside the tensors.  Every wave counts by itself: a lane takes
-// ceil(groups / 64) groups, a wave scan gives each lane its first tile.
+// Offsets are clamped to [0, rows] and count at least as much as every one
+// before them: none leads outside the tensors, no two groups share a row, so
+// that no two workgroups write one (nor one row's parts of a split sum), and
+// there are never more tiles than the grid was made for.  Every wave counts by
+// itself: a lane takes ceil(groups / 64) groups, a wave scan gives each lane
+// its first tile.
 struct Tile { int e, row0, rows; };
 struct RowTiles {
   const int32_t* offsets;
-  int rows, bm, e0, e1, first, mine, total;
+  int rows, bm, e0, e1, from, first, mine, total;   // from: group e0's rows start there or later
 
-  __device__ __forceinline__ void range(int e, int& lo, int& hi) const {
-    lo = min(max(offsets[e], 0), rows);
-    hi = min(max(offsets[e + 1], lo), rows);
+  __device__ __forceinline__ int clamped(int e) const { return min(max(offsets[e], 0), rows); }
+  // Counts the lane's tiles; last: where the last one ends.  True if an offset
+  // is below the one before it.
+  __device__ __forceinline__ bool count(int& last) {
+    bool falls = false;
+    mine = 0;
+    last = from;
+    for (int e = e0; e < e1; ++e) {
+      const int lo = max(clamped(e), last), to = clamped(e + 1);
+      falls |= to < lo;
+      last = max(to, lo);
+      mine += (last - lo + bm - 1) / bm;
+    }
+    return falls;
   }
-  __device__ __forceinline__ RowTiles(const int32_t* o, int groups, int r, int b, int lane) : offsets(o), rows(r), bm(b) {
+  __device__ __forceinline__ RowTiles(const int32_t* o, int groups, int r, int b, int lane)
+      : offsets(o), rows(r), bm(b), from(0) {
     const int per = (groups + kWave - 1) / kWave;
     e0 = min(lane * per, groups);
     e1 = min(e0 + per, groups);
-    mine = 0;
-    for (int e = e0; e < e1; ++e) {
-      int lo, hi;
-      range(e, lo, hi);
-      mine += (hi - lo + bm - 1) / bm;
+    int last;
+    if (__any(count(last))) {   // each lane starts from the largest offset of the lanes before it
+#pragma unroll
+      for (int d = 1; d < kWave; d <<= 1) {
+        const int v = __shfl_up(last, d, kWave);
+        if (lane >= d) last = max(last, v);
+      }
+      const int before = __shfl_up(last, 1, kWave);
+      if (lane > 0) from = before;
+      count(last);
     }
     int upto = mine;
 #pragma unroll
@@ -172,10 +192,10 @@ struct RowTiles {
     Tile t = {0, 0, 0};
     const bool here = tile >= first && tile < first + mine;
     if (here) {
-      int at = first;
+      int at = first, hi = from;
       for (int e = e0; e < e1; ++e) {
-        int lo, hi;
-        range(e, lo, hi);
+        const int lo = max(clamped(e), hi);
+        hi = max(clamped(e + 1), lo);
         const int n = (hi - lo + bm - 1) / bm;
         if (tile < at + n) {
           t.e = e;
@@ -553,6 +573,7 @@ struct BackwardArgs {
 
 // Tile `id` of dw: a group's tiles in bands of eight tile rows, whose
 // concurrent ones share their columns of dy and x.
+// A group's own two offsets count, clamped: every group has an output of its own.
 struct DwTile {
   int e, n0, k0, lo, length, rows, cols, part;
 };

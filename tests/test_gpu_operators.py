@@ -422,6 +422,38 @@ def test_grouped_offsets_are_clamped():
     np.testing.assert_array_equal(f64(dw), want)
 
 
+DECREASING = [   # offsets (the largest is the number of rows), n, k
+    ([0, 718, 0, 718], 64, 6672),               # the forward sum in parts
+    ([0, 400, 300, 600, 718], 64, 6672),
+    ([50, 100, 0, 120, 90, 130], 4104, 72),     # dx in parts
+    ([0, 6000, 10, 9700], 584, 184),
+    ([7, 3, 260, 255, 255, 400, 0, 401], 264, 136),
+    (list(range(0, 900, 3)) + [40, 41, 800, 905, 899, 910, 0, 912], 72, 96),   # several groups a lane
+    (list(range(900, 0, -3)), 72, 96),
+]
+
+
+@pytest.mark.parametrize("offsets,n,k", DECREASING)
+def test_grouped_decreasing_offsets_share_no_row(offsets, n, k):
+    """An offset below an earlier one counts as that one: in out and dx every row is the first
+    group's that holds it, whole, and the same in every run; dw takes each pair as it is."""
+    rng = np.random.default_rng(len(offsets) + k)
+    rows, groups = max(offsets), len(offsets) - 1
+    x, dy, w = ints(rng, (rows + 3, k)), ints(rng, (rows + 3, n)), ints(rng, (groups, n, k))
+    # the rows behind the largest offset are no group's
+    off = np.maximum.accumulate(offsets)
+    Y, D = np.full((rows + 3, n), 11.0), np.full((rows + 3, k), -7.0)
+    args = up(dy, BF), up(x, BF), up(w, BF), up(np.array(offsets, np.int32))
+    want_y = bf16_rounded(oracle.grouped_matmul(x, w, off, Y))
+    want_dx = bf16_rounded(oracle.grouped_matmul_backward(dy, x, w, off, D)[0])
+    want_dw = np.stack([dy[i:max(i, j)].T @ x[i:max(i, j)] for i, j in zip(offsets, offsets[1:])])
+    for _ in range(2):
+        np.testing.assert_array_equal(f64(moe.grouped_matmul(*args[1:], out=up(Y, BF))), want_y)
+        dx, dw = moe.grouped_matmul_backward(*args, dx=up(D, BF))
+        np.testing.assert_array_equal(f64(dx), want_dx)
+        np.testing.assert_array_equal(f64(dw), want_dw)
+
+
 def test_grouped_empty_calls():
     w = torch.ones((3, 16, 24), dtype=BF, device=dev())
     off = torch.zeros(4, dtype=torch.int32, device=dev())
