@@ -28,6 +28,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import os
+import warnings
 from typing import Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -564,7 +565,9 @@ def grouped_matmul(x, w, offsets, out=None, stream=None):
     (moe_grouped_matmul): x [rows, k] bf16 (its rows contiguous), w [num_groups, n, k]
     bf16, offsets [num_groups + 1] int32 on the device, as Plan.route gives them.
     Rows outside every group are left as they were (undefined in a new `out`).
-    No autograd graph is recorded: grouped_matmul_backward gives the gradients."""
+    No autograd graph is recorded: grouped_matmul_backward gives the gradients.  A
+    call that autograd would have recorded warns; under torch.no_grad(), or inside
+    a torch.autograd.Function, it does not."""
     import torch
     groups, n, k = _grouped(w, offsets)
     ld = _rows(x, "x", (torch.bfloat16,), k, w)
@@ -576,6 +579,8 @@ def grouped_matmul(x, w, offsets, out=None, stream=None):
     else:
         _need_shape(out, "out", torch.bfloat16, (rows, n), w)
         _apart(out, "out", ("x", x), ("w", w), ("offsets", offsets))
+    if (x.requires_grad or w.requires_grad) and torch.is_grad_enabled():
+        warnings.warn("grouped_matmul records no autograd graph: the gradients are grouped_matmul_backward's", stacklevel=2)
     lib, used, space, size = load_library(), (x, w, offsets, out), None, 0
     if k > 3000:   # a shorter sum is never split
         size = lib.moe_grouped_matmul_workspace(rows, groups, n, k)

@@ -1,6 +1,7 @@
 """Refusals of the MXFP4 quantiser and product and of the grouped products:
 the C entries' checks (no GPU is touched) and the binding's."""
 import os
+import warnings
 
 import pytest
 import torch
@@ -243,3 +244,24 @@ def test_the_stride_of_a_matrix_that_is_not_read_is_not_checked(lib):
     no_dw = lambda ldx: (None, 16, None, ldx, P, P, 0, 2, 16, 64, None, None, 0, None, 0, None)
     assert [lib.moe_grouped_matmul_backward(*no_dw(ldx)) for ldx in (0, -8, 3, 64)] == [0] * 4
     refused(lib, "moe_grouped_matmul_backward", (P, 16, P, 0, P, P, 4, 2, 16, 64, None, P, 0, None, 0, None), 2, "ldx must be")
+
+
+@pytest.mark.parametrize("leaf", ["x", "w"])
+def test_a_gradient_that_would_be_lost_is_warned_of(lib, leaf):
+    """grouped_matmul records no graph: where autograd would have, it says so."""
+    t = {"x": z(4, 64), "w": z(2, 16, 64)}
+    t[leaf].requires_grad_()
+
+    def call():
+        with pytest.raises(moe.MoeError, match="must be on a GPU"):
+            moe.grouped_matmul(t["x"], t["w"], z(3, dtype=I32))
+
+    with pytest.warns(UserWarning, match="grouped_matmul records no autograd graph") as seen:
+        call()
+    assert seen[0].filename == __file__
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        with torch.no_grad():
+            call()
+        t[leaf].requires_grad_(False)
+        call()
