@@ -48,9 +48,10 @@ typedef enum {
   MOE_ERR_ARG = 1,          /* null pointer, bad enum, negative count */
   MOE_ERR_SHAPE = 2,        /* dimension not supported (see moe_mxfp4_config) */
   MOE_ERR_ALIGN = 3,        /* a device pointer is not 16-byte aligned */
-  MOE_ERR_CAPACITY = 4,     /* num_tokens > max_tokens, or memory too small */
+  MOE_ERR_CAPACITY = 4,     /* num_tokens > max_tokens or than the fixed scratch holds; workspace of a grouped
+                               product too small */
   MOE_ERR_SCALE_BYTE = 5,   /* a weight scale byte is not accepted (plan) */
-  MOE_ERR_WORKSPACE = 6,    /* workspace or repacked buffer too small */
+  MOE_ERR_WORKSPACE = 6,    /* a plan's workspace or repacked buffer too small */
   MOE_ERR_UNSUPPORTED = 7,  /* device is not gfx950 */
   MOE_ERR_HIP = 8,          /* a HIP runtime call failed (text from hipGetErrorString) */
   MOE_ERR_TIMEOUT = 9       /* a wait of a fused forward passed its time bound (moe_mxfp4_fused_status) */
@@ -286,8 +287,9 @@ moe_status moe_mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, con
  * strides multiples of 8 up to 2^20.  Enqueue-only.
  *   workspace  NULL, or device memory of moe_grouped_matmul_workspace bytes (0
  *           for most sizes) that nothing else uses until the call has run: few
- *           rows and columns with a long sum are then summed in parts, in a
- *           second launch joined in order, which spreads them over the GPU */
+ *           rows and columns with a long sum are then summed in parts, which
+ *           more workgroups share, and joined in order in a second launch.
+ *           Smaller memory than that is MOE_ERR_CAPACITY */
 size_t moe_grouped_matmul_workspace(int32_t rows, int32_t num_groups, int32_t n, int32_t k);
 moe_status moe_grouped_matmul(const uint16_t* x, int64_t ldx, const uint16_t* w, const int32_t* offsets, int32_t rows,
                               int32_t num_groups, int32_t n, int32_t k, uint16_t* out, void* workspace,
