@@ -544,6 +544,12 @@ def mxfp4_matmul(a_codes, a_scales, b_codes, b_scales, dtype=None, out=None, str
     return out
 
 
+# No reduction of at most this many terms (a group's, of rows) is split by the
+# grouped entries, whatever the other sizes: their workspace sizes, a question
+# that costs a small call 0.5 us, are asked for above it only.
+_LONGEST_WHOLE_SUM = 3000
+
+
 def _grouped(w, offsets):
     import torch
     try:
@@ -582,7 +588,7 @@ def grouped_matmul(x, w, offsets, out=None, stream=None):
     if (x.requires_grad or w.requires_grad) and torch.is_grad_enabled():
         warnings.warn("grouped_matmul records no autograd graph: the gradients are grouped_matmul_backward's", stacklevel=2)
     lib, used, space, size = load_library(), (x, w, offsets, out), None, 0
-    if k > 3000:   # a shorter sum is never split
+    if k > _LONGEST_WHOLE_SUM:
         size = lib.moe_grouped_matmul_workspace(rows, groups, n, k)
         if size:
             space = _new((size,), torch.uint8, x, stream)
@@ -635,7 +641,7 @@ def grouped_matmul_backward(dy, x, w, offsets, dx=None, dw=None, dw_dtype=None, 
         raise _arg_error("dx is given, but need_dx is False")
     lib, space = load_library(), None
     size = 0
-    if n > 3000 or rows > 3000 * groups:   # shorter sums are never split
+    if n > _LONGEST_WHOLE_SUM or rows > _LONGEST_WHOLE_SUM * groups:
         size = lib.moe_grouped_matmul_backward_workspace(rows, groups, n, k, need_dx, need_dw)
     if size:
         used.append(_new((size,), torch.uint8, w, stream))

@@ -265,3 +265,18 @@ def test_a_gradient_that_would_be_lost_is_warned_of(lib, leaf):
             call()
         t[leaf].requires_grad_(False)
         call()
+
+
+def test_the_binding_asks_for_every_workspace_there_is(lib):
+    """Sums that the binding takes to be whole are: no workspace for any of them, while one
+    is given not far above (the binding's limit is the entries' rule, not a looser one)."""
+    fwd, bwd = lib.moe_grouped_matmul_workspace, lib.moe_grouped_matmul_backward_workspace
+    most = moe._LONGEST_WHOLE_SUM
+    lengths = list(range(8, most + 1, 8))
+    for rows, groups, other in ((1, 1, 8), (1, 4096, 8), (64, 1, 128), (300, 2, 512), (4000, 1, 64), (700, 40, 8192)):
+        assert not any(fwd(rows, groups, other, length) for length in lengths), (rows, groups, other)
+        assert not any(bwd(rows, groups, length, other, 1, 0) for length in lengths), (rows, groups, other)
+    for groups, n, k in ((1, 8, 8), (1, 584, 184), (7, 128, 128), (64, 64, 64)):
+        assert not any(bwd(rows * groups, groups, n, k, 0, 1) for rows in lengths), (groups, n, k)
+    near = most + most // 10
+    assert fwd(64, 1, 64, near // 8 * 8) and bwd(64, 1, near // 8 * 8, 64, 1, 0) and bwd(2 * near, 2, 64, 64, 0, 1)
