@@ -310,6 +310,73 @@ def test_grouped_sums_in_parts_and_whole(counts, n, k):
         assert torch.equal(g, t)
 
 
+PARTS = [([718], 64, 6672), ([1, 0, 3] * 6, 264, 5552), ([90, 30], 4104, 72), ([3300], 3208, 72), ([6000, 566], 584, 184)]
+
+
+@pytest.mark.parametrize("counts,n,k", PARTS)
+def test_grouped_sums_in_parts_of_real_values(counts, n, k):
+    """A sum in parts has no more additions, one after another, than the whole one: the same bounds."""
+    rng = np.random.default_rng(n)
+    off = offsets_of(counts)
+    rows = int(off[-1])
+    assert moe.load_library().moe_grouped_matmul_workspace(rows, len(counts), n, k) + \
+        moe.load_library().moe_grouped_matmul_backward_workspace(rows, len(counts), n, k, 1, 1) > 0
+    x, dy = (torch.from_numpy(rng.standard_normal((rows, c)) * np.exp2(rng.integers(-6, 7, (rows, 1)))).to(BF) for c in (k, n))
+    w = torch.from_numpy(rng.standard_normal((len(counts), n, k)) / 40).to(BF)
+    X, DY, W = f64(x), f64(dy), f64(w)
+    y = moe.grouped_matmul(x.to(dev()), w.to(dev()), up(off))
+    dx, dw = moe.grouped_matmul_backward(dy.to(dev()), x.to(dev()), w.to(dev()), up(off))
+    zero = lambda c: np.zeros((rows, c))
+    want = oracle.grouped_matmul(X, W, off, zero(n)), *oracle.grouped_matmul_backward(DY, X, W, off, zero(k))
+    size = (oracle.grouped_matmul(abs(X), abs(W), off, zero(n)),
+            *oracle.grouped_matmul_backward(abs(DY), abs(X), abs(W), off, zero(k)))
+    for name, got, ref, big, terms in (("y", y, want[0], size[0], k), ("dx", dx, want[1], size[1], n),
+                                       ("dw", dw, want[2], size[2], max(counts))):
+        bound = terms * 2.0 ** -23 * big
+        if got.dtype == BF:
+            bound = bound + 2.0 ** -8 * (abs(ref) + bound)
+        assert (abs(f64(got) - ref) <= bound).all(), name
+
+
+@pytest.mark.parametrize("dw_dtype", [BF, torch.float32])
+@pytest.mark.parametrize("counts,n,k", [([6600, 0], 584, 184), ([9700, 0, 30], 64, 184), ([0, 6600], 40, 72)])
+def test_grouped_weight_gradients_in_parts_of_an_empty_group(counts, n, k, dw_dtype):
+    """Parts without rows still give zeros: dw held NaN."""
+    off, x, dy, w = grouped_case(counts, n, k, 1, 2, 5)
+    assert moe.load_library().moe_grouped_matmul_backward_workspace(len(x), len(counts), n, k, 0, 1) > 0
+    dw = torch.full(w.shape, float("nan"), dtype=dw_dtype, device=dev())
+    moe.grouped_matmul_backward(up(poisoned(dy, off), BF), up(poisoned(x, off), BF), up(w, BF), up(off), dw=dw, need_dx=False)
+    want = oracle.grouped_matmul_backward(dy, x, w, off, np.zeros(x.shape))[1]
+    np.testing.assert_array_equal(f64(dw), want if dw_dtype == torch.float32 else bf16_rounded(want))
+
+
+@pytest.mark.parametrize("counts,n,k", PARTS)
+def test_grouped_sums_in_parts_on_another_stream(counts, n, k):
+    """The workspace is the given stream's, the inputs are kept until it has passed: neither is
+    given to what either stream allocates right after the call."""
+    off, x, dy, w = grouped_case(counts, n, k, 0, 0, 21)
+    X, DY, W, O = up(x, BF), up(dy, BF), up(w, BF), up(off)
+    want = moe.grouped_matmul(X, W, O), *moe.grouped_matmul_backward(DY, X, W, O)
+    busy = torch.ones((4096, 4096), dtype=BF, device=dev())
+    sizes = {t.numel() for t in (X, DY, W, O)} | {want[2].numel() * 8, 1 << 19, 1 << 21}
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        args = [t.clone() for t in (DY, X, W, O)]
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            for _ in range(4):
+                torch.mm(busy, busy)
+        got = moe.grouped_matmul(*args[1:], stream=s), *moe.grouped_matmul_backward(*args, stream=s)
+        del args
+        junk = [torch.full((m,), float("nan"), device=dev()) for m in sizes]
+        with torch.cuda.stream(s):
+            junk += [torch.full((m,), float("nan"), device=dev()) for m in sizes]
+        torch.cuda.current_stream().wait_stream(s)
+        for g, t in zip(got, want):
+            assert torch.equal(g, t)
+        del junk, got
+
+
 def test_grouped_sums_in_parts_in_a_graph():
     off, x, dy, w = grouped_case([90, 30], 4104, 72, 1, 1, 9)
     X, DY, W, O = up(x, BF), up(dy, BF), up(w, BF), up(off)
