@@ -304,8 +304,9 @@ moe_status moe_grouped_matmul(const uint16_t* x, int64_t ldx, const uint16_t* w,
  *      decreasing offsets each group's own two count here: a decreasing pair
  *      is an empty group, a row between two groups' offsets is in both sums
  * A NULL gradient is not computed; w is read for dx only, x for dw only, and
- * either may be NULL where it is not read.  Each output is one fp32 sum in a
- * fixed order, rounded once (no atomics).  Enqueue-only. */
+ * either may be NULL where it is not read.  Each output is an fp32 sum in a
+ * fixed order, which follows from the call's sizes and, where a sum is split,
+ * from the workspace; it is rounded once (no atomics).  Enqueue-only. */
 size_t moe_grouped_matmul_backward_workspace(int32_t rows, int32_t num_groups, int32_t n, int32_t k, int32_t need_dx,
                                              int32_t need_dw);
 moe_status moe_grouped_matmul_backward(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx,

@@ -31,7 +31,8 @@
 //     (row >> 3) & 1: the eight rows that half a wave's transposed read takes
 //     lie in eight different halves, again all 64 banks.
 // Both operands number the reduction alike, so every output is one fp32 sum
-// in ascending order of 32 values an MFMA, whatever the tile.
+// in ascending order of 32 values an MFMA, whatever the tile; in a split
+// reduction each part is such a sum and the parts are added in their order.
 //
 // Q is the instruction's first operand: a lane then ends with four
 // consecutive columns of one output row, stored together.
