@@ -314,6 +314,89 @@ moe_status moe_grouped_matmul_backward(const uint16_t* dy, int64_t lddy, const u
                                        int32_t n, int32_t k, uint16_t* dx, void* dw, int32_t dw_dtype,
                                        void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* Router with scores: the topk_ids / topk_weights that moe_mxfp4_forward
+ * consumes, from logits [num_tokens, num_experts] of `dtype`, rows ldl apart.
+ * A logit of -inf or NaN masks its expert for that token; one above fp32's
+ * largest number counts as it.
+ *   score s_e   MOE_SCORE_SOFTMAX: exp(l_e) / sum of exp(l) over the experts
+ *               that are not masked; MOE_SCORE_SIGMOID: 1 / (1 + exp(-l_e))
+ *   value c_e   s_e + bias_e (bias [num_experts] fp32, -inf or NaN: the expert
+ *               is never selected), in fp64; with bias NULL experts rank by l_e
+ *   groups      num_groups (1..64) runs of num_experts / num_groups experts: the
+ *               group_limit groups with the largest sum of their group_top (1
+ *               or 2) largest values (without a bias: scores) stay, the lower
+ *               group first where sums are equal in fp64
+ *   topk_ids    [num_tokens, top_k] int32: the largest values of the experts
+ *               that stay, in descending order, the lower id first where they
+ *               are equal; -1 once none is left (a token whose experts are all
+ *               masked: -1 throughout), which the forward counts as no route
+ *   topk_weights [num_tokens, top_k] fp32: scale * s_id, or with renormalize
+ *               scale * s_id / sum of the selected scores (taken relative to
+ *               the largest, so that no score is too small); 0 for id -1
+ * 1 <= num_experts <= 1024, 1 <= top_k <= min(32, group_limit * num_experts /
+ * num_groups), num_tokens <= 2^24, 0 is a no-op.  logits, bias, ids and weights
+ * need their element's alignment only.  Enqueue-only, no workspace. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+moe_status moe_router_select(const void* logits, int32_t dtype, int64_t ldl, int32_t num_tokens, int32_t num_experts,
+                             int32_t top_k, int32_t score, const float* bias, int32_t num_groups, int32_t group_limit,
+                             int32_t group_top, int32_t renormalize, float scale, int32_t* topk_ids,
+                             float* topk_weights, hipStream_t stream);
+
+/* Gradient of moe_router_select's weights for dweights [num_tokens, top_k]
+ * fp32 and the ids it gave (selection itself has no gradient, so a bias has
+ * none): dlogits [num_tokens, num_experts] of `dtype`, contiguous and 16-byte
+ * aligned, every element written: fp32 sums rounded once.  Slots whose id is
+ * outside [0, num_experts) or whose expert is masked add nothing, whatever
+ * their dweights; an id given twice gets both slots' terms.  Enqueue-only. */
+moe_status moe_router_select_backward(const float* dweights, const void* logits, int32_t dtype, int64_t ldl,
+                                      const int32_t* topk_ids, int32_t num_tokens, int32_t num_experts, int32_t top_k,
+                                      int32_t score, int32_t renormalize, float scale, void* dlogits,
+                                      hipStream_t stream);
+
+/* Product of bf16 rows with an MXFP4 matrix (a shared expert or a projection
+ * beside the routed ones, for one token or many; W in checkpoint layout):
+ *   gate 0:  out [m, n] = x W^T
+ *   gate 1:  out [m, n/2] = silu(x Wg^T) * (x Wu^T), W = [Wg; Wu] as in the
+ *            fused w1||w3, silu(z) = z / (1 + exp(-z)); n even
+ *   x [m, k] bf16, rows ldx apart (a multiple of 8 up to 2^20);
+ *   codes [n, k/2], scales [n, k/32]; any scale byte, as moe_mxfp4_dequantize
+ *   reads it
+ * Sums and the gate are fp32, rounded once to `dtype`.  k a multiple of 32 in
+ * [32, 65536]; m and n in [0, 2^19], 0 is a no-op.  Enqueue-only, no
+ * workspace. */
+moe_status moe_mxfp4_linear(const uint16_t* x, int64_t ldx, const uint8_t* codes, const uint8_t* scales, int32_t m,
+                            int32_t n, int32_t k, int32_t gate, int32_t dtype, void* out, hipStream_t stream);
+
+/* Each token's sum of its routes' rows: the layer's epilogue for rows that
+ * moe_grouped_matmul made, in the order that moe_mxfp4_route gives.
+ *   out [num_tokens, hidden] of `dtype`: out_t = sum over slots s, ascending,
+ *       of weights[t,s] * y[rowpos[t,s]], in fp32, rounded once
+ *   y [rows, hidden] bf16, rows ldy apart; rowpos [num_tokens, top_k] int32: a
+ *       value outside [0, rows) is no route (neither y nor its weight is read)
+ *   weights [num_tokens, top_k] fp32, or NULL: all 1 (the gradient of gathering
+ *       rows by perm[r] / top_k)
+ * hidden a multiple of 8 in [8, 65536], top_k <= 32, num_tokens <= 2^21, rows
+ * <= 2^26; rowpos, perm and weights need 4-byte alignment only.  Enqueue-only. */
+moe_status moe_expert_combine(const uint16_t* y, int64_t ldy, int32_t rows, const int32_t* rowpos,
+                              const float* weights, int32_t num_tokens, int32_t top_k, int32_t hidden, int32_t dtype,
+                              void* out, hipStream_t stream);
+
+/* Gradients of moe_expert_combine for dout [num_tokens, hidden] of
+ * `dout_dtype`, rows lddout apart:
+ *   dy       [rows, hidden] bf16 or NULL: dy_r = weights[t,s] * dout_t for the
+ *            route f = t * top_k + s = perm[r] with rowpos[f] = r (perm [rows]
+ *            as moe_mxfp4_route writes it); other rows are left as they were,
+ *            and none is written twice, whatever the indexes hold
+ *   dweights [num_tokens, top_k] fp32 or NULL: <dout_t, y[rowpos[t,s]]>, 0 for no
+ *            route; an fp32 sum in a fixed order
+ * A NULL gradient is not computed; y is read for dweights only and perm for dy
+ * only, and either may be NULL where it is not read.  With weights NULL, dy is
+ * dout's rows gathered into the experts' order.  Enqueue-only. */
+moe_status moe_expert_combine_backward(const void* dout, int32_t dout_dtype, int64_t lddout, const uint16_t* y,
+                                       int64_t ldy, int32_t rows, const int32_t* rowpos, const int32_t* perm,
+                                       const float* weights, int32_t num_tokens, int32_t top_k, int32_t hidden,
+                                       uint16_t* dy, float* dweights, hipStream_t stream);
+
 /* Peak micro-benchmarks: the measured ceilings a benchmark reports its
  * kernels against beside the published peaks (the pages record each run's
  * GPU operating state because the clock policy moved their numbers: b12x PR

@@ -20,6 +20,11 @@ Names follow the C ABI in include/moe_mxfp4.h:
   mxfp4_matmul(a_codes, a_scales, b_codes, b_scales)  -> A B^T       (moe_mxfp4_matmul)
   grouped_matmul(x, w, offsets)         rows sorted by group times the group's matrix (moe_grouped_matmul)
   grouped_matmul_backward(dy, x, w, offsets)          -> (dx, dw)    (moe_grouped_matmul_backward)
+  router_select(logits, k, ...)         -> (topk_ids, topk_weights)  (moe_router_select)
+  router_select_backward(dweights, logits, ids, ...)  -> dlogits     (moe_router_select_backward)
+  mxfp4_linear(x, codes, scales)        bf16 rows times an MXFP4 matrix, plain or gated (moe_mxfp4_linear)
+  expert_combine(y, rowpos, weights)    weighted sum of each token's rows (moe_expert_combine)
+  expert_combine_backward(dout, y, rowpos, perm, weights)  -> (dy, dweights)  (moe_expert_combine_backward)
   probe_memory(kind, src, dst, sink)    peak micro-benchmarks (moe_probe_memory / moe_probe_mfma)
   probe_mfma(kind, iters, sink)         -> flops of the launch
 """
@@ -46,7 +51,8 @@ EXPORTS = ("moe_mxfp4_query_sizes", "moe_mxfp4_plan", "moe_mxfp4_forward", "moe_
            "moe_mxfp4_fused_status", "moe_mxfp4_route", "moe_mxfp4_workspace_region", "moe_mxfp8_quantize",
            "moe_router_topk", "moe_mxfp4_quantize", "moe_mxfp4_dequantize", "moe_mxfp4_matmul",
            "moe_grouped_matmul", "moe_grouped_matmul_backward", "moe_grouped_matmul_workspace",
-           "moe_grouped_matmul_backward_workspace", "moe_probe_memory", "moe_probe_mfma", "moe_probe_mfma_f8f4_blocks",
+           "moe_grouped_matmul_backward_workspace", "moe_router_select", "moe_router_select_backward",
+           "moe_mxfp4_linear", "moe_expert_combine", "moe_expert_combine_backward", "moe_probe_memory", "moe_probe_mfma", "moe_probe_mfma_f8f4_blocks",
            "moe_mxfp4_set_stage_events",
            "moe_mxfp4_destroy", "moe_mxfp4_last_error")
 _STATUS_FNS = tuple(n for n in EXPORTS if n not in ("moe_mxfp4_destroy", "moe_mxfp4_last_error") and not n.endswith("_workspace"))
@@ -110,6 +116,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_grouped_matmul_workspace.argtypes = [i32] * 4
     lib.moe_grouped_matmul_backward_workspace.argtypes = [i32] * 6
     lib.moe_grouped_matmul_workspace.restype = lib.moe_grouped_matmul_backward_workspace.restype = sz
+    f32 = ctypes.c_float
+    lib.moe_router_select.argtypes = [vp, i32, i64, i32, i32, i32, i32, vp, i32, i32, i32, i32, f32, vp, vp, vp]
+    lib.moe_router_select_backward.argtypes = [vp, vp, i32, i64, vp, i32, i32, i32, i32, i32, f32, vp, vp]
+    lib.moe_mxfp4_linear.argtypes = [vp, i64, vp, vp, i32, i32, i32, i32, i32, vp, vp]
+    lib.moe_expert_combine.argtypes = [vp, i64, i32, vp, vp, i32, i32, i32, i32, vp, vp]
+    lib.moe_expert_combine_backward.argtypes = [vp, i32, i64, vp, i64, i32, vp, vp, vp, i32, i32, i32, vp, vp, vp]
     lib.moe_probe_memory.argtypes = [i32, vp, vp, sz, vp, i32, vp]
     lib.moe_probe_mfma.argtypes = [i32, i32, vp, i32, ctypes.POINTER(ctypes.c_double), vp]
     lib.moe_probe_mfma_f8f4_blocks.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp]
@@ -650,6 +662,214 @@ def grouped_matmul_backward(dy, x, w, offsets, dx=None, dw=None, dw_dtype=None, 
             (dy.data_ptr(), lddy, x_at, ldx, w.data_ptr(), offsets.data_ptr(), rows, groups, n, k, dx_at, dw_at, code,
              space, size), w, stream, used)
     return dx, dw
+
+
+def _warn_no_graph(name: str, gradient: str, *tensors):
+    """Warn where autograd would have recorded the call."""
+    import torch
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        warnings.warn(f"{name} records no autograd graph{gradient}", stacklevel=3)
+
+
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+
+
+def _logits(logits):
+    """(rows, experts, row stride, type code) of a router's logits."""
+    import torch
+    ld = _rows(logits, "logits", (torch.float32, torch.bfloat16), None, None)
+    rows, experts = logits.shape
+    if (rows | experts) >> 31:
+        raise _too_large(num_tokens=rows, num_experts=experts)
+    return rows, experts, ld, MOE_F32 if logits.dtype is torch.float32 else MOE_BF16
+
+
+def router_select(logits, top_k, score=MOE_SCORE_SOFTMAX, bias=None, num_groups=1, group_limit=1, group_top=1,
+                  renormalize=True, scale=1.0, ids=None, weights=None, stream=None):
+    """topk_ids int32 [T, k] and topk_weights fp32 [T, k] from logits [T, E] in fp32
+    or bf16 (moe_router_select).  Experts are ranked by score (softmax over the
+    row, or sigmoid) plus bias fp32 [E]; of num_groups equal runs of experts the
+    group_limit with the largest sums of their group_top best are kept; weights
+    are scale times the selected scores, which do not contain the bias,
+    renormalised to a sum of 1 by default.  An expert with a logit of -inf or NaN
+    is never selected; slots for which no expert is left get id -1 and weight 0.
+    No autograd graph is recorded: router_select_backward gives the gradient (a
+    call that autograd would have recorded warns)."""
+    import torch
+    rows, experts, ld, code = _logits(logits)
+    if max(top_k, num_groups, group_limit, group_top) >> 31 > 0:
+        raise _too_large(top_k=top_k, num_groups=num_groups, group_limit=group_limit, group_top=group_top)
+    if not 0 < top_k <= experts:
+        raise MoeError(MOE_ERR_SHAPE, f"top_k must be in [1, {experts}], got {top_k}")
+    shape = (rows, top_k)
+    used = [logits]
+    if bias is not None:
+        _need_shape(bias, "bias", torch.float32, (experts,), logits)
+        used.append(bias)
+    if ids is None:
+        ids = _new(shape, torch.int32, logits, stream)
+    else:
+        _need_shape(ids, "ids", torch.int32, shape, logits)
+        _apart(ids, "ids", *zip(("logits", "bias"), used))
+    if weights is None:
+        weights = _new(shape, torch.float32, logits, stream)
+    else:
+        _need_shape(weights, "weights", torch.float32, shape, logits)
+        _apart(weights, "weights", ("ids", ids), *zip(("logits", "bias"), used))
+    if logits.requires_grad:
+        _warn_no_graph("router_select", ": the gradient is router_select_backward's", logits)
+    _launch(load_library().moe_router_select,
+            (logits.data_ptr(), code, ld, rows, experts, top_k, score, _ptr(bias), num_groups, group_limit, group_top,
+             bool(renormalize), scale, ids.data_ptr(), weights.data_ptr()), logits, stream, (*used, ids, weights))
+    return ids, weights
+
+
+def router_select_backward(dweights, logits, ids, score=MOE_SCORE_SOFTMAX, renormalize=True, scale=1.0, dlogits=None,
+                           stream=None):
+    """The gradient [T, E] of router_select's logits, in their type, for dweights
+    fp32 [T, k] and the ids int32 [T, k] that it gave; score, renormalize and
+    scale as there (moe_router_select_backward)."""
+    import torch
+    rows, experts, ld, code = _logits(logits)
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise _arg_error("ids must be a 2-D torch.Tensor [T, top_k]")
+    shape = (rows, ids.shape[1])
+    if shape[1] >> 31:
+        raise _too_large(top_k=shape[1])
+    _need_shape(ids, "ids", torch.int32, shape, logits)
+    _need_shape(dweights, "dweights", torch.float32, shape, logits)
+    if dlogits is None:
+        dlogits = _new((rows, experts), logits.dtype, logits, stream)
+    else:
+        _need_shape(dlogits, "dlogits", logits.dtype, (rows, experts), logits)
+        _apart(dlogits, "dlogits", ("dweights", dweights), ("logits", logits), ("ids", ids))
+    _launch(load_library().moe_router_select_backward,
+            (dweights.data_ptr(), logits.data_ptr(), code, ld, ids.data_ptr(), rows, experts, shape[1], score,
+             bool(renormalize), scale, dlogits.data_ptr()), logits, stream, (dweights, logits, ids, dlogits))
+    return dlogits
+
+
+def mxfp4_linear(x, codes, scales, gate=False, dtype=None, out=None, stream=None):
+    """x W^T [m, n] of bf16 rows x [m, k] (contiguous, or a slice of wider ones) and
+    an MXFP4 matrix W [n, k] (codes uint8 [n, k/2], scales uint8 [n, k/32]), summed
+    in fp32 and rounded once to bf16 (default) or left in fp32 (moe_mxfp4_linear).
+    gate: W is a fused w1||w3 and the result silu(x w1^T) * (x w3^T) [m, n/2].
+    No autograd graph is recorded (a call that autograd would have recorded
+    warns): the weights are four-bit constants."""
+    import torch
+    n, k = _mxfp4_operand(codes, scales, "codes", "scales", codes)
+    ld = _rows(x, "x", (torch.bfloat16,), k, codes)
+    m = x.shape[0]
+    if m >> 31:
+        raise _too_large(m=m)
+    if gate and n % 2:
+        raise MoeError(MOE_ERR_SHAPE, f"a gated product needs an even n, got {n}")
+    out, code = _float_out(out, "out", (m, n // 2 if gate else n), dtype, codes, stream, ("x", x), ("codes", codes),
+                           ("scales", scales))
+    if x.requires_grad:
+        _warn_no_graph("mxfp4_linear", "", x)
+    _launch(load_library().moe_mxfp4_linear,
+            (x.data_ptr(), ld, codes.data_ptr(), scales.data_ptr(), m, n, k, bool(gate), code, out.data_ptr()), codes,
+            stream, (x, codes, scales, out))
+    return out
+
+
+def _routes(rowpos, weights, like):
+    """(tokens, top_k) of rowpos and the weights, if there are any."""
+    import torch
+    if not isinstance(rowpos, torch.Tensor) or rowpos.dim() != 2:
+        raise _arg_error("rowpos must be a 2-D torch.Tensor [T, top_k]")
+    shape = rowpos.shape
+    _need_shape(rowpos, "rowpos", torch.int32, shape, like)
+    if weights is not None:
+        _need_shape(weights, "weights", torch.float32, shape, like)
+    return shape
+
+
+def expert_combine(y, rowpos, weights=None, dtype=None, out=None, stream=None):
+    """out [T, hidden]: each token's sum over its slots of weights[t, s] times the row
+    rowpos[t, s] of y [rows, hidden] bf16, in fp32 and rounded once to bf16
+    (default) or left in fp32 (moe_expert_combine).  rowpos int32 [T, k] as
+    Plan.route gives it (reshaped); a value outside [0, rows) is no route.
+    weights fp32 [T, k], None: all 1.  No autograd graph is recorded:
+    expert_combine_backward gives the gradients (a call that autograd would have
+    recorded warns)."""
+    import torch
+    ld = _rows(y, "y", (torch.bfloat16,), None, None)
+    rows, hidden = y.shape
+    tokens, top_k = _routes(rowpos, weights, y)
+    if (rows | hidden | tokens | top_k) >> 31:
+        raise _too_large(rows=rows, hidden=hidden, num_tokens=tokens, top_k=top_k)
+    used = [("y", y), ("rowpos", rowpos)]
+    if weights is not None:
+        used.append(("weights", weights))
+    out, code = _float_out(out, "out", (tokens, hidden), dtype, y, stream, *used)
+    if y.requires_grad or weights is not None and weights.requires_grad:
+        _warn_no_graph("expert_combine", ": the gradients are expert_combine_backward's", y, weights)
+    _launch(load_library().moe_expert_combine,
+            (y.data_ptr(), ld, rows, rowpos.data_ptr(), _ptr(weights), tokens, top_k, hidden, code, out.data_ptr()), y,
+            stream, (*(t for _, t in used), out))
+    return out
+
+
+def expert_combine_backward(dout, y, rowpos, perm=None, weights=None, dy=None, dweights=None, need_dy=True,
+                            need_dw=True, stream=None):
+    """(dy, dweights) of expert_combine for dout [T, hidden] in bf16 or fp32: dy
+    [rows, hidden] bf16, dy[r] = weights[t, s] * dout[t] for the route t * k + s =
+    perm[r] (rows without one are left as they were, undefined in a new dy);
+    dweights fp32 [T, k], 0 for no route (moe_expert_combine_backward).  rowpos
+    int32 [T, k] and perm int32 [rows] as Plan.route gives them.  need_dy /
+    need_dw False: that gradient is not computed and returned as None (perm is
+    read for dy only and y for dweights only; either may then be None).  With
+    weights None and need_dw False, dy is the rows of dout in the experts' order."""
+    import torch
+    if not (need_dy or need_dw):
+        raise _arg_error("need_dy or need_dw must be True")
+    ld = _rows(dout, "dout", (torch.bfloat16, torch.float32), None, None)
+    tokens, top_k = _routes(rowpos, weights, dout)
+    hidden = dout.shape[1]
+    if dout.shape[0] != tokens:
+        raise _arg_error(f"dout must have rowpos's {tokens} rows, got shape {tuple(dout.shape)}")
+    used = [("dout", dout), ("rowpos", rowpos)]
+    if weights is not None:
+        used.append(("weights", weights))
+    rows, ldy, y_at, dy_at, perm_at, dw_at = None, hidden, None, None, None, None
+    if need_dw:
+        ldy = _rows(y, "y", (torch.bfloat16,), hidden, dout)
+        rows, y_at = y.shape[0], y.data_ptr()
+        used.append(("y", y))
+    elif dweights is not None:
+        raise _arg_error("dweights is given, but need_dw is False")
+    if need_dy:
+        if rows is None:
+            if not isinstance(perm, torch.Tensor) or perm.dim() != 1:
+                raise _arg_error("perm must be a 1-D torch.Tensor [rows]")
+            rows = perm.shape[0]
+        _need_shape(perm, "perm", torch.int32, (rows,), dout)
+        perm_at = perm.data_ptr()
+        used.append(("perm", perm))
+        if dy is None:
+            dy = _new((rows, hidden), torch.bfloat16, dout, stream)
+        else:
+            _need_shape(dy, "dy", torch.bfloat16, (rows, hidden), dout)
+            _apart(dy, "dy", *used)
+        dy_at = dy.data_ptr()
+    elif dy is not None:
+        raise _arg_error("dy is given, but need_dy is False")
+    if need_dw:
+        if dweights is None:
+            dweights = _new((tokens, top_k), torch.float32, dout, stream)
+        else:
+            _need_shape(dweights, "dweights", torch.float32, (tokens, top_k), dout)
+            _apart(dweights, "dweights", *used, *((("dy", dy),) if need_dy else ()))
+        dw_at = dweights.data_ptr()
+    if (rows | hidden | tokens | top_k) >> 31:
+        raise _too_large(rows=rows, hidden=hidden, num_tokens=tokens, top_k=top_k)
+    _launch(load_library().moe_expert_combine_backward,
+            (dout.data_ptr(), MOE_F32 if dout.dtype is torch.float32 else MOE_BF16, ld, y_at, ldy, rows,
+             rowpos.data_ptr(), perm_at, _ptr(weights), tokens, top_k, hidden, dy_at, dw_at), dout, stream,
+            [t for _, t in used] + [t for t in (dy, dweights) if t is not None])
+    return dy, dweights
 
 
 MOE_PROBE_READ, MOE_PROBE_READ_NT, MOE_PROBE_COPY = 0, 1, 2

@@ -196,6 +196,67 @@ constexpr int kRouterMaxExperts = 1024;
 hipError_t launch_router_topk(const float* logits, int32_t T, int32_t E, int32_t k, int32_t* ids, float* weights,
                               hipStream_t stream);
 
+// Router with scores, bias and groups, and its gradient (router_select.hip):
+// E <= kRouterMaxExperts, k <= kMaxTopK, groups <= kRouterMaxGroups, rows above zero.
+constexpr int kRouterMaxGroups = 64;
+struct SelectArgs {
+  const void* logits;   // [rows, experts] bf16 or (f32) fp32, rows ld apart
+  long long ld;
+  const float* bias;    // [experts] or null
+  int32_t* ids;         // [rows, top_k]
+  float* weights;       // [rows, top_k]
+  int rows, experts, top_k, groups, limit, group_top, score;
+  float scale;
+  bool f32, renormalize;
+};
+struct SelectBackwardArgs {
+  const float* dweights;   // [rows, top_k]
+  const void* logits;
+  long long ld;
+  const int32_t* ids;
+  void* dlogits;           // [rows, experts] of the logits' type
+  int rows, experts, top_k, score;
+  float scale;
+  bool f32, renormalize;
+};
+hipError_t launch_router_select(const SelectArgs& a, hipStream_t stream);
+hipError_t launch_router_select_backward(const SelectBackwardArgs& a, hipStream_t stream);
+
+// out [m, n] = x [m, k] W [n, k]^T with MXFP4 W, or (gate) silu of its first
+// n / 2 columns times the others (mxfp4_linear.hip); k a multiple of 32.
+struct LinearArgs {
+  const uint16_t* x;
+  long long ldx;
+  const uint8_t *codes, *scales;
+  void* out;
+  int m, n, k;
+};
+hipError_t launch_mxfp4_linear(const LinearArgs& a, bool gate, bool f32, hipStream_t stream);
+
+// Weighted sum of each token's route rows, and its gradients
+// (expert_combine.hip); hidden a multiple of 8, tokens above zero.
+struct CombineArgs {
+  const uint16_t* y;        // [rows, hidden] bf16, rows ldy apart
+  long long ldy;
+  const int32_t* rowpos;    // [tokens, top_k]
+  const float* weights;     // [tokens, top_k] or null (1)
+  void* out;                // [tokens, hidden] bf16 or fp32
+  int rows, tokens, top_k, hidden;
+};
+struct CombineBackwardArgs {
+  const void* dout;         // [tokens, hidden] bf16 or fp32, rows lddout apart
+  long long lddout;
+  const uint16_t* y;        // read for dweights only
+  long long ldy;
+  const int32_t *rowpos, *perm;   // perm [rows]: read for dy only
+  const float* weights;
+  uint16_t* dy;             // [rows, hidden] or null
+  float* dweights;          // [tokens, top_k] or null
+  int rows, tokens, top_k, hidden;
+};
+hipError_t launch_expert_combine(const CombineArgs& a, bool f32, hipStream_t stream);
+hipError_t launch_expert_combine_backward(const CombineBackwardArgs& a, bool f32, hipStream_t stream);
+
 // Peak micro-benchmarks (probe.hip).  `sink` holds one float per workgroup
 // (grid <= kProbeSinkFloats).
 constexpr int kProbeSinkFloats = 16384;

@@ -12,6 +12,7 @@ module):
   router   router top-k ids and softmax route weights from logits (upstream of the layer)
   moe      fp64 forward of the layer, MXFP8 activation quantisation
   operators  MXFP4 quantiser and product, products of ragged row groups and their gradients
+  selection  scored router and its gradient, product with an MXFP4 matrix, experts' combine and its gradients
   brute    scalar-loop brute force for tiny shapes
   compare  the acceptance rule (3 bf16 ULP or 4e-3 row relative L2)
 
@@ -31,6 +32,8 @@ from .moe import (expert_mlp, forward, fp32_dot_bound, mxfp8_dequantize, mxfp8_q
 from .compare import check_rows, rel_l2
 from .operators import (e2m1_encode, grouped_matmul, grouped_matmul_backward, mxfp4_matmul, mxfp4_quantize,
                         mxfp4_scale_exponent, mxfp4_values)
+from .selection import (expert_combine, expert_combine_backward, mxfp4_linear, router_select, router_select_backward,
+                        scores, selected_weights)
 from .brute import forward_brute, e2m1_closed_form
 
 __all__ = [n for n in dir() if not n.startswith("_")]
