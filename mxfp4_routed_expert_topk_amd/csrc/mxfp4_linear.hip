@@ -13,95 +13,268 @@ namespace moe {
 namespace {
 
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) void lds_void_t;
 
-// ---- few rows: W is streamed once per 16 MT rows of x.
-//
-// A workgroup owns 16 output columns and MT 16-row blocks of x; its kSplit
-// waves take 256 K at a time in turn and their partial sums are added in wave
-// order.  In 256 K a lane takes the 32 contiguous bytes of weight blocks 2q
-// and 2q + 1 (q its quarter of the wave) and x's values alike: which K values
-// share an MFMA does not matter to the sum.
-constexpr int kSplit = 8;
+constexpr uint32_t kPastEnd = 0x80000000u;   // beyond every buffer resource below
+
+// vmcnt <= n and lgkmcnt 0
+#define MOE_WAIT_VM(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (7 << 4) | ((((n) >> 4) & 3) << 14))
 
 __device__ __forceinline__ float gated(float g, float u) { return g / (1.f + expf(-g)) * u; }
 
-template <int MT, bool GATE, bool F32>
-__global__ __launch_bounds__(kSplit* kWave) void linear_rows(LinearArgs a) {
-  constexpr int NB = GATE ? 2 : 1;   // weight rows an output column needs
-  __shared__ f32x4_t part[kSplit][NB][MT][kWave];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// ---- few rows: the waves of a workgroup split K.
+//
+// A workgroup owns MT 16-row blocks of x and RB 16-row blocks of W; each of its
+// SPLIT waves has its part of K to itself, in chunks of 128, and their sums are
+// added in wave order. No barrier until then; DEPTH chunks are in flight.
+//   Everything passes through LDS, because a load serves sixteen consecutive
+// lanes at a time and costs a clock for every line that they touch: 64 for the
+// MFMA's own order, which has sixteen rows side by side (W and scales loaded so:
+// 64 columns of W over 8192 K, 25.7 us a workgroup, 11 GB/s). A copy of x is four
+// rows of 256 bytes, one of W sixteen rows of 64; the scales of a workgroup's
+// rows, one run of memory, come first and all at once.
+//   x: a row's 16-byte pieces are permuted by piece ^ 2 (row & 7), W's by piece ^
+// 2 (row >> 3): of the sixteen lanes that ds_read_b128 serves at once, eight rows
+// of one piece and the other eight of the next (lanes 0-3, 12-15, 20-27), no two
+// then share a bank.
+//   Lane quarter q reads the 16 bytes of block q of its row of W; two swaps of
+// 32-lane halves and two of 16-lane rows transpose them between the quarters,
+// dword q of block j for MFMA step j.
+//   With a gate and RB 1 the block is eight rows of w1 and the same eight of w3
+// (the lanes of an output's two values are 32 apart), else blocks alternate.
+// Byte j of s where the scaled converter reads it: bits 30:23, whatever the
+// others hold (checked for every byte).
+__device__ __forceinline__ float scale_byte(uint32_t s, int j) { return __uint_as_float(j < 3 ? s << (23 - 8 * j) : s >> 1); }
+
+// dword i of quarter q's lanes to dword q of quarter i's
+__device__ __forceinline__ void transpose_quarters(u32x4_t& v) {
+  const auto a = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
+  const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+  const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+  v = u32x4_t{c[0], c[1], d[0], d[1]};
+}
+
+// COPIES: of x for a chunk, four rows each.
+// GROUPS: the most scales a row has here.
+template <int MT, int RB, int SPLIT, int DEPTH, int COPIES, int GROUPS, bool GATE>
+__device__ __forceinline__ void linear_rows_block(uint8_t* smem, uint32_t* scale, const LinearArgs& a, bool f32) {
+  constexpr int kXBytes = COPIES * 1024, kPlace = kXBytes + RB * 1024;   // a chunk of x, and of W behind it
+  constexpr int kCols = GATE ? 8 * RB : 16 * RB;   // output columns
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
-  const int cols = GATE ? a.n / 2 : a.n, groups = a.k / 32;
-  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * (16 * MT);
-  // columns past the matrix repeat its last and are not stored
-  const int n = min(n0 + r, cols - 1);
-  f32x4_t acc[NB][MT];
+  const int cols = GATE ? a.n / 2 : a.n, groups = a.k / 32, c0 = blockIdx.x * kCols, m0 = blockIdx.y * (16 * MT);
+  const int chunks = (groups + 3) / 4, per = (chunks + SPLIT - 1) / SPLIT;
+  const int first = wave * per, mine = min(max(chunks - first, 0), per);   // the wave's chunks
+  // row of W of a block's row i; columns past the matrix repeat its last and are not stored
+  auto matrix_row = [&](int b, int i) {
+    const int col = c0 + (GATE ? (RB == 1 ? i & 7 : 16 * (b >> 1) + i) : 16 * b + i);
+    return min(col, cols - 1) + (GATE ? (RB == 1 ? i >> 3 : b & 1) * cols : 0);
+  };
+
+  // Scales: dword d of row i holds blocks 4 d .. 4 d + 3, those past K as 0 (2^-127).
+  const int scales = a.n * groups;
+  const __amdgpu_buffer_rsrc_t ss =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.scales), (short)0, scales, kRsrcWord3);
+  constexpr int kLine = SPLIT * kWave / 16, kTurns = GROUPS / 4 / kLine;   // thread -> row, and every kLine-th dword of it
+  uint32_t sv[RB][kTurns];
+  const int srow = threadIdx.x / kLine, sd = threadIdx.x % kLine;
+  auto scale_at = [&](int b, int j) { return matrix_row(b, srow) * groups + 4 * (sd + kLine * j); };
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
+  for (int j = 0; j < kTurns; ++j)
+    if (kLine * j < chunks) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) acc[b][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int units = (groups + 7) / 8;
-  for (int u = wave; u < units; u += kSplit) {
+      for (int b = 0; b < RB; ++b)   // the matrix may end inside a dword: its last four bytes then
+        sv[b][j] = __builtin_amdgcn_raw_buffer_load_b32(ss, min(scale_at(b, j), scales - 4), 0, 0);
+    }
+
+  // Copies of x: lane -> row 4 t + lane / 16 and a piece of it. Rows past the
+  // matrix read as zeros, and so does what is past K.
+  const int mrows = min(16 * MT, a.m - m0);
+  const uint16_t* const xbase = a.x + (size_t)m0 * a.ldx;
+  const int xrange = (int)(((mrows - 1) * a.ldx + a.k) * 2);
+  auto xpiece = [&](int t) { return r ^ (2 * ((4 * t + q) & 7)); };
+  uint32_t xoff[COPIES];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int g = 8 * u + 2 * q + h;
-      const bool in = g < groups;
-      u32x4_t w[NB];
-      float s[NB];
+  for (int t = 0; t < COPIES; ++t)
+    xoff[t] = 4 * t + q < mrows ? (uint32_t)((4 * t + q) * a.ldx * 2) + 16 * xpiece(t) : kPastEnd;
+  uint8_t* const ring = smem + wave * DEPTH * kPlace;
+  // W's copies: lane -> row lane / 4, piece lane % 4 in its place. With a gate, w1
+  // and w3 have a resource each, but one reaches both with RB 1 (2^31 bytes at most).
+  const uint32_t pitch = (uint32_t)groups * 16;
+  constexpr int kHalves = GATE && RB > 1 ? 2 : 1;
+  const int wpiece = (lane & 3) ^ (2 * (lane >> 5));
+  uint32_t woff[RB];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const size_t at = (size_t)(n + b * cols) * groups + g;
-        w[b] = in ? *reinterpret_cast<const u32x4_t*>(a.codes + at * 16) : u32x4_t{0, 0, 0, 0};
-        s[b] = e8m0_to_f32(in ? a.scales[at] : 127);
-      }
+  for (int b = 0; b < RB; ++b)
+    woff[b] = (uint32_t)(matrix_row(b, lane >> 2) - matrix_row(b % kHalves, 0)) * pitch + 16 * wpiece;
+  auto issue = [&](auto whole, int d, int c) {   // chunk c into place d; one that K ends in or before is not whole
+    uint8_t* const to = ring + d * kPlace;
+    const int c_ = whole ? c : 0;   // else offsets count from the rows' start
+    __amdgpu_buffer_rsrc_t ws[kHalves];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        bf16x8_t x[MT];
+    for (int h = 0; h < kHalves; ++h)
+      ws[h] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.codes) + (size_t)matrix_row(h, 0) * pitch + 64 * c_,
+                                                (short)0, 0x7FFFFFFF, kRsrcWord3);
+    const __amdgpu_buffer_rsrc_t xs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(xbase) + 128 * c_, (short)0,
+                                                                        xrange - 256 * c_, kRsrcWord3);
+    auto copy_w = [&](int b, uint32_t at) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ws[b % kHalves], (lds_void_t*)(to + kXBytes + b * 1024), 16, at, 0, 0, 0);
+    };
+    auto copy_x = [&](int t, uint32_t at) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(xs, (lds_void_t*)(to + t * 1024), 16, at, 0, 0, 0);
+    };
+    if constexpr (whole) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          const int m = m0 + 16 * i + r;
-          x[i] = bf16x8_t{};
-          if (in && m < a.m) x[i] = *reinterpret_cast<const bf16x8_t*>(a.x + (size_t)m * a.ldx + 32 * g + 8 * j);
-        }
+      for (int b = 0; b < RB; ++b) copy_w(b, woff[b]);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const bf16x8_t v = dequant8(w[b][j], s[b]);
+      for (int t = 0; t < COPIES; ++t) copy_x(t, xoff[t]);
+    } else {   // a block past K repeats the last one (its scale is 0)
 #pragma unroll
-          for (int i = 0; i < MT; ++i) acc[b][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, x[i], acc[b][i], 0, 0, 0);
-        }
+      for (int b = 0; b < RB; ++b) copy_w(b, woff[b] + 16 * (min(4 * c + wpiece, groups - 1) - wpiece));
+#pragma unroll
+      for (int t = 0; t < COPIES; ++t) copy_x(t, 128 * c + 8 * xpiece(t) < a.k ? xoff[t] + 256 * c : kPastEnd);
+    }
+  };
+  constexpr int kEach = RB + COPIES;   // copies of a chunk
+  static_assert((DEPTH - 1) * kEach < 64, "vmcnt counts them");
+  // chunks past the wave's last are copied too (from the last one's lines): the waits below count on it
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d) issue(std::false_type{}, d, first + d);   // (no branch: the scales' wait counts them)
+#pragma unroll
+  for (int j = 0; j < kTurns; ++j)
+    if (kLine * j < chunks) {
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+        const int at = scale_at(b, j), d = sd + kLine * j, live = groups - 4 * d;
+        const uint32_t v = sv[b][j] >> (8 * (at - min(at, scales - 4)) & 31);
+        if (d < chunks) scale[(16 * b + srow) * chunks + d] = live >= 4 ? v : v & ((1u << (8 * live)) - 1);
       }
     }
+  __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (3 << 14));   // lgkmcnt 0: this wave's scales are in LDS
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+
+  f32x4_t acc[RB][MT];
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[b][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int xr = COPIES < 4 ? r & (4 * COPIES - 1) : r;   // rows that are not staged repeat others and are not stored
+  int d = 0;   // place of chunk i
+  for (int i = 0; i < mine; ++i) {
+    MOE_WAIT_VM((DEPTH - 1) * kEach);   // the chunk has landed; those after it may be in flight
+    asm volatile("" ::: "memory");
+    const uint8_t* const at = ring + d * kPlace;
+    u32x4_t w[RB];
+    uint32_t sc[RB];
+    bf16x8_t x[MT][4];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      w[b] = *reinterpret_cast<const u32x4_t*>(at + kXBytes + b * 1024 + r * 64 + (q ^ (2 * (r >> 3))) * 16);
+      sc[b] = scale[(16 * b + r) * chunks + first + i];
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        x[t][j] = *reinterpret_cast<const bf16x8_t*>(at + t * 4096 + xr * 256 + ((4 * j + q) ^ (2 * (xr & 7))) * 16);
+    __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (3 << 14));   // lgkmcnt 0: the place has been read
+    asm volatile("" ::: "memory");
+    const int c = first + i + DEPTH;
+    if (4 * c + 4 <= groups) issue(std::true_type{}, d, c);
+    else issue(std::false_type{}, d, c);
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      transpose_quarters(w[b]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bf16x8_t v = dequant8(w[b][j], scale_byte(sc[b], j));
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, x[t][j], acc[b][t], 0, 0, 0);
+      }
+    }
+    d = d + 1 == DEPTH ? 0 : d + 1;
   }
+  MOE_WAIT_VM(0);    // the copies past the end still write LDS
+  __syncthreads();   // every wave is done with its ring
+  f32x4_t* const part = reinterpret_cast<f32x4_t*>(smem);
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
+  for (int b = 0; b < RB; ++b)
 #pragma unroll
-    for (int i = 0; i < MT; ++i) part[wave][b][i][lane] = acc[b][i];
+    for (int i = 0; i < MT; ++i) part[((wave * RB + b) * MT + i) * kWave + lane] = acc[b][i];
   __syncthreads();
-  if (wave >= MT) return;   // wave i adds and stores row block i
-  f32x4_t v[NB];
+  auto sum = [&](int b, int i) {
+    f32x4_t v = part[(b * MT + i) * kWave + lane];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    v[b] = part[0][b][wave][lane];
+    for (int w = 1; w < SPLIT; ++w) v += part[((w * RB + b) * MT + i) * kWave + lane];
+    return v;
+  };
+  // a wave adds and stores a 16 x 16 block, with a gate a pair of them
+  constexpr int kPairs = GATE && RB > 1 ? RB / 2 : RB;
+  for (int task = wave; task < MT * kPairs; task += SPLIT) {
+    const int i = task / kPairs, b = task % kPairs, m = 16 * i + r;
+    f32x4_t v;
+    if constexpr (GATE) {
+      f32x4_t u;
+      if constexpr (RB > 1) {
+        v = sum(2 * b, i);
+        u = sum(2 * b + 1, i);
+      } else {
+        v = sum(0, i);
 #pragma unroll
-    for (int w = 1; w < kSplit; ++w) v[b] += part[w][b][wave][lane];
+        for (int e = 0; e < 4; ++e) u[e] = __shfl_xor(v[e], 32, kWave);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = gated(v[e], u[e]);
+      if (RB == 1 && q >= 2) continue;   // the lanes of w3
+    } else {
+      v = sum(b, i);
+    }
+    const int c = c0 + 16 * b + 4 * q;
+    if (m >= mrows || c >= cols) continue;
+    const size_t at = (size_t)(m0 + m) * cols + c;
+    if (cols % 4 == 0) {
+      if (f32) *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + at) = v;
+      else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+      continue;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (c + e >= cols) break;
+      if (f32) static_cast<float*>(a.out)[at + e] = v[e];
+      else static_cast<uint16_t*>(a.out)[at + e] = f32_to_bf16_rne(v[e]);
+    }
   }
-  const int m = m0 + 16 * wave + r, c = n0 + 4 * q;
-  if (m >= a.m) return;
-  const size_t at = (size_t)m * cols + c;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (c + e >= cols) break;
-    const float f = GATE ? gated(v[0][e], v[NB - 1][e]) : v[0][e];
-    if (F32) static_cast<float*>(a.out)[at + e] = f;
-    else static_cast<uint16_t*>(a.out)[at + e] = f32_to_bf16_rne(f);
-  }
+}
+
+template <int MT, int RB, int SPLIT, int DEPTH, int COPIES, int GROUPS, bool GATE>
+__global__ __launch_bounds__(SPLIT* kWave) void linear_rows(LinearArgs a, bool f32) {
+  constexpr int kParts = SPLIT * RB * MT * 1024;   // the waves' sums, in the ring's memory after it
+  constexpr int kRing = SPLIT * DEPTH * (COPIES + RB) * 1024;
+  // One array: the compiler lets reads of a ring wait for every copy in flight
+  // (vmcnt(0)) once there are two.
+  constexpr int kMost = kRing > kParts ? kRing : kParts;
+  __shared__ __align__(1024) uint8_t smem[kMost + RB * 16 * GROUPS];
+  linear_rows_block<MT, RB, SPLIT, DEPTH, COPIES, GROUPS, GATE>(smem, reinterpret_cast<uint32_t*>(smem + kMost), a, f32);
+}
+
+template <int MT, int RB, int SPLIT, int DEPTH, int COPIES, int GROUPS>
+hipError_t launch_rows(const LinearArgs& a, bool gate, bool f32, hipStream_t stream) {
+  const int cols = gate ? a.n / 2 : a.n, wide = (gate ? 8 : 16) * RB;
+  const dim3 grid((cols + wide - 1) / wide, (a.m + 16 * MT - 1) / (16 * MT)), block(SPLIT * kWave);
+  if (gate) hipLaunchKernelGGL((linear_rows<MT, RB, SPLIT, DEPTH, COPIES, GROUPS, true>), grid, block, 0, stream, a, f32);
+  else hipLaunchKernelGGL((linear_rows<MT, RB, SPLIT, DEPTH, COPIES, GROUPS, false>), grid, block, 0, stream, a, f32);
+  return hipGetLastError();
 }
 
 // ---- many rows: BM x BN tiles, operands staged through LDS.
 //
-// A stage is 64 K. x comes as it lies, 128 bytes a row, into a ring of three
+// A stage is 64 K. x comes as it lies, 128 bytes a row, into a ring of
 // stages; W comes as packed codes, 128 K at a time (a unit, 64 bytes a row),
-// into a ring of three units: both by buffer_load ... lds copies of 1 KB a wave
+// into a ring of units: both by buffer_load ... lds copies of 1 KB a wave
 // instruction, past an edge as zeros. A wave turns the codes of its columns
 // into bf16 fragments in registers on the scaled converter, so a staged weight
 // costs a quarter of a bf16 one's LDS traffic, and x, which every weight row
@@ -117,31 +290,27 @@ __global__ __launch_bounds__(kSplit* kWave) void linear_rows(LinearArgs a) {
 // cover all eight places.
 //   W rows are 64 bytes: chunk ^ (row >> 2 & 3) puts the rows four apart, which
 // share banks, into different places.
-//   Scales, a byte per row and block, go straight to registers, four a unit.
+//   Scales, a byte per row and block, go straight to registers, four a unit and row.
 //   With a gate the tile's 16-row blocks of W alternate between w1 and w3, so
 // that a lane holds both values of an output.
-typedef __attribute__((address_space(3))) void lds_void_t;
-typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
-
-constexpr uint32_t kPastEnd = 0x80000000u;   // beyond every buffer resource below
-constexpr int kMaxRange = 0x7FFFFFFF;
-
-// vmcnt <= n and lgkmcnt 0
-#define MOE_WAIT_VM(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (7 << 4) | ((((n) >> 4) & 3) << 14))
-
 __device__ __forceinline__ int swz_x(int c, int r) { return c ^ (((r >> 1) & 1) | ((r >> 1) & 4)); }
 __device__ __forceinline__ int swz_w(int c, int r) { return c ^ ((r >> 2) & 3); }
 
-template <int BM_, int BN_, int WM_, int WN_, int PER_CU_>
+// NX stages in x's ring (odd), NW units in W's.
+template <int BM_, int BN_, int WM_, int WN_, int PER_CU_, int NX_, int NW_>
 struct LinearShape {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, kWaves = WM * WN, kPerCU = PER_CU_;
-  static constexpr bool kAlone = kWaves * kPerCU == 4;    // a wave has its SIMD, and 512 registers, to itself
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, kWaves = WM * WN, kPerCU = PER_CU_, NX = NX_, NW = NW_;
   static constexpr int MI = BM / WM / 16, NJ = BN / WN / 16;
   static constexpr int kXBytes = BM * 128, kWBytes = BN * 64;
-  static constexpr int kX = BM / 8 / kWaves, kW = BN / 16 / kWaves;   // copies per wave: a stage's x, a unit's W
-  static constexpr int kSmem = 3 * (kXBytes + kWBytes);
+  static constexpr int kX = BM / 8 / kWaves, kW = BN / 16 / kWaves, kWh = kW / 2;   // copies per wave: a stage's x, a unit's W
+  static constexpr int kSmem = NX * kXBytes + NW * kWBytes;
+  // copies and scale loads that a wave issues after a stage's x and before that stage starts
+  static constexpr int kSc = (NJ + 3) / 4;   // loads of a unit's scales
+  static constexpr int kAfter = kWh + (NX - 2) * (kX + kWh) + kSc * (NX - 1) / 2;
   static_assert(kX * kWaves * 8 == BM && kW * kWaves * 16 == BN && kW % 2 == 0 && kWaves % 2 == 0, "even split");
   static_assert(kPerCU * kSmem <= 160 * 1024 && MI % 2 == 0 && NJ % 2 == 0, "rings fit");
+  static_assert(4 * (kX - 1) < 3 * (kX + kWh), "a stage's x before its scales");
+  static_assert(NX % 2 == 1 && 2 * NW >= NX + 2 && kAfter < 64, "W lands before x of its stage; vmcnt counts them");
 };
 
 template <class C, bool GATE, bool F32>
@@ -163,7 +332,7 @@ __device__ __forceinline__ void linear_tile(uint8_t* smem, const LinearArgs& a, 
   const uint32_t pitch = (uint32_t)groups * 16;   // bytes of a row's codes
   const int units = (groups + 3) / 4;
 
-  uint8_t* const ring_w = smem + 3 * C::kXBytes;
+  uint8_t* const ring_w = smem + C::NX * C::kXBytes;
   // Copies: lane -> (row, place in the row); the permutation repeats every 16
   // rows, so a lane has one offset for all its copies, whose resources start
   // at their own rows (offsets of each copy's own would be spilled) and end
@@ -193,30 +362,35 @@ __device__ __forceinline__ void linear_tile(uint8_t* smem, const LinearArgs& a, 
   };
 
   const int wm = wave / C::WN, wn = wave % C::WN, rl = lane & 15, q = lane >> 4;
-  // Scales: the four bytes of a unit's blocks of each of the wave's 16-row
-  // blocks. A last unit that is not whole takes the row's last four bytes,
-  // moved down; what follows is 0, so that codes past K are finite whatever they
-  // are (x is zero there).
-  uint32_t sc[C::NJ], next[C::NJ];
-  __amdgpu_buffer_rsrc_t srsrc[GATE ? 2 : 1];   // rows past the matrix read as 0
+  // Scales: a lane loads the four bytes of a unit's blocks of one row, of the
+  // wave's 16-row block lane / 16 (and 4 more, ..), and the lanes that multiply
+  // that row take them from it. (A lane that loads its own rows' makes every
+  // load touch sixteen lines four times over, 64 clocks: 128 x 128 tiles of 128 rows 65 -> 60 us.) The
+  // matrix's last four bytes may start before the unit's and are moved down;
+  // past K they are 0, so that codes there are finite whatever they are (x is 0).
+  constexpr int kSc = C::kSc;
+  const int scales = a.n * groups, last = max(scales - 4, 0);
+  const __amdgpu_buffer_rsrc_t srsrc =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.scales), (short)0, scales, kRsrcWord3);
+  int srow[kSc];   // offset of the lane's rows; rows past the matrix repeat its last
 #pragma unroll
-  for (int h = 0; h < (GATE ? 2 : 1); ++h)
-    srsrc[h] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.scales) + (size_t)(c0 + h * cols) * groups, (short)0,
-                                                 ncols * groups, kRsrcWord3);
-  const uint32_t srow = rl * groups;
-  auto scale_at = [&](int j, int g) {   // byte g of block j's rows
-    const int b = wn * C::NJ + j;
-    return srow + (uint32_t)(16 * (GATE ? b >> 1 : b) * groups + g);
-  };
-  auto load_scale = [&](int j, int u) {
-    next[j] = __builtin_amdgcn_raw_buffer_load_b32(srsrc[GATE ? j & 1 : 0], scale_at(j, max(min(4 * u, groups - 4), 0)), 0, 0);
+  for (int i = 0; i < kSc; ++i) {
+    const int b = wn * C::NJ + min(4 * i + q, C::NJ - 1);
+    srow[i] = (min(c0 + 16 * (GATE ? b >> 1 : b) + rl, cols - 1) + (GATE && (b & 1) ? cols : 0)) * groups;
+  }
+  uint32_t sc[C::NJ], next[kSc];
+  auto load_scale = [&](int i, int u) {
+    next[i] = __builtin_amdgcn_raw_buffer_load_b32(srsrc, min(srow[i] + 4 * u, last), 0, 0);
   };
   // the byte of lane quarter q's block of the unit's first stage in bits 7:0, of the second in 23:16
   auto take_scales = [&](int u) {
-    const int past = groups >= 4 ? 8 * max(4 * u + 4 - groups, 0) : 0;
-    const uint32_t by = (uint32_t)min(past, 31) + 8 * (q >> 1);
+    const int live = groups - 4 * u;
+    const uint32_t mask = live >= 4 ? ~0u : (1u << (8 * live)) - 1;
 #pragma unroll
-    for (int j = 0; j < C::NJ; ++j) sc[j] = (uint32_t)((unsigned long long)next[j] >> by);
+    for (int i = 0; i < kSc; ++i) next[i] = next[i] >> (8 * max(srow[i] + 4 * u - last, 0) & 31) & mask;
+#pragma unroll
+    for (int j = 0; j < C::NJ; ++j)
+      sc[j] = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (16 * (j % 4) + rl), (int)next[j / 4]) >> (8 * (q >> 1));
   };
 
   f32x4_t acc[C::MI][C::NJ];
@@ -225,31 +399,37 @@ __device__ __forceinline__ void linear_tile(uint8_t* smem, const LinearArgs& a, 
 #pragma unroll
     for (int j = 0; j < C::NJ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  // The rings' fill, in the order that a stage's wait counts on: unit 1's W and
-  // the scales as if stages before the first had issued them.
-  constexpr int kHalf = C::MI / 2, kM = kHalf * C::NJ, kWh = C::kW / 2, kG = C::kX + kWh;
+  // The rings' fill, in the order that a stage's wait counts on, as if stages
+  // 1 - NX .. -1 had issued it (but for the scales of units before the first:
+  // as many copies of the first W once more).
+  constexpr int kHalf = C::MI / 2, kM = kHalf * C::NJ, kWh = C::kWh, kG = C::kX + kWh;
+  constexpr int kUnits = (C::NX - 1) / 2;   // those stages' units
+  unrolled<C::NW - 1 - kUnits>([&](auto u) {
 #pragma unroll
-  for (int j = 0; j < C::kW; ++j) issue_w(ring_w, 0, j);
+    for (int j = 0; j < C::kW; ++j) issue_w(ring_w + u * C::kWBytes, u, j);
+  });
+  unrolled<C::NX - 1>([&](auto vc) {
+    constexpr int v = decltype(vc)::value, u = C::NW - 1 - kUnits + v / 2;
 #pragma unroll
-  for (int j = 0; j < C::kX; ++j) issue_x(smem, 0, j);
+    for (int j = 0; j < C::kX; ++j) issue_x(smem + v * C::kXBytes, v, j);
 #pragma unroll
-  for (int j = 0; j < kWh; ++j) issue_w(ring_w + C::kWBytes, 1, j);
-  __builtin_amdgcn_sched_barrier(0);
+    for (int j = 0; j < kWh; ++j) issue_w(ring_w + u * C::kWBytes, u, v % 2 * kWh + j);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (v % 2 == 0 && v < C::NX - 3) {
 #pragma unroll
-  for (int j = 0; j < C::NJ; ++j) {
-    if (groups >= 4) {
-      load_scale(j, 0);
-    } else {   // K below 128: one unit, byte by byte
-      next[j] = 0;
-      for (int g = 0; g < groups; ++g)
-        next[j] |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(srsrc[GATE ? j & 1 : 0], scale_at(j, g), 0, 0) << (8 * g);
+      for (int j = 0; j < kSc; ++j) issue_w(ring_w, 0, 0);
+    } else if constexpr (v == C::NX - 3) {
+#pragma unroll
+      for (int j = 0; j < kSc; ++j) load_scale(j, 0);
+      if (scales < 4) {   // one unit, byte by byte
+        uint32_t v = 0;
+        for (int g = 0; g < scales; ++g) v |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(srsrc, g, 0, 0) << (8 * g);
+#pragma unroll
+        for (int j = 0; j < kSc; ++j) next[j] = v;
+      }
     }
-  }
-  __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-  for (int j = 0; j < C::kX; ++j) issue_x(smem + C::kXBytes, 1, j);
-#pragma unroll
-  for (int j = kWh; j < C::kW; ++j) issue_w(ring_w + C::kWBytes, 1, j);
+    __builtin_amdgcn_sched_barrier(0);
+  });
 
   // A stage is four lists of MFMAs: steps 0 and 1, the wave's upper and lower
   // row blocks. Behind each MFMA stands a share of the LDS reads and
@@ -268,26 +448,23 @@ __device__ __forceinline__ void linear_tile(uint8_t* smem, const LinearArgs& a, 
   auto keep = [&] {
     unrolled<C::MI * C::NJ>([&](auto mc) {
       f32x4_t& v = acc[decltype(mc)::value / C::NJ][decltype(mc)::value % C::NJ];
-      if constexpr (C::kAlone) pin_agpr(v);
-      else pin(v[0]);
+      pin(v[0]);
     });
   };
-  if constexpr (C::kAlone) keep();
   int ix = 0, iw = 0;   // the ring places of stage s and unit u
   auto run_stage = [&](auto pc, int u) {   // stage p of unit u
     constexpr int p = decltype(pc)::value;
     const int s = 2 * u + p;
     // This wave's copies of the stage have landed and its LDS reads are done;
-    // the barrier extends both to every wave. After the stage's x copies it has
-    // issued the W copies beside them, a stage's copies and a unit's scales.
-    MOE_WAIT_VM(2 * kWh + C::kX + C::NJ);
+    // the barrier extends both to every wave.
+    MOE_WAIT_VM(C::kAfter);
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     const uint8_t* const bx = smem + ix * C::kXBytes;
     const uint8_t* const bw = ring_w + iw * C::kWBytes;
-    uint8_t* const to_x = smem + (ix ? ix - 1 : 2) * C::kXBytes;
-    uint8_t* const to_w = ring_w + (iw ? iw - 1 : 2) * C::kWBytes;
+    uint8_t* const to_x = smem + (ix ? ix - 1 : C::NX - 1) * C::kXBytes;
+    uint8_t* const to_w = ring_w + (iw ? iw - 1 : C::NW - 1) * C::kWBytes;
     asm volatile("" : "+v"(xat), "+v"(wat));   // derived anew in each stage: held over the loop, they would be spilled
     auto read_x = [&](auto ic, auto jc) {
       constexpr int i = decltype(ic)::value, j = decltype(jc)::value;
@@ -299,7 +476,7 @@ __device__ __forceinline__ void linear_tile(uint8_t* smem, const LinearArgs& a, 
     };
     auto convert = [&](auto jc, auto step) {
       constexpr int j = decltype(jc)::value, k = decltype(step)::value;
-      fw[k][j] = dequant8(raw[j][k], e8m0_to_f32((p ? sc[j] >> 16 : sc[j]) & 0xFFu));
+      fw[k][j] = dequant8(raw[j][k], scale_byte(sc[j], 2 * p));
     };
     unrolled<4>([&](auto hc) {
       constexpr int h = decltype(hc)::value;
@@ -308,7 +485,6 @@ __device__ __forceinline__ void linear_tile(uint8_t* smem, const LinearArgs& a, 
       unrolled<kM>([&](auto mc) {
         constexpr int m = decltype(mc)::value, i = lo * kHalf + m / C::NJ, j = m % C::NJ;
         acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[step][j], fx[i], acc[i][j], 0, 0, 0);
-        if constexpr (C::kAlone) pin_agpr(acc[i][j]);
         // reads of the next list's x blocks; W's at the stage's start
         if constexpr (h == 0) {
           unrolled<C::NJ>([&](auto b) { if constexpr (b * (kM / 4) / C::NJ == m) read_w(b); });
@@ -334,19 +510,19 @@ __device__ __forceinline__ void linear_tile(uint8_t* smem, const LinearArgs& a, 
         unrolled<kG>([&](auto cc) {
           constexpr int c = decltype(cc)::value;
           if constexpr (c * 4 * kM / kG == h * kM + m) {
-            if constexpr (c < C::kX) issue_x(to_x, s + 2, c);
-            else issue_w(to_w, u + 2, p * kWh + c - C::kX);
+            if constexpr (c < C::kX) issue_x(to_x, s + C::NX - 1, c);
+            else issue_w(to_w, u + C::NW - 1, p * kWh + c - C::kX);
           }
         });
         if constexpr (p == 0 && h == 3) {
-          unrolled<C::NJ>([&](auto b) { if constexpr (b * kM / C::NJ == m) load_scale(b, u + 1); });
+          unrolled<kSc>([&](auto b) { if constexpr (b * kM / kSc == m) load_scale(b, u + 1); });
         }
         __builtin_amdgcn_sched_barrier(0);
       });
     });
     keep();
-    ix = ix == 2 ? 0 : ix + 1;
-    if constexpr (p == 1) iw = iw == 2 ? 0 : iw + 1;
+    ix = ix == C::NX - 1 ? 0 : ix + 1;
+    if constexpr (p == 1) iw = iw == C::NW - 1 ? 0 : iw + 1;
   };
   for (int u = 0; u < units; ++u) {
     run_stage(std::integral_constant<int, 0>{}, u);
@@ -437,30 +613,53 @@ hipError_t launch_tiles(const LinearArgs& a, bool gate, bool f32, hipStream_t st
   return hipGetLastError();
 }
 
-using Linear256 = LinearShape<256, 256, 2, 4, 1>;
-using Linear128 = LinearShape<128, 128, 2, 2, 2>;
-
-template <int MT>
-hipError_t launch_rows(const LinearArgs& a, bool gate, bool f32, hipStream_t stream) {
-  const int cols = gate ? a.n / 2 : a.n;
-  const dim3 grid((cols + 15) / 16, (a.m + 16 * MT - 1) / (16 * MT)), block(kSplit * kWave);
-  if (gate && f32) hipLaunchKernelGGL((linear_rows<MT, true, true>), grid, block, 0, stream, a);
-  else if (gate) hipLaunchKernelGGL((linear_rows<MT, true, false>), grid, block, 0, stream, a);
-  else if (f32) hipLaunchKernelGGL((linear_rows<MT, false, true>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((linear_rows<MT, false, false>), grid, block, 0, stream, a);
-  return hipGetLastError();
-}
+using Linear256 = LinearShape<256, 256, 2, 4, 1, 3, 3>;
+using Linear128 = LinearShape<128, 128, 2, 2, 2, 3, 3>;
 
 }  // namespace
 
 hipError_t launch_mxfp4_linear(const LinearArgs& a, bool gate, bool f32, hipStream_t stream) {
-  if (a.m > 64) {
-    if ((long long)((a.m + 255) / 256) * ((a.n + 255) / 256) >= 192) return launch_tiles<Linear256>(a, gate, f32, stream);
-    return launch_tiles<Linear128>(a, gate, f32, stream);
+  const int groups = a.k / 32;
+  const long long mb = (a.m + 15) / 16, blocks = mb * ((a.n + 15) / 16);   // 16 x 16 outputs, gated ones counted twice
+  // The streaming kernel reads scales four at a time and reaches both halves
+  // of a gated matrix with 32-bit offsets; its rows of W hold up to 512 scales
+  // (2048 in the form for up to 16 rows).
+  const bool streams = (long long)a.n * groups >= 4 && (!gate || (long long)(a.n / 2) * groups * 16 < (1ll << 31));
+  // Up to 4096 blocks it beats the 128 x 128 tiles, over a long K up to 8192 (K 7168
+  // to 4096 columns: 512 rows, 8192 blocks, 43 against 60 us, 1024 rows 81 against
+  // 61; K 2048 to 7168: 128 rows, 3584 blocks, 11.8 against 19.7, 256 rows 20.3
+  // against 19.7; K 512 to 1024: 2048 rows, 8192 blocks, 11.0 against 7.8).
+  if (streams && blocks <= (a.k > 4096 ? 8192 : 4096) && (groups <= 512 || a.m <= 16)) {
+    if (groups > 512) return launch_rows<1, 1, 8, 3, 4, 2048>(a, gate, f32, stream);
+    // up to four rows one copy of x a chunk, and room for a second chunk (one row, K 7168
+    // to 4096 columns: 6.3 us, with four copies and one chunk 7.4)
+    if (a.m <= 4) return launch_rows<1, 1, 8, 2, 1, 512>(a, gate, f32, stream);
+    // The smallest share of a workgroup that keeps the workgroups to one a CU or
+    // two: less of W or x is loaded twice with a larger one, and more CUs work with
+    // a smaller. us for shares of 1 x 1, 1 x 2, 2 x 2, 2 x 4, 4 x 4 blocks of x and W
+    // (in each row the one taken is the fastest measured):
+    //   K 7168 to 4096   16 rows (256 blocks)    8.8 10.4 12.5 17.7 21.6
+    //                    32 rows (512)          12.7 10.2 13.9 18.7 22.9
+    //                    37 rows (768)          15.3 13.3 11.0 16.1 23.6
+    //                    128 rows (2048)        32.1 23.7 21.9 17.0 23.7
+    //                    256 rows (4096)        58.8 41.6 39.4 29.0 23.5
+    //   K 2048 to 7168   16 rows (448)           5.9  4.9  5.6  7.4 10.8
+    //                    32 rows (896)           8.2  6.8  6.2  7.7 11.2
+    //                    37 rows (1344)         10.0  8.7  9.3  7.7 11.4
+    //                    128 rows (3584)        20.5 16.3 17.0 13.0 11.8
+    // One block of rows is not spread over two: 1 x 4 from 513 blocks.
+    if (blocks <= 256) return launch_rows<1, 1, 8, 1, 4, 512>(a, gate, f32, stream);
+    if (blocks <= 512) return launch_rows<1, 2, 8, 1, 4, 512>(a, gate, f32, stream);
+    if (mb == 1) return launch_rows<1, 4, 8, 1, 4, 512>(a, gate, f32, stream);
+    if (blocks <= 1024) return launch_rows<2, 2, 8, 1, 8, 512>(a, gate, f32, stream);
+    if (blocks <= 2048 || mb == 2) return launch_rows<2, 4, 8, 1, 8, 512>(a, gate, f32, stream);
+    return launch_rows<4, 4, 4, 1, 16, 512>(a, gate, f32, stream);
   }
-  if (a.m <= 16) return launch_rows<1>(a, gate, f32, stream);
-  if (a.m <= 32) return launch_rows<2>(a, gate, f32, stream);
-  return launch_rows<4>(a, gate, f32, stream);
+  // 256 x 256 tiles once they fill most of the CUs (K 7168 to 4096 columns: 2048
+  // rows, 128 of them, 140 against 106 us; K 2048 to 7168: 2048 rows, 224 of them,
+  // 49 against 59).
+  if ((long long)((a.m + 255) / 256) * ((a.n + 255) / 256) >= 192) return launch_tiles<Linear256>(a, gate, f32, stream);
+  return launch_tiles<Linear128>(a, gate, f32, stream);
 }
 
 }  // namespace moe

@@ -323,7 +323,11 @@ def rounded(v, dtype):
 LINEAR_SIZES = [(1, 1, 32), (1, 16, 64), (2, 17, 96), (16, 16, 128), (17, 33, 160), (1, 4096, 1024), (5, 100, 2048),
                 (33, 257, 288), (64, 64, 512), (65, 130, 544), (128, 128, 256), (130, 250, 1056), (256, 256, 768),
                 (257, 511, 800), (300, 1000, 2048), (513, 264, 4096), (700, 300, 96), (1, 129, 4128), (37, 384, 1376),
-                (3, 7168, 2048), (1, 300, 65536), (2000, 1201, 352), (4097, 40, 64)]
+                (3, 7168, 2048), (1, 300, 65536), (2000, 1201, 352), (4097, 40, 64),
+                # fewer than four scales in all, and rows of x and W that end inside every kind of workgroup
+                (3, 1, 96), (70, 3, 32), (5, 2, 32), (4, 4090, 160), (5, 70, 224), (16, 5001, 544), (13, 9001, 416),
+                (33, 4090, 160), (50, 7100, 672), (100, 8100, 96), (4, 130, 20000), (9, 66, 20000), (40, 66, 20000),
+                (2049, 6100, 96), (1111, 5002, 160)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -340,7 +344,9 @@ def test_linear_is_exact_on_integers(m, n, k, dtype):
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("m,n,k", [(1, 32, 64), (1, 256, 7168), (7, 130, 2048), (16, 34, 96), (37, 200, 1024), (70, 514, 288),
-                                   (300, 258, 640), (1030, 80, 512), (2050, 1154, 160), (4, 2, 32)])
+                                   (300, 258, 640), (1030, 80, 512), (2050, 1154, 160), (4, 2, 32),
+                                   (2, 2, 32), (3, 4106, 352), (11, 1030, 224), (16, 5010, 544), (9, 9002, 96), (31, 4118, 96),
+                                   (50, 7102, 160), (100, 8110, 96), (2100, 6014, 96), (6, 26, 20000)])
 @pytest.mark.parametrize("gate", [False, True])
 def test_linear_of_real_values(m, n, k, gate, dtype):
     rng = np.random.default_rng(m * n + k)
@@ -405,7 +411,7 @@ def test_linear_rows_of_a_wider_matrix(m):
 
 
 @pytest.mark.parametrize("gate", [False, True])
-@pytest.mark.parametrize("m", [1, 3, 16, 17, 40, 100, 300, 1100])
+@pytest.mark.parametrize("m", [1, 3, 16, 17, 40, 100, 300, 1100, 9000])
 def test_linear_row_does_not_depend_on_other_rows_values(m, gate):
     """NaN and infinite rows next to it change no row's bits."""
     rng = np.random.default_rng(m)
