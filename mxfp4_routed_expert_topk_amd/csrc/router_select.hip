@@ -43,107 +43,129 @@ __device__ __forceinline__ V wave_reduce(V v, F f) {
   for (int off = kWave / 2; off > 0; off >>= 1) v = f(v, (V)__shfl_xor(v, off, kWave));
   return v;
 }
-template <class V> __device__ __forceinline__ V wave_sum(V v) { return wave_reduce(v, [](V a, V b) { return a + b; }); }
-template <class V> __device__ __forceinline__ V wave_max(V v) { return wave_reduce(v, [](V a, V b) { return a > b ? a : b; }); }
+
+// Reductions of 32-bit values on DPP moves (6 instructions, no LDS); the result
+// is uniform. A lane without a source gets `none`.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp(uint32_t none, uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, CTRL, ROWS, 0xF, false);
+}
+template <class F>
+__device__ __forceinline__ uint32_t reduce32(uint32_t v, uint32_t none, F f) {
+  v = f(v, dpp<0x111, 0xF>(none, v));   // row_shr 1, 2, 4, 8: lane 15 of each row of 16 has its row's
+  v = f(v, dpp<0x112, 0xF>(none, v));
+  v = f(v, dpp<0x114, 0xF>(none, v));
+  v = f(v, dpp<0x118, 0xF>(none, v));
+  v = f(v, dpp<0x142, 0xA>(none, v));   // row_bcast 15 into rows 1 and 3, 31 into rows 2 and 3
+  v = f(v, dpp<0x143, 0xC>(none, v));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, kWave - 1);
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  return __uint_as_float(reduce32(__float_as_uint(v), 0u, [](uint32_t a, uint32_t b) { return __float_as_uint(__uint_as_float(a) + __uint_as_float(b)); }));
+}
+__device__ __forceinline__ float wave_max(float v) {
+  return __uint_as_float(reduce32(__float_as_uint(v), __float_as_uint(-INFINITY), [](uint32_t a, uint32_t b) { return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b))); }));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) { return reduce32(v, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; }); }
+__device__ __forceinline__ double wave_sum(double v) { return wave_reduce(v, [](double a, double b) { return a + b; }); }
+
+// 2^(x log2 e) on the hardware's exponential: off by (|x| + 2) u of the value
+__device__ __forceinline__ float quick_exp(float x) { return __expf(x); }
 
 __device__ __forceinline__ void wave_lds_order() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
 }
 
-// PER: logits per lane (expert lane + 64 j).  KEY: uint32_t, or with a bias 64 bits.
-template <int PER, bool BIAS>
-__global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectArgs a) {
-  using Key = std::conditional_t<BIAS, unsigned long long, uint32_t>;
-  __shared__ double graded[kTokensPerBlock][PER * kWave];
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  const int t = blockIdx.x * kTokensPerBlock + wave;
-  if (t >= a.rows) return;   // whole waves
-  const int E = a.experts;
-  const bool softmax = a.score == 0, limited = a.groups > a.limit;
-  float l[PER];   // -inf where masked
-  float top = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    const int e = lane + kWave * j;
-    const float v = e < E ? load_logit(a.logits, a.f32, (size_t)t * a.ld + e) : -INFINITY;
-    l[j] = is_masked(v) ? -INFINITY : finite(v);
-    top = fmaxf(top, l[j]);
-  }
-  top = wave_max(top);
-  if (top == -INFINITY) top = 0.f;   // every expert masked
-  float total = 0.f;                 // of exp(l - top)
-  if (softmax && !a.renormalize) {
-#pragma unroll
-    for (int j = 0; j < PER; ++j) total += expf(l[j] - top);
-    total = wave_sum(total);
-  }
+constexpr int kMostCandidates = kWave;
 
-  Key key[PER];   // 0: masked, taken or not there
-  const bool wide = BIAS || (limited && a.group_top == 2);
-  double s[PER];
-  if (wide) {
+// The groups that stay, from each expert's value (-INFINITY: none): bit
+// side * g of the result, `side` lanes a group. gap: what separates the last
+// that stays from the first that does not.
+template <int PER, class V>
+__device__ __forceinline__ unsigned long long open_groups(const SelectArgs& a, const V (&value)[PER], V* graded, int lane,
+                                                          int& side, V& gap) {
+  const int per = a.experts / a.groups;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) graded[lane + kWave * j] = value[j];
+  wave_lds_order();
+  int padded = 1;
+  while (padded < a.groups) padded *= 2;
+  side = kWave / padded;
+  const int g = lane / side;
+  V first = -INFINITY, second = -INFINITY;   // the two largest of the lane's share
+  if (g < a.groups)
+    for (int i = lane % side; i < per; i += side) {
+      const V v = graded[g * per + i];
+      second = max(second, min(first, v));
+      first = max(first, v);
+    }
+  for (int off = 1; off < side; off *= 2) {
+    const V f = __shfl_xor(first, off, kWave), s = __shfl_xor(second, off, kWave);
+    second = max(min(first, f), max(second, s));
+    first = max(first, f);
+  }
+  const V grade = g >= a.groups ? -INFINITY : a.group_top == 2 && second > -INFINITY ? first + second : first;
+  int better = 0;   // groups that rank before this lane's
+  for (int o = 0; o < a.groups; ++o) {
+    const V v = __shfl(grade, o * side, kWave);
+    better += v > grade || (v == grade && o < g);
+  }
+  const unsigned long long open = __ballot(g < a.groups && better < a.limit);
+  const int last = __ffsll((unsigned long long)__ballot(g < a.groups && better == a.limit - 1)) - 1;
+  const int next = __ffsll((unsigned long long)__ballot(g < a.groups && better == a.limit)) - 1;
+  gap = __shfl(grade, last, kWave) - __shfl(grade, next, kWave);
+  return open;
+}
+
+// Whether expert lane + 64 j's group is open.
+__device__ __forceinline__ bool group_open(unsigned long long open, int side, float inverse, int e) {
+  const int of = (int)(((float)e + 0.5f) * inverse);   // e / per, exact below 1024 experts
+  return (open >> (of * side & 63)) & 1;
+}
+
+// The ids of a token's slots, slot r on lane r (-1: none), by k rounds of the
+// best over the wave, every value exact: for rows that the quick way below
+// cannot settle.
+template <int PER, bool BIAS>
+__device__ __forceinline__ int select_by_rounds(const SelectArgs& a, const float (&l)[PER], const float (&b)[PER], float top,
+                                                double* graded, int lane) {
+  using Key = std::conditional_t<BIAS, unsigned long long, uint32_t>;
+  const bool limited = a.groups > a.limit;
+  double v[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) v[j] = (double)l[j];
+  if (BIAS || (limited && a.group_top == 2)) {
     double sum = 0.0;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       const double x = (double)l[j];
-      s[j] = softmax ? exp(x - (double)top) : 1.0 / (1.0 + exp(-x));
-      sum += s[j];
+      v[j] = a.score == 0 ? exp(x - (double)top) : 1.0 / (1.0 + exp(-x));
+      sum += v[j];
     }
     if (BIAS) {
-      const double scale = softmax ? 1.0 / wave_sum(sum) : 1.0;
+      const double scale = a.score == 0 ? 1.0 / wave_sum(sum) : 1.0;
 #pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        const int e = lane + kWave * j;
-        const float b = e < E ? a.bias[e] : 0.f;
-        if (!(b > -INFINITY)) l[j] = -INFINITY;   // switched off (its score has counted above)
-        s[j] = s[j] * scale + (double)b;
-      }
+      for (int j = 0; j < PER; ++j) v[j] = v[j] * scale + (double)b[j];
     }
   }
+  Key key[PER];   // 0: masked, taken or not there
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
-    if constexpr (BIAS) key[j] = l[j] == -INFINITY ? 0 : order_key(s[j]);
-    else key[j] = l[j] == -INFINITY ? 0 : order_key(l[j]);
+    const bool none = l[j] == -INFINITY || (BIAS && !(b[j] > -INFINITY));
+    if constexpr (BIAS) key[j] = none ? 0 : order_key(v[j]);
+    else key[j] = none ? 0 : order_key(l[j]);
+    if (none) v[j] = -INFINITY;
   }
-
   if (limited) {
-    const int per = E / a.groups;
+    int side;
+    double gap;
+    const unsigned long long open = open_groups<PER, double>(a, v, graded, lane, side, gap);
+    const float inverse = 1.f / (float)(a.experts / a.groups);
 #pragma unroll
     for (int j = 0; j < PER; ++j)
-      graded[wave][lane + kWave * j] = key[j] == 0 ? -INFINITY : wide ? s[j] : (double)l[j];
-    wave_lds_order();
-    // `side` lanes a group, a power of two; each finds the two largest of its share
-    int padded = 1;
-    while (padded < a.groups) padded *= 2;
-    const int side = kWave / padded, g = lane / side;
-    double first = -INFINITY, second = -INFINITY;
-    if (g < a.groups)
-      for (int i = lane % side; i < per; i += side) {
-        const double v = graded[wave][g * per + i];
-        second = fmax(second, fmin(first, v));
-        first = fmax(first, v);
-      }
-    for (int off = 1; off < side; off *= 2) {
-      const double f = __shfl_xor(first, off, kWave), s2 = __shfl_xor(second, off, kWave);
-      second = fmax(fmin(first, f), fmax(second, s2));
-      first = fmax(first, f);
-    }
-    const double grade = a.group_top == 2 && second > -INFINITY ? first + second : first;
-    int better = 0;   // groups that rank before this lane's
-    for (int o = 0; o < a.groups; ++o) {
-      const double v = __shfl(grade, o * side, kWave);
-      better += v > grade || (v == grade && o < g);
-    }
-    const unsigned long long open = __ballot(g < a.groups && better < a.limit);   // bit side * g
-    const float inverse = 1.f / (float)per;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int of = (int)(((float)(lane + kWave * j) + 0.5f) * inverse);   // exact below 1024 experts
-      if (!((open >> (of * side & 63)) & 1)) key[j] = 0;
-    }
+      if (!group_open(open, side, inverse, lane + kWave * j)) key[j] = 0;
   }
-
   int my_id = -1;
   for (int r = 0; r < a.top_k; ++r) {
     Key best = 0;
@@ -169,10 +191,158 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
       if (id == lane + kWave * j) key[j] = 0;
     if (lane == r) my_id = id;
   }
+  return my_id;
+}
 
-  // weights, a slot a lane
-  const bool live = my_id >= 0;
-  const float x = live ? finite(load_logit(a.logits, a.f32, (size_t)t * a.ld + my_id)) : -INFINITY;
+// One wave a token; PER logits per lane (expert lane + 64 j).
+//   The quick way: of the lanes' largest values the k-th, found bit by bit with
+// ballots, bounds the k-th largest of all from below; what reaches it, about
+// k + 2 experts, is packed to one a lane, ordered exactly and ranked by
+// comparison with every other. k rounds of the best over the wave took 80 us
+// for 16383 tokens of 896 experts, top-16, where this takes WWW.
+//   With a bias the bound is taken in fp32 and lowered by twice what an fp32
+// value can be off, so that no expert of the fp64 order is lost, and only the
+// packed ones get fp64 values: one exponential a lane for six. Groups are
+// graded in fp32 too where the grades at the border are further apart than
+// that. Left to the rounds are a bias on softmax scores (whose sum would have
+// to be fp64), grades that close and more than 64 experts that reach the
+// bound (many equal ones).
+template <int PER, bool BIAS>
+__global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectArgs a) {
+  __shared__ double shared[kTokensPerBlock][PER * kWave];
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int t = blockIdx.x * kTokensPerBlock + wave;
+  if (t >= a.rows) return;   // whole waves
+  const int E = a.experts, k = a.top_k;
+  const bool softmax = a.score == 0, limited = a.groups > a.limit;
+  const size_t row = (size_t)t * a.ld;
+  float l[PER], b[PER];   // l: -inf where masked
+  float top = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int e = lane + kWave * j;
+    const float v = e < E ? load_logit(a.logits, a.f32, row + e) : -INFINITY;
+    l[j] = is_masked(v) ? -INFINITY : finite(v);
+    b[j] = BIAS && e < E ? a.bias[e] : 0.f;
+    top = fmaxf(top, l[j]);
+  }
+  float total = 0.f;   // of exp(l - top)
+  if (softmax) {
+    top = wave_max(top);
+    if (top == -INFINITY) top = 0.f;   // every expert masked
+    if (!a.renormalize) {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) total += quick_exp(l[j] - top);
+      total = wave_sum(total);
+    }
+  }
+
+  // fp32 values: the logit, or an approximate score plus the bias
+  float value[PER];
+  bool settled = !(BIAS && softmax);
+  constexpr float kOff = 0x1p-20f;   // an approximate value v is off by less than kOff (1 + |v|)
+  if (settled) {
+    const bool graded = limited && !BIAS && a.group_top == 2;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      value[j] = l[j];
+      if (BIAS || graded) {
+        const float small = quick_exp(softmax ? l[j] - top : -fabsf(l[j]));
+        const float s = softmax ? small : (l[j] < 0.f ? small : 1.f) * __builtin_amdgcn_rcpf(1.f + small);
+        value[j] = l[j] == -INFINITY || (BIAS && !(b[j] > -INFINITY)) ? -INFINITY : s + b[j];
+      }
+    }
+    if (limited) {
+      int side;
+      float gap;
+      const unsigned long long open =
+          open_groups<PER, float>(a, value, reinterpret_cast<float*>(shared[wave]), lane, side, gap);
+      float most = -INFINITY;
+      if (BIAS || graded) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+          if (value[j] > -INFINITY) most = fmaxf(most, fabsf(value[j]));
+        // two sums of two values; a gap to a group without experts is infinite
+        settled = gap > 8.f * kOff * (1.f + fmaxf(wave_max(most), 0.f));
+      }
+      const float inverse = 1.f / (float)(E / a.groups);
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        if (graded) value[j] = l[j];
+        if (!group_open(open, side, inverse, lane + kWave * j)) value[j] = -INFINITY;
+      }
+    }
+  }
+
+  int id = -1, slot = lane;   // this lane's expert, and its place among the chosen
+  float x = -INFINITY;
+  if (settled) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) most = max(most, value[j] == -INFINITY ? 0u : order_key(value[j]));
+    uint32_t bound = 1;   // of the lanes' largest, the k-th or a little less
+    if (PER > 1) {
+      bound = 0;
+      for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t next = bound | 1u << bit;
+        const int n = __popcll(__ballot(most >= next));
+        if (n >= k) bound = next;
+        if (n == k) break;
+      }
+      if (bound == 0) bound = 1;   // fewer than k lanes have an expert
+      if (BIAS && bound > 1) {
+        const uint32_t u = bound & 0x80000000u ? bound ^ 0x80000000u : ~bound;   // the value of a key
+        const float v = __uint_as_float(u), low = v - 2.f * kOff * (1.f + fabsf(v));
+        bound = low > -INFINITY ? order_key(low) : 1;   // an infinite bias: every expert (1), or too many
+      }
+    }
+    int n = 0;
+    uint2* const packed = reinterpret_cast<uint2*>(shared[wave]);
+    wave_lds_order();   // the grades have been read
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const bool in = value[j] > -INFINITY && order_key(value[j]) >= bound;
+      const unsigned long long mask = __ballot(in);
+      const int at = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+      if (in && at < kMostCandidates) packed[at] = make_uint2(lane + kWave * j, __float_as_uint(l[j]));   // ids ascend
+      n += __popcll(mask);
+    }
+    wave_lds_order();
+    settled = n <= kMostCandidates;
+    if (settled) {
+      using Key = std::conditional_t<BIAS, unsigned long long, uint32_t>;
+      Key key = 0;
+      if (lane < n) {
+        const uint2 v = packed[lane];
+        id = (int)v.x;
+        x = __uint_as_float(v.y);
+        if constexpr (BIAS) key = order_key(1.0 / (1.0 + exp(-(double)x)) + (double)a.bias[id]);
+        else key = order_key(x);
+      }
+      slot = 0;
+      for (int s = 0; s < n; ++s) {
+        Key other;
+        if constexpr (BIAS)
+          other = (unsigned long long)(uint32_t)__builtin_amdgcn_readlane((int)(key >> 32), s) << 32 |
+                  (uint32_t)__builtin_amdgcn_readlane((int)key, s);
+        else
+          other = (uint32_t)__builtin_amdgcn_readlane((int)key, s);
+        slot += other > key || (other == key && s < lane);
+      }
+      if (lane >= n) slot = lane;   // an empty slot, if it is one
+      else if (slot >= k) id = -1;
+    }
+  }
+  if (!settled) {
+    wave_lds_order();
+    id = select_by_rounds<PER, BIAS>(a, l, b, top, shared[wave], lane);
+    slot = lane;
+    x = id >= 0 ? finite(load_logit(a.logits, a.f32, row + id)) : -INFINITY;
+  }
+
+  // weights
+  const bool live = id >= 0;
+  if (!live) x = -INFINITY;
   float w;
   if (softmax) {
     w = expf(x - (a.renormalize ? wave_max(x) : top));
@@ -187,9 +357,9 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
     const float sum = wave_sum(w);
     if (live) w /= sum;
   }
-  if (lane < a.top_k) {
-    a.ids[(size_t)t * a.top_k + lane] = my_id;
-    a.weights[(size_t)t * a.top_k + lane] = w * a.scale;
+  if (slot < k) {
+    a.ids[(size_t)t * k + slot] = id;
+    a.weights[(size_t)t * k + slot] = w * a.scale;
   }
 }
 
@@ -231,7 +401,7 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select_backward
     total = 0.f;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-      l[j] = expf(l[j] - top);
+      l[j] = quick_exp(l[j] - top);
       total += l[j];
     }
     total = wave_sum(total);
@@ -250,7 +420,7 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select_backward
     if (!softmax) d *= other;
   } else if (softmax) {
     d = g;
-    base = wave_sum(live ? expf(x - top) / total * g : 0.f);
+    base = wave_sum(live ? quick_exp(x - top) / total * g : 0.f);
   } else {
     d = g * other * (x < 0.f ? small : 1.f) / (1.f + small);
   }
@@ -263,12 +433,13 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select_backward
   wave_lds_order();
   if (live) row[id] = mine;
   wave_lds_order();
+  const float inverse = 1.f / total;
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const int e = lane + kWave * j;
     if (e >= E) break;
     float v = row[e];
-    if (dense) v = l[j] > 0.f ? l[j] / total * (v - base) : 0.f;
+    if (dense) v = l[j] > 0.f ? l[j] * inverse * (v - base) : 0.f;
     if (a.f32) static_cast<float*>(a.dlogits)[(size_t)t * E + e] = v;
     else static_cast<uint16_t*>(a.dlogits)[(size_t)t * E + e] = f32_to_bf16_rne(v);
   }

@@ -166,6 +166,40 @@ def test_select_masks(dtype, score, renormalize, biased, groups):
     assert (ids[:2] == -1).all() and (w[:2] == 0).all()
 
 
+@pytest.mark.parametrize("E,near", [(40, 40), (384, 30), (384, 384), (896, 60), (1024, 65)])
+@pytest.mark.parametrize("groups", [{}, dict(num_groups=8, group_limit=3, group_top=2),
+                                    dict(num_groups=8, group_limit=4, group_top=1)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_select_orders_values_that_fp32_cannot(E, near, groups, score):
+    """Biases that bring `near` experts' values within a rounding of fp32 of one another."""
+    rng = np.random.default_rng(near + E)
+    l = np.repeat(rng.standard_normal((1, E)).astype(np.float32), 5, axis=0)
+    s = oracle.scores(l[0], score)
+    bias = rng.standard_normal(E) * 0.05 - 2.0
+    pick = rng.permutation(E)[:near]
+    bias[pick] = (0.9 - s)[pick]
+    l[1:] += (rng.standard_normal((4, E)) * 1e-7 * np.abs(l[1:])).astype(np.float32)   # the last bits of some logits
+    value = s + bias.astype(np.float32)
+    gaps = np.diff(np.sort(value[pick]))
+    assert (gaps < 6e-8).mean() > 0.9 and (gaps > 1e-14).mean() > 0.5
+    check_select(up(l), 8, score, bias=bias, **groups)
+
+
+def test_select_of_few_lanes_with_experts():
+    """Fewer lanes than slots hold an open expert; one lane holds many."""
+    l = np.full((4, 1024), -INF, np.float32)
+    rng = np.random.default_rng(1)
+    l[0, 5::64] = rng.standard_normal(16)            # all of one lane's
+    l[1, 5::64] = rng.standard_normal(16)
+    l[1, 6::64] = rng.standard_normal(16)
+    l[2, :20] = rng.standard_normal(20)
+    l[3, [0, 1023]] = [1.0, 2.0]
+    for bias in (None, rng.standard_normal(1024) * 0.1):
+        for score in SCORE:
+            check_select(up(l), 16, score, bias=bias)
+            check_select(up(l), 32, score, bias=bias, num_groups=2, group_limit=1, group_top=2)
+
+
 def test_select_keeps_scores_that_underflow():
     """Renormalised weights of experts that only the bias selects: their softmax is below
     fp32's range, the ratio is not."""
