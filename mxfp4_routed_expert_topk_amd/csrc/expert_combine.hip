@@ -59,55 +59,103 @@ __global__ __launch_bounds__(kThreads) void expert_combine(CombineArgs a) {
   }
 }
 
-// One workgroup a token; a thread owns columns 8 threadIdx.x + 8 blockDim.x i.
+// One workgroup a token; a thread owns columns 8 threadIdx.x + 8 blockDim.x i
+// and keeps dout's in registers over the slots, whose rows of y are loaded
+// eight together. dout is read once (with a loop over the slots outside, and a
+// wait for each row, 4096 tokens of 8 x 7168 took 285 us, so 194: 1.0 GB at 5.1 TB/s). y passes the caches by and dy
+// too (206 and 208 us with plain loads or stores).
 // A row of dy belongs to the route that perm names alone, whatever rowpos
 // holds, so no two workgroups write one.
+//   dweights: a thread's products in the order of its columns, then the wave's
+// lanes and the waves in a fixed order.
 constexpr int kBackThreads = 1024;
-template <bool F32>
+
+__device__ __forceinline__ float lanes_sum(float v) {   // on lane 63, by DPP moves
+#define MOE_DPP_ADD(ctrl, rows) \
+  v += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), ctrl, rows, 0xF, false))
+  MOE_DPP_ADD(0x111, 0xF);   // row_shr 1, 2, 4, 8
+  MOE_DPP_ADD(0x112, 0xF);
+  MOE_DPP_ADD(0x114, 0xF);
+  MOE_DPP_ADD(0x118, 0xF);
+  MOE_DPP_ADD(0x142, 0xA);   // row_bcast 15, 31
+  MOE_DPP_ADD(0x143, 0xC);
+#undef MOE_DPP_ADD
+  return v;
+}
+
+template <bool F32, bool DW>
 __global__ __launch_bounds__(kBackThreads) void expert_combine_backward(CombineBackwardArgs a) {
   __shared__ float part[kBackThreads / kWave][kMaxTopK];
-  const int t = blockIdx.x, lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  for (int s = 0; s < a.top_k; ++s) {
-    const size_t f = (size_t)t * a.top_k + s;
-    const int r = a.rowpos[f];
-    const bool live = r >= 0 && r < a.rows;
-    const bool owns = a.dy && live && a.perm[r] == (long long)f;
-    const float w = live && a.weights ? a.weights[f] : 1.f;
-    float dot = 0.f;
-    if (live)
-      for (int c = threadIdx.x * 8; c < a.hidden; c += blockDim.x * 8) {
-        float d[8];
-        if constexpr (F32) {
-          const f32x4_t* const p = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(a.dout) + (size_t)t * a.lddout + c);
-          const f32x4_t lo = p[0], hi = p[1];
+  const int t = blockIdx.x, lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, k = a.top_k;
+  // slot s on lane s: its row (-1: none), whether dy's row is its own, its weight
+  int row = -1, own = 0;
+  float weight = 1.f;
+  if (lane < k) {
+    const size_t f = (size_t)t * k + lane;
+    row = a.rowpos[f];
+    if (row < 0 || row >= a.rows) row = -1;
+    if (row >= 0) {
+      own = a.dy && a.perm[row] == (long long)f;
+      if (a.weights) weight = a.weights[f];
+    }
+  }
+  for (int s0 = 0; s0 < k; s0 += kAhead) {
+    float dot[kAhead];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            d[i] = lo[i];
-            d[4 + i] = hi[i];
-          }
-        } else {
-          unpack8(*reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(a.dout) + (size_t)t * a.lddout + c), d);
-        }
-        if (a.dweights) {
-          float v[8];
-          unpack8(*reinterpret_cast<const u32x4_t*>(a.y + (size_t)r * a.ldy + c), v);
+    for (int j = 0; j < kAhead; ++j) dot[j] = 0.f;
+    for (int c = threadIdx.x * 8; c < a.hidden; c += blockDim.x * 8) {
+      u32x4_t v[kAhead];
+      if (DW) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dot = fmaf(d[i], v[i], dot);
+        for (int j = 0; j < kAhead; ++j) {
+          const int r = s0 + j < k ? __builtin_amdgcn_readlane(row, s0 + j) : -1;
+          if (r >= 0) v[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(a.y + (size_t)r * a.ldy + c));
         }
-        if (owns)
-          *reinterpret_cast<u32x4_t*>(a.dy + (size_t)r * a.hidden + c) =
-              u32x4_t{bf16_pair(w * d[0], w * d[1]), bf16_pair(w * d[2], w * d[3]), bf16_pair(w * d[4], w * d[5]),
-                      bf16_pair(w * d[6], w * d[7])};
+      }
+      float d[8];
+      if constexpr (F32) {
+        const f32x4_t* const p = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(a.dout) + (size_t)t * a.lddout + c);
+        const f32x4_t lo = p[0], hi = p[1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          d[i] = lo[i];
+          d[4 + i] = hi[i];
+        }
+      } else {
+        unpack8(*reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(a.dout) + (size_t)t * a.lddout + c), d);
       }
 #pragma unroll
-    for (int off = kWave / 2; off > 0; off >>= 1) dot += __shfl_xor(dot, off, kWave);
-    if (lane == 0) part[wave][s] = dot;
+      for (int j = 0; j < kAhead; ++j) {
+        if (s0 + j >= k) break;
+        const int r = __builtin_amdgcn_readlane(row, s0 + j);
+        if (__builtin_amdgcn_readlane(own, s0 + j)) {
+          const float w = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(weight), s0 + j));
+          const u32x4_t o = {bf16_pair(w * d[0], w * d[1]), bf16_pair(w * d[2], w * d[3]), bf16_pair(w * d[4], w * d[5]),
+                             bf16_pair(w * d[6], w * d[7])};
+          __builtin_nontemporal_store(o, reinterpret_cast<u32x4_t*>(a.dy + (size_t)r * a.hidden + c));
+        }
+        if (DW && r >= 0) {
+          float f[8];
+          unpack8(v[j], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot[j] = fmaf(d[i], f[i], dot[j]);
+        }
+      }
+    }
+    if (DW) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const float sum = lanes_sum(dot[j]);
+        if (lane == kWave - 1 && s0 + j < k) part[wave][s0 + j] = sum;
+      }
+    }
   }
+  if (!DW) return;
   __syncthreads();
-  if (a.dweights && (int)threadIdx.x < a.top_k) {
+  if ((int)threadIdx.x < k) {
     float sum = 0.f;
     for (int w = 0; w < (int)blockDim.x / kWave; ++w) sum += part[w][threadIdx.x];
-    a.dweights[(size_t)t * a.top_k + threadIdx.x] = sum;
+    a.dweights[(size_t)t * k + threadIdx.x] = sum;
   }
 }
 
@@ -125,8 +173,9 @@ hipError_t launch_expert_combine(const CombineArgs& a, bool f32, hipStream_t str
 hipError_t launch_expert_combine_backward(const CombineBackwardArgs& a, bool f32, hipStream_t stream) {
   const int chunks = a.hidden / 8;
   const dim3 block(chunks >= kBackThreads ? kBackThreads : (chunks + kWave - 1) / kWave * kWave);
-  if (f32) hipLaunchKernelGGL(expert_combine_backward<true>, dim3(a.tokens), block, 0, stream, a);
-  else hipLaunchKernelGGL(expert_combine_backward<false>, dim3(a.tokens), block, 0, stream, a);
+  auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(a.tokens), block, 0, stream, a); };
+  if (f32) run(a.dweights ? expert_combine_backward<true, true> : expert_combine_backward<true, false>);
+  else run(a.dweights ? expert_combine_backward<false, true> : expert_combine_backward<false, false>);
   return hipGetLastError();
 }
 

@@ -79,6 +79,16 @@ __device__ __forceinline__ void wave_lds_order() {
 
 constexpr int kMostCandidates = kWave;
 
+// v of a uniform lane
+__device__ __forceinline__ float at_lane(float v, int lane) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+}
+__device__ __forceinline__ double at_lane(double v, int lane) {
+  const long long u = __double_as_longlong(v);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), lane);
+  return __longlong_as_double((long long)((unsigned long long)hi << 32 | (uint32_t)__builtin_amdgcn_readlane((int)u, lane)));
+}
+
 // The groups that stay, from each expert's value (-INFINITY: none): bit
 // side * g of the result, `side` lanes a group. gap: what separates the last
 // that stays from the first that does not.
@@ -108,13 +118,13 @@ __device__ __forceinline__ unsigned long long open_groups(const SelectArgs& a, c
   const V grade = g >= a.groups ? -INFINITY : a.group_top == 2 && second > -INFINITY ? first + second : first;
   int better = 0;   // groups that rank before this lane's
   for (int o = 0; o < a.groups; ++o) {
-    const V v = __shfl(grade, o * side, kWave);
+    const V v = at_lane(grade, o * side);
     better += v > grade || (v == grade && o < g);
   }
   const unsigned long long open = __ballot(g < a.groups && better < a.limit);
   const int last = __ffsll((unsigned long long)__ballot(g < a.groups && better == a.limit - 1)) - 1;
   const int next = __ffsll((unsigned long long)__ballot(g < a.groups && better == a.limit)) - 1;
-  gap = __shfl(grade, last, kWave) - __shfl(grade, next, kWave);
+  gap = at_lane(grade, last) - at_lane(grade, next);
   return open;
 }
 
@@ -262,8 +272,9 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
 #pragma unroll
         for (int j = 0; j < PER; ++j)
           if (value[j] > -INFINITY) most = fmaxf(most, fabsf(value[j]));
-        // two sums of two values; a gap to a group without experts is infinite
-        settled = gap > 8.f * kOff * (1.f + fmaxf(wave_max(most), 0.f));
+        most = wave_max(most);
+        // two sums of two values; a gap to a group without experts is infinite, and a row without any has no order
+        settled = most == -INFINITY || gap > 8.f * kOff * (1.f + most);
       }
       const float inverse = 1.f / (float)(E / a.groups);
 #pragma unroll
