@@ -200,14 +200,17 @@ hipError_t launch_router_topk(const float* logits, int32_t T, int32_t E, int32_t
 // E <= kRouterMaxExperts, k <= kMaxTopK, groups <= kRouterMaxGroups, rows above zero.
 constexpr int kRouterMaxGroups = 64;
 struct SelectArgs {
-  const void* logits;   // [rows, experts] bf16 or (f32) fp32, rows ld apart
+  const void* logits;   // [rows, experts] bf16 or fp32, rows ld apart
   long long ld;
   const float* bias;    // [experts] or null
   int32_t* ids;         // [rows, top_k]
   float* weights;       // [rows, top_k]
   int rows, experts, top_k, groups, limit, group_top, score;
   float scale;
-  bool f32, renormalize;
+  bool renormalize;
+  // filled in by the launcher: experts of a group and the inverse, log2 of the lanes a group has
+  int per = 0, side = 0;
+  float inverse = 0.f;
 };
 struct SelectBackwardArgs {
   const float* dweights;   // [rows, top_k]
@@ -217,10 +220,10 @@ struct SelectBackwardArgs {
   void* dlogits;           // [rows, experts] of the logits' type
   int rows, experts, top_k, score;
   float scale;
-  bool f32, renormalize;
+  bool renormalize;
 };
-hipError_t launch_router_select(const SelectArgs& a, hipStream_t stream);
-hipError_t launch_router_select_backward(const SelectBackwardArgs& a, hipStream_t stream);
+hipError_t launch_router_select(SelectArgs a, bool f32, hipStream_t stream);
+hipError_t launch_router_select_backward(const SelectBackwardArgs& a, bool f32, hipStream_t stream);
 
 // out [m, n] = x [m, k] W [n, k]^T with MXFP4 W, or (gate) silu of its first
 // n / 2 columns times the others (mxfp4_linear.hip); k a multiple of 32.

@@ -233,7 +233,7 @@ moe_status moe_router_select(const void* logits, int32_t dtype, int64_t ldl, int
     if (moe_status s = check_ptrs({{"bias", bias, 4}})) return s;
   const hipError_t e = moe::launch_router_select(
       {logits, ldl, bias, topk_ids, topk_weights, num_tokens, num_experts, top_k, num_groups, group_limit, group_top,
-       score, scale, dtype == MOE_F32, renormalize != 0}, stream);
+       score, scale, renormalize != 0}, dtype == MOE_F32, stream);
   return e == hipSuccess ? ok() : hip_fail(e, "router select launch");
 }
 
@@ -248,8 +248,8 @@ moe_status moe_router_select_backward(const float* dweights, const void* logits,
                                  {"dlogits", dlogits}}))
     return s;
   const hipError_t e = moe::launch_router_select_backward(
-      {dweights, logits, ldl, topk_ids, dlogits, num_tokens, num_experts, top_k, score, scale, dtype == MOE_F32,
-       renormalize != 0}, stream);
+      {dweights, logits, ldl, topk_ids, dlogits, num_tokens, num_experts, top_k, score, scale, renormalize != 0},
+      dtype == MOE_F32, stream);
   return e == hipSuccess ? ok() : hip_fail(e, "router select backward launch");
 }
 

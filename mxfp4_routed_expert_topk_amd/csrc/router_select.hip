@@ -21,11 +21,15 @@ namespace {
 
 constexpr int kTokensPerBlock = 4;   // one wave a token
 
-__device__ __forceinline__ float load_logit(const void* p, bool f32, size_t i) {
-  return f32 ? static_cast<const float*>(p)[i] : __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
+template <bool F32>
+__device__ __forceinline__ float load_logit(const void* p, size_t i) {
+  return F32 ? static_cast<const float*>(p)[i] : __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
 }
-__device__ __forceinline__ bool is_masked(float l) { return !(l > -INFINITY); }
-__device__ __forceinline__ float finite(float l) { return fminf(l, 3.402823466e38f); }
+constexpr float kMost = 3.402823466e38f;   // fp32's largest number
+// NaN as -inf, +inf as the largest number (as integers: what lies above it is infinite or NaN)
+__device__ __forceinline__ float cleaned(float l) {
+  return l > -INFINITY ? __int_as_float(min(__float_as_int(l), __float_as_int(kMost))) : -INFINITY;
+}
 
 // Order-preserving integers; 0 is below every value.  -0 and +0 are equal.
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -77,8 +81,6 @@ __device__ __forceinline__ void wave_lds_order() {
   __builtin_amdgcn_wave_barrier();
 }
 
-constexpr int kMostCandidates = kWave;
-
 // v of a uniform lane
 __device__ __forceinline__ float at_lane(float v, int lane) {
   return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
@@ -89,24 +91,19 @@ __device__ __forceinline__ double at_lane(double v, int lane) {
   return __longlong_as_double((long long)((unsigned long long)hi << 32 | (uint32_t)__builtin_amdgcn_readlane((int)u, lane)));
 }
 
-// The groups that stay, from each expert's value (-INFINITY: none): bit
-// side * g of the result, `side` lanes a group. gap: what separates the last
-// that stays from the first that does not.
+// The groups that stay (bit g), from each expert's value (-INFINITY: none).
+// gap: what separates the last that stays from the first that does not.
 template <int PER, class V>
 __device__ __forceinline__ unsigned long long open_groups(const SelectArgs& a, const V (&value)[PER], V* graded, int lane,
-                                                          int& side, V& gap) {
-  const int per = a.experts / a.groups;
+                                                          V& gap) {
 #pragma unroll
   for (int j = 0; j < PER; ++j) graded[lane + kWave * j] = value[j];
   wave_lds_order();
-  int padded = 1;
-  while (padded < a.groups) padded *= 2;
-  side = kWave / padded;
-  const int g = lane / side;
-  V first = -INFINITY, second = -INFINITY;   // the two largest of the lane's share
-  if (g < a.groups)
-    for (int i = lane % side; i < per; i += side) {
-      const V v = graded[g * per + i];
+  const int side = 1 << a.side, share = lane >> a.side;   // `side` lanes a group
+  V first = -INFINITY, second = -INFINITY;                // the two largest of the lane's experts
+  if (share < a.groups)
+    for (int i = lane & (side - 1); i < a.per; i += side) {
+      const V v = graded[share * a.per + i];
       second = max(second, min(first, v));
       first = max(first, v);
     }
@@ -115,23 +112,25 @@ __device__ __forceinline__ unsigned long long open_groups(const SelectArgs& a, c
     second = max(min(first, f), max(second, s));
     first = max(first, f);
   }
-  const V grade = g >= a.groups ? -INFINITY : a.group_top == 2 && second > -INFINITY ? first + second : first;
-  int better = 0;   // groups that rank before this lane's
+  const V sum = a.group_top == 2 && second > -INFINITY ? first + second : first;
+  const V grade = __shfl(sum, lane << a.side & (kWave - 1), kWave);   // group g on lane g
+  int better = 0;                                                     // groups that rank before it
   for (int o = 0; o < a.groups; ++o) {
-    const V v = at_lane(grade, o * side);
-    better += v > grade || (v == grade && o < g);
+    const V v = at_lane(grade, o);
+    better += v > grade || (v == grade && o < lane);
   }
-  const unsigned long long open = __ballot(g < a.groups && better < a.limit);
-  const int last = __ffsll((unsigned long long)__ballot(g < a.groups && better == a.limit - 1)) - 1;
-  const int next = __ffsll((unsigned long long)__ballot(g < a.groups && better == a.limit)) - 1;
-  gap = at_lane(grade, last) - at_lane(grade, next);
-  return open;
+  const bool is = lane < a.groups;
+  const int last = __ffsll((unsigned long long)__ballot(is && better == a.limit - 1)) - 1;
+  const int next = __ffsll((unsigned long long)__ballot(is && better == a.limit)) - 1;
+  gap = at_lane(grade, last & (kWave - 1)) - at_lane(grade, next & (kWave - 1));   // (none of a rank: NaN grades)
+  return __ballot(is && better < a.limit);
 }
 
-// Whether expert lane + 64 j's group is open.
-__device__ __forceinline__ bool group_open(unsigned long long open, int side, float inverse, int e) {
-  const int of = (int)(((float)e + 0.5f) * inverse);   // e / per, exact below 1024 experts
-  return (open >> (of * side & 63)) & 1;
+// Whether expert e's group is open.
+__device__ __forceinline__ bool group_open(const SelectArgs& a, unsigned long long open, int e) {
+  const int of = (int)(((float)e + 0.5f) * a.inverse);   // e / per, exact below 1024 experts
+  const uint32_t word = a.groups > 32 && of >= 32 ? (uint32_t)(open >> 32) : (uint32_t)open;
+  return word >> (of & 31) & 1;
 }
 
 // The ids of a token's slots, slot r on lane r (-1: none), by k rounds of the
@@ -168,13 +167,11 @@ __device__ __forceinline__ int select_by_rounds(const SelectArgs& a, const float
     if (none) v[j] = -INFINITY;
   }
   if (limited) {
-    int side;
     double gap;
-    const unsigned long long open = open_groups<PER, double>(a, v, graded, lane, side, gap);
-    const float inverse = 1.f / (float)(a.experts / a.groups);
+    const unsigned long long open = open_groups<PER, double>(a, v, graded, lane, gap);
 #pragma unroll
     for (int j = 0; j < PER; ++j)
-      if (!group_open(open, side, inverse, lane + kWave * j)) key[j] = 0;
+      if (!group_open(a, open, lane + kWave * j)) key[j] = 0;
   }
   int my_id = -1;
   for (int r = 0; r < a.top_k; ++r) {
@@ -204,6 +201,10 @@ __device__ __forceinline__ int select_by_rounds(const SelectArgs& a, const float
   return my_id;
 }
 
+// Whether logit j of every lane exists: E is above 64 (PER - 2), and 64 for PER 2.
+template <int PER>
+__device__ __forceinline__ bool there(int j) { return j < PER - 2; }
+
 // One wave a token; PER logits per lane (expert lane + 64 j).
 //   The quick way: of the lanes' largest values the k-th, found bit by bit with
 // ballots, bounds the k-th largest of all from below; what reaches it, about
@@ -217,7 +218,7 @@ __device__ __forceinline__ int select_by_rounds(const SelectArgs& a, const float
 // that. Left to the rounds are a bias on softmax scores (whose sum would have
 // to be fp64), grades that close and more than 64 experts that reach the
 // bound (many equal ones).
-template <int PER, bool BIAS>
+template <int PER, bool BIAS, bool F32>
 __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectArgs a) {
   __shared__ double shared[kTokensPerBlock][PER * kWave];
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -231,9 +232,11 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const int e = lane + kWave * j;
-    const float v = e < E ? load_logit(a.logits, a.f32, row + e) : -INFINITY;
-    l[j] = is_masked(v) ? -INFINITY : finite(v);
-    b[j] = BIAS && e < E ? a.bias[e] : 0.f;
+    const bool in = there<PER>(j) || e < E;
+    const int at = there<PER>(j) ? e : min(e, E - 1);   // loaded without a branch, which would wait
+    l[j] = cleaned(load_logit<F32>(a.logits, row + at));
+    b[j] = BIAS ? a.bias[at] : 0.f;
+    if (!in) l[j] = -INFINITY;
     top = fmaxf(top, l[j]);
   }
   float total = 0.f;   // of exp(l - top)
@@ -263,10 +266,8 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
       }
     }
     if (limited) {
-      int side;
       float gap;
-      const unsigned long long open =
-          open_groups<PER, float>(a, value, reinterpret_cast<float*>(shared[wave]), lane, side, gap);
+      const unsigned long long open = open_groups<PER, float>(a, value, reinterpret_cast<float*>(shared[wave]), lane, gap);
       float most = -INFINITY;
       if (BIAS || graded) {
 #pragma unroll
@@ -276,11 +277,10 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
         // two sums of two values; a gap to a group without experts is infinite, and a row without any has no order
         settled = most == -INFINITY || gap > 8.f * kOff * (1.f + most);
       }
-      const float inverse = 1.f / (float)(E / a.groups);
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
         if (graded) value[j] = l[j];
-        if (!group_open(open, side, inverse, lane + kWave * j)) value[j] = -INFINITY;
+        if (!group_open(a, open, lane + kWave * j)) value[j] = -INFINITY;
       }
     }
   }
@@ -288,23 +288,23 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
   int id = -1, slot = lane;   // this lane's expert, and its place among the chosen
   float x = -INFINITY;
   if (settled) {
-    uint32_t most = 0;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) most = max(most, value[j] == -INFINITY ? 0u : order_key(value[j]));
-    uint32_t bound = 1;   // of the lanes' largest, the k-th or a little less
+    float bound = -kMost;   // what a candidate reaches
     if (PER > 1) {
-      bound = 0;
+      float most = value[0];
+#pragma unroll
+      for (int j = 1; j < PER; ++j) most = fmaxf(most, value[j]);
+      const uint32_t key = most > -INFINITY ? order_key(most) : 0;
+      uint32_t kth = 0;   // of the lanes' largest keys, the k-th or a little less
       for (int bit = 31; bit >= 0; --bit) {
-        const uint32_t next = bound | 1u << bit;
-        const int n = __popcll(__ballot(most >= next));
-        if (n >= k) bound = next;
+        const uint32_t next = kth | 1u << bit;
+        const int n = __popcll(__ballot(key >= next));
+        if (n >= k) kth = next;
         if (n == k) break;
       }
-      if (bound == 0) bound = 1;   // fewer than k lanes have an expert
-      if (BIAS && bound > 1) {
-        const uint32_t u = bound & 0x80000000u ? bound ^ 0x80000000u : ~bound;   // the value of a key
-        const float v = __uint_as_float(u), low = v - 2.f * kOff * (1.f + fabsf(v));
-        bound = low > -INFINITY ? order_key(low) : 1;   // an infinite bias: every expert (1), or too many
+      if (kth) bound = __uint_as_float(kth & 0x80000000u ? kth ^ 0x80000000u : ~kth);   // else fewer than k lanes have one
+      if (BIAS) {
+        bound -= 2.f * kOff * (1.f + fabsf(bound));
+        if (!(bound > -kMost)) bound = -kMost;   // NaN of an infinite bias: every expert is a candidate
       }
     }
     int n = 0;
@@ -312,33 +312,33 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
     wave_lds_order();   // the grades have been read
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-      const bool in = value[j] > -INFINITY && order_key(value[j]) >= bound;
+      const bool in = value[j] >= bound;
       const unsigned long long mask = __ballot(in);
-      const int at = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
-      if (in && at < kMostCandidates) packed[at] = make_uint2(lane + kWave * j, __float_as_uint(l[j]));   // ids ascend
+      const int at = __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, n));
+      if (in) packed[at] = make_uint2(lane + kWave * j, __float_as_uint(l[j]));   // ids ascend; there is room for all
       n += __popcll(mask);
     }
     wave_lds_order();
-    settled = n <= kMostCandidates;
+    settled = n <= kWave;
     if (settled) {
-      using Key = std::conditional_t<BIAS, unsigned long long, uint32_t>;
-      Key key = 0;
       if (lane < n) {
         const uint2 v = packed[lane];
         id = (int)v.x;
         x = __uint_as_float(v.y);
-        if constexpr (BIAS) key = order_key(1.0 / (1.0 + exp(-(double)x)) + (double)a.bias[id]);
-        else key = order_key(x);
       }
-      slot = 0;
-      for (int s = 0; s < n; ++s) {
-        Key other;
-        if constexpr (BIAS)
-          other = (unsigned long long)(uint32_t)__builtin_amdgcn_readlane((int)(key >> 32), s) << 32 |
-                  (uint32_t)__builtin_amdgcn_readlane((int)key, s);
-        else
-          other = (uint32_t)__builtin_amdgcn_readlane((int)key, s);
-        slot += other > key || (other == key && s < lane);
+      slot = 0;   // how many candidates rank before the lane's
+      if constexpr (BIAS) {
+        const unsigned long long key = lane < n ? order_key(1.0 / (1.0 + exp(-(double)x)) + (double)a.bias[id]) : 0;
+        for (int s = 0; s < n; ++s) {
+          const unsigned long long other = (unsigned long long)(uint32_t)__builtin_amdgcn_readlane((int)(key >> 32), s) << 32 |
+                                           (uint32_t)__builtin_amdgcn_readlane((int)key, s);
+          slot += other > key || (other == key && s < lane);
+        }
+      } else {
+        const uint32_t high = order_key(x);
+        const unsigned long long key = (unsigned long long)high << 32 | (uint32_t)(kWave - lane);
+        for (int s = 0; s < n; ++s)
+          slot += ((unsigned long long)(uint32_t)__builtin_amdgcn_readlane((int)high, s) << 32 | (uint32_t)(kWave - s)) > key;
       }
       if (lane >= n) slot = lane;   // an empty slot, if it is one
       else if (slot >= k) id = -1;
@@ -348,7 +348,7 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
     wave_lds_order();
     id = select_by_rounds<PER, BIAS>(a, l, b, top, shared[wave], lane);
     slot = lane;
-    x = id >= 0 ? finite(load_logit(a.logits, a.f32, row + id)) : -INFINITY;
+    x = id >= 0 ? cleaned(load_logit<F32>(a.logits, row + id)) : -INFINITY;
   }
 
   // weights
@@ -380,7 +380,7 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
 //   sigmoid        dl_j = g_j s_j (1 - s_j)
 //   softmax        dl_e = s_e (G_e - sum s_j g_j), G_e the sum of e's g_j
 // An id that occurs twice gets both slots' terms; all other logits get 0.
-template <int PER>
+template <int PER, bool F32>
 __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select_backward(SelectBackwardArgs a) {
   __shared__ float rows[kTokensPerBlock][PER * kWave];
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
@@ -392,9 +392,8 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select_backward
 #pragma unroll
   for (int j = 0; j < PER; ++j) row[lane + kWave * j] = 0.f;
   const int id = lane < k ? a.ids[(size_t)t * k + lane] : -1;
-  float x = id >= 0 && id < E ? load_logit(a.logits, a.f32, (size_t)t * a.ld + id) : -INFINITY;
-  const bool live = !is_masked(x);
-  x = live ? finite(x) : -INFINITY;
+  const float x = id >= 0 && id < E ? cleaned(load_logit<F32>(a.logits, (size_t)t * a.ld + id)) : -INFINITY;
+  const bool live = x > -INFINITY;
   const float g = live ? a.scale * a.dweights[(size_t)t * k + lane] : 0.f;
 
   float l[PER], top = 0.f, total = 1.f;
@@ -403,8 +402,8 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select_backward
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       const int e = lane + kWave * j;
-      const float v = e < E ? load_logit(a.logits, a.f32, (size_t)t * a.ld + e) : -INFINITY;
-      l[j] = is_masked(v) ? -INFINITY : finite(v);
+      l[j] = cleaned(load_logit<F32>(a.logits, (size_t)t * a.ld + (there<PER>(j) ? e : min(e, E - 1))));
+      if (!there<PER>(j) && e >= E) l[j] = -INFINITY;
       top = fmaxf(top, l[j]);
     }
     top = wave_max(top);
@@ -448,40 +447,46 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select_backward
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const int e = lane + kWave * j;
-    if (e >= E) break;
+    if (!there<PER>(j) && e >= E) break;
     float v = row[e];
     if (dense) v = l[j] > 0.f ? l[j] * inverse * (v - base) : 0.f;
-    if (a.f32) static_cast<float*>(a.dlogits)[(size_t)t * E + e] = v;
+    if constexpr (F32) static_cast<float*>(a.dlogits)[(size_t)t * E + e] = v;
     else static_cast<uint16_t*>(a.dlogits)[(size_t)t * E + e] = f32_to_bf16_rne(v);
   }
 }
 
-// f(integral_constant PER) for the smallest power of two with 64 PER >= E
-template <class F>
+// f(integral_constant PER): 1, or the smallest even number with 64 PER >= E
+template <int PER = 1, class F>
 void per_lane(int E, F f) {
-  if (E <= 64) f(std::integral_constant<int, 1>{});
-  else if (E <= 128) f(std::integral_constant<int, 2>{});
-  else if (E <= 256) f(std::integral_constant<int, 4>{});
-  else if (E <= 512) f(std::integral_constant<int, 8>{});
-  else f(std::integral_constant<int, 16>{});
+  if constexpr (PER < kRouterMaxExperts / kWave) {
+    if (E > kWave * PER) return per_lane<PER == 1 ? 2 : PER + 2>(E, f);
+  }
+  f(std::integral_constant<int, PER>{});
 }
 
 }  // namespace
 
-hipError_t launch_router_select(const SelectArgs& a, hipStream_t stream) {
+hipError_t launch_router_select(SelectArgs a, bool f32, hipStream_t stream) {
+  a.per = a.experts / a.groups;
+  a.inverse = 1.f / (float)a.per;
+  a.side = 6;
+  for (int padded = 1; padded < a.groups; padded *= 2) --a.side;
   const dim3 grid((unsigned)((a.rows + kTokensPerBlock - 1) / kTokensPerBlock)), block(kTokensPerBlock * kWave);
   per_lane(a.experts, [&](auto per) {
     constexpr int PER = decltype(per)::value;
-    if (a.bias) hipLaunchKernelGGL((router_select<PER, true>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((router_select<PER, false>), grid, block, 0, stream, a);
+    auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
+    if (a.bias) run(f32 ? router_select<PER, true, true> : router_select<PER, true, false>);
+    else run(f32 ? router_select<PER, false, true> : router_select<PER, false, false>);
   });
   return hipGetLastError();
 }
 
-hipError_t launch_router_select_backward(const SelectBackwardArgs& a, hipStream_t stream) {
+hipError_t launch_router_select_backward(const SelectBackwardArgs& a, bool f32, hipStream_t stream) {
   const dim3 grid((unsigned)((a.rows + kTokensPerBlock - 1) / kTokensPerBlock)), block(kTokensPerBlock * kWave);
   per_lane(a.experts, [&](auto per) {
-    hipLaunchKernelGGL((router_select_backward<decltype(per)::value>), grid, block, 0, stream, a);
+    constexpr int PER = decltype(per)::value;
+    auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
+    run(f32 ? router_select_backward<PER, true> : router_select_backward<PER, false>);
   });
   return hipGetLastError();
 }
