@@ -133,18 +133,13 @@ __device__ __forceinline__ bool group_open(const SelectArgs& a, unsigned long lo
   return word >> (of & 31) & 1;
 }
 
-// The ids of a token's slots, slot r on lane r (-1: none), by k rounds of the
-// best over the wave, every value exact: for rows that the quick way below
-// cannot settle.
+// The fp64 values that groups are graded by (-inf: masked or switched off).
 template <int PER, bool BIAS>
-__device__ __forceinline__ int select_by_rounds(const SelectArgs& a, const float (&l)[PER], const float (&b)[PER], float top,
-                                                double* graded, int lane) {
-  using Key = std::conditional_t<BIAS, unsigned long long, uint32_t>;
-  const bool limited = a.groups > a.limit;
-  double v[PER];
+__device__ __forceinline__ void exact_values(const SelectArgs& a, const float (&l)[PER], const float (&b)[PER], float top,
+                                             double (&v)[PER]) {
 #pragma unroll
   for (int j = 0; j < PER; ++j) v[j] = (double)l[j];
-  if (BIAS || (limited && a.group_top == 2)) {
+  if (BIAS || (a.groups > a.limit && a.group_top == 2)) {
     double sum = 0.0;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
@@ -158,15 +153,27 @@ __device__ __forceinline__ int select_by_rounds(const SelectArgs& a, const float
       for (int j = 0; j < PER; ++j) v[j] = v[j] * scale + (double)b[j];
     }
   }
+#pragma unroll
+  for (int j = 0; j < PER; ++j)
+    if (l[j] == -INFINITY || (BIAS && !(b[j] > -INFINITY))) v[j] = -INFINITY;
+}
+
+// The ids of a token's slots, slot r on lane r (-1: none), by k rounds of the
+// best over the wave, every value exact: for rows that the quick way below
+// cannot settle.
+template <int PER, bool BIAS>
+__device__ __forceinline__ int select_by_rounds(const SelectArgs& a, const float (&l)[PER], const float (&b)[PER], float top,
+                                                double* graded, int lane) {
+  using Key = std::conditional_t<BIAS, unsigned long long, uint32_t>;
+  double v[PER];
+  exact_values<PER, BIAS>(a, l, b, top, v);
   Key key[PER];   // 0: masked, taken or not there
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
-    const bool none = l[j] == -INFINITY || (BIAS && !(b[j] > -INFINITY));
-    if constexpr (BIAS) key[j] = none ? 0 : order_key(v[j]);
-    else key[j] = none ? 0 : order_key(l[j]);
-    if (none) v[j] = -INFINITY;
+    if constexpr (BIAS) key[j] = v[j] == -INFINITY ? 0 : order_key(v[j]);
+    else key[j] = l[j] == -INFINITY ? 0 : order_key(l[j]);
   }
-  if (limited) {
+  if (a.groups > a.limit) {
     double gap;
     const unsigned long long open = open_groups<PER, double>(a, v, graded, lane, gap);
 #pragma unroll
@@ -210,14 +217,15 @@ __device__ __forceinline__ bool there(int j) { return j < PER - 2; }
 // ballots, bounds the k-th largest of all from below; what reaches it, about
 // k + 2 experts, is packed to one a lane, ordered exactly and ranked by
 // comparison with every other. k rounds of the best over the wave took 80 us
-// for 16383 tokens of 896 experts, top-16, where this takes WWW.
+// for 16383 tokens of 896 experts, top-16, where this takes 17.5;
+// 4133 tokens of 384, top-8, sigmoid scores, a bias and four of eight groups: 19.2 and 8.7.
 //   With a bias the bound is taken in fp32 and lowered by twice what an fp32
 // value can be off, so that no expert of the fp64 order is lost, and only the
 // packed ones get fp64 values: one exponential a lane for six. Groups are
 // graded in fp32 too where the grades at the border are further apart than
-// that. Left to the rounds are a bias on softmax scores (whose sum would have
-// to be fp64), grades that close and more than 64 experts that reach the
-// bound (many equal ones).
+// that, else in fp64. Left to the rounds are a bias on softmax scores (whose
+// sum would have to be fp64) and more than 64 experts that reach the bound
+// (many equal ones).
 template <int PER, bool BIAS, bool F32>
 __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectArgs a) {
   __shared__ double shared[kTokensPerBlock][PER * kWave];
@@ -253,7 +261,9 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
   // fp32 values: the logit, or an approximate score plus the bias
   float value[PER];
   bool settled = !(BIAS && softmax);
-  constexpr float kOff = 0x1p-20f;   // an approximate value v is off by less than kOff (1 + |v|)
+  // An approximate value v is off by less than kOff (1 + |v|): the exponential by (1.5 |x| + 2) u of itself, which
+  // 1 / (1 + e) passes on as 0.7 u at most, the reciprocal 2 u, two roundings and the sum's: 4.7 u + u |v|; 8 u taken.
+  constexpr float kOff = 0x1p-21f;
   if (settled) {
     const bool graded = limited && !BIAS && a.group_top == 2;
 #pragma unroll
@@ -267,15 +277,21 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
     }
     if (limited) {
       float gap;
-      const unsigned long long open = open_groups<PER, float>(a, value, reinterpret_cast<float*>(shared[wave]), lane, gap);
-      float most = -INFINITY;
+      unsigned long long open = open_groups<PER, float>(a, value, reinterpret_cast<float*>(shared[wave]), lane, gap);
       if (BIAS || graded) {
+        float most = -INFINITY;
 #pragma unroll
         for (int j = 0; j < PER; ++j)
           if (value[j] > -INFINITY) most = fmaxf(most, fabsf(value[j]));
         most = wave_max(most);
-        // two sums of two values; a gap to a group without experts is infinite, and a row without any has no order
-        settled = most == -INFINITY || gap > 8.f * kOff * (1.f + most);
+        // A gap between two sums of two values, each off by kOff (1 + most) and once rounded. One that could be
+        // of the other sign is decided in fp64; a gap to a group without experts is infinite.
+        if (most > -INFINITY && !(gap > 4.f * kOff * (1.f + most))) {
+          double v[PER], exact_gap;
+          exact_values<PER, BIAS>(a, l, b, top, v);
+          wave_lds_order();
+          open = open_groups<PER, double>(a, v, shared[wave], lane, exact_gap);
+        }
       }
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
