@@ -69,7 +69,8 @@ __global__ __launch_bounds__(kThreads) void expert_combine(CombineArgs a) {
   }
 }
 
-// One workgroup a token; a thread owns columns 8 threadIdx.x + 8 blockDim.x i
+// A workgroup takes up to eight slots of a token (fewer where tokens are few:
+// two tokens of 16 x 6712, 10.1 us in one each, UUU); a thread owns columns 8 threadIdx.x + 8 blockDim.x i
 // and keeps dout's in registers over the slots, whose rows of y are loaded
 // eight together. dout is read once (with a loop over the slots outside, and a
 // wait for each row, 4096 tokens of 8 x 7168 took 285 us, so 194: 1.0 GB at 5.1 TB/s). y passes the caches by and dy
@@ -95,13 +96,14 @@ __device__ __forceinline__ float lanes_sum(float v) {   // on lane 63, by DPP mo
 
 template <bool F32, bool DW>
 __global__ __launch_bounds__(kBackThreads) void expert_combine_backward(CombineBackwardArgs a) {
-  __shared__ float part[kBackThreads / kWave][kMaxTopK];
+  __shared__ float part[kBackThreads / kWave][kAhead];
   const int t = blockIdx.x, lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, k = a.top_k;
-  // slot s on lane s: its row (-1: none), whether dy's row is its own, its weight
+  const int s0 = blockIdx.y * a.slots, slots = min(a.slots, k - s0);
+  // slot s0 + s on lane s: its row (-1: none), whether dy's row is its own, its weight
   int row = -1, own = 0;
   float weight = 1.f;
-  if (lane < k) {
-    const size_t f = (size_t)t * k + lane;
+  if (lane < slots) {
+    const size_t f = (size_t)t * k + s0 + lane;
     row = a.rowpos[f];
     if (row < 0 || row >= a.rows) row = -1;
     if (row >= 0) {
@@ -109,63 +111,59 @@ __global__ __launch_bounds__(kBackThreads) void expert_combine_backward(CombineB
       if (a.weights) weight = a.weights[f];
     }
   }
-  for (int s0 = 0; s0 < k; s0 += kAhead) {
-    float dot[kAhead];
+  float dot[kAhead];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) dot[j] = 0.f;
-    for (int c = threadIdx.x * 8; c < a.hidden; c += blockDim.x * 8) {
-      u32x4_t v[kAhead];
-      if (DW) {
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          const int r = s0 + j < k ? __builtin_amdgcn_readlane(row, s0 + j) : -1;
-          if (r >= 0) v[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(a.y + (size_t)r * a.ldy + c));
-        }
-      }
-      float d[8];
-      if constexpr (F32) {
-        const f32x4_t* const p = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(a.dout) + (size_t)t * a.lddout + c);
-        const f32x4_t lo = p[0], hi = p[1];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          d[i] = lo[i];
-          d[4 + i] = hi[i];
-        }
-      } else {
-        unpack8(*reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(a.dout) + (size_t)t * a.lddout + c), d);
-      }
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        if (s0 + j >= k) break;
-        const int r = __builtin_amdgcn_readlane(row, s0 + j);
-        if (__builtin_amdgcn_readlane(own, s0 + j)) {
-          const float w = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(weight), s0 + j));
-          const u32x4_t o = {bf16_pair(w * d[0], w * d[1]), bf16_pair(w * d[2], w * d[3]), bf16_pair(w * d[4], w * d[5]),
-                             bf16_pair(w * d[6], w * d[7])};
-          __builtin_nontemporal_store(o, reinterpret_cast<u32x4_t*>(a.dy + (size_t)r * a.hidden + c));
-        }
-        if (DW && r >= 0) {
-          float f[8];
-          unpack8(v[j], f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) dot[j] = fmaf(d[i], f[i], dot[j]);
-        }
-      }
-    }
+  for (int j = 0; j < kAhead; ++j) dot[j] = 0.f;
+  for (int c = threadIdx.x * 8; c < a.hidden; c += blockDim.x * 8) {
+    u32x4_t v[kAhead];
     if (DW) {
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        const float sum = lanes_sum(dot[j]);
-        if (lane == kWave - 1 && s0 + j < k) part[wave][s0 + j] = sum;
+        const int r = __builtin_amdgcn_readlane(row, j);
+        if (r >= 0) v[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(a.y + (size_t)r * a.ldy + c));
+      }
+    }
+    float d[8];
+    if constexpr (F32) {
+      const f32x4_t* const p = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(a.dout) + (size_t)t * a.lddout + c);
+      const f32x4_t lo = p[0], hi = p[1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        d[i] = lo[i];
+        d[4 + i] = hi[i];
+      }
+    } else {
+      unpack8(*reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(a.dout) + (size_t)t * a.lddout + c), d);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int r = __builtin_amdgcn_readlane(row, j);
+      if (r < 0) continue;
+      if (__builtin_amdgcn_readlane(own, j)) {
+        const float w = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(weight), j));
+        const u32x4_t o = {bf16_pair(w * d[0], w * d[1]), bf16_pair(w * d[2], w * d[3]), bf16_pair(w * d[4], w * d[5]),
+                           bf16_pair(w * d[6], w * d[7])};
+        __builtin_nontemporal_store(o, reinterpret_cast<u32x4_t*>(a.dy + (size_t)r * a.hidden + c));
+      }
+      if (DW) {
+        float f[8];
+        unpack8(v[j], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dot[j] = fmaf(d[i], f[i], dot[j]);
       }
     }
   }
   if (!DW) return;
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) {
+    const float sum = lanes_sum(dot[j]);
+    if (lane == kWave - 1) part[wave][j] = sum;
+  }
   __syncthreads();
-  if ((int)threadIdx.x < k) {
+  if ((int)threadIdx.x < slots) {
     float sum = 0.f;
     for (int w = 0; w < (int)blockDim.x / kWave; ++w) sum += part[w][threadIdx.x];
-    a.dweights[(size_t)t * k + threadIdx.x] = sum;
+    a.dweights[(size_t)t * k + s0 + threadIdx.x] = sum;
   }
 }
 
@@ -182,10 +180,13 @@ hipError_t launch_expert_combine(const CombineArgs& a, bool f32, hipStream_t str
   return hipGetLastError();
 }
 
-hipError_t launch_expert_combine_backward(const CombineBackwardArgs& a, bool f32, hipStream_t stream) {
+hipError_t launch_expert_combine_backward(CombineBackwardArgs a, bool f32, hipStream_t stream) {
+  for (a.slots = kAhead; a.slots > 1 && (long long)a.tokens * ((a.top_k + a.slots - 1) / a.slots) < 256; a.slots /= 2) {}
   const int chunks = a.hidden / 8;
   const dim3 block(chunks >= kBackThreads ? kBackThreads : (chunks + kWave - 1) / kWave * kWave);
-  auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(a.tokens), block, 0, stream, a); };
+  auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(a.tokens, (a.top_k + a.slots - 1) / a.slots), block, 0, stream, a);
+  };
   if (f32) run(a.dweights ? expert_combine_backward<true, true> : expert_combine_backward<true, false>);
   else run(a.dweights ? expert_combine_backward<false, true> : expert_combine_backward<false, false>);
   return hipGetLastError();

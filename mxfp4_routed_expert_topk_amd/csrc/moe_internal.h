@@ -256,9 +256,10 @@ struct CombineBackwardArgs {
   uint16_t* dy;             // [rows, hidden] or null
   float* dweights;          // [tokens, top_k] or null
   int rows, tokens, top_k, hidden;
+  int slots = 0;            // of a workgroup (filled in by the launcher)
 };
 hipError_t launch_expert_combine(const CombineArgs& a, bool f32, hipStream_t stream);
-hipError_t launch_expert_combine_backward(const CombineBackwardArgs& a, bool f32, hipStream_t stream);
+hipError_t launch_expert_combine_backward(CombineBackwardArgs a, bool f32, hipStream_t stream);
 
 // Peak micro-benchmarks (probe.hip).  `sink` holds one float per workgroup
 // (grid <= kProbeSinkFloats).

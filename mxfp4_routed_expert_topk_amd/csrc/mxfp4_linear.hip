@@ -302,15 +302,15 @@ struct LinearShape {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, kWaves = WM * WN, kPerCU = PER_CU_, NX = NX_, NW = NW_;
   static constexpr int MI = BM / WM / 16, NJ = BN / WN / 16;
   static constexpr int kXBytes = BM * 128, kWBytes = BN * 64;
-  static constexpr int kX = BM / 8 / kWaves, kW = BN / 16 / kWaves, kWh = kW / 2;   // copies per wave: a stage's x, a unit's W
+  static constexpr int kX = BM / 8 / kWaves, kW = BN / 16 / kWaves;   // copies per wave: a stage's x, a unit's W
   static constexpr int kSmem = NX * kXBytes + NW * kWBytes;
   // copies and scale loads that a wave issues after a stage's x and before that stage starts
   static constexpr int kSc = (NJ + 3) / 4;   // loads of a unit's scales
-  static constexpr int kAfter = kWh + (NX - 2) * (kX + kWh) + kSc * (NX - 1) / 2;
-  static_assert(kX * kWaves * 8 == BM && kW * kWaves * 16 == BN && kW % 2 == 0 && kWaves % 2 == 0, "even split");
+  static constexpr int kAfter = (NX - 2) * kX + (kW + kSc) * (NX - 1) / 2;
+  static_assert(kX * kWaves * 8 == BM && kW * kWaves * 16 == BN && kWaves % 2 == 0, "even split");
   static_assert(kPerCU * kSmem <= 160 * 1024 && MI % 2 == 0 && NJ % 2 == 0, "rings fit");
-  static_assert(4 * (kX - 1) < 3 * (kX + kWh), "a stage's x before its scales");
-  static_assert(NX % 2 == 1 && 2 * NW >= NX + 2 && kAfter < 64, "W lands before x of its stage; vmcnt counts them");
+  static_assert(4 * (kX - 1) < 3 * (kX + kW), "a stage's x before its scales");
+  static_assert(NX % 2 == 1 && 2 * NW > NX + 1 && kAfter < 64, "W lands before x of its stage; vmcnt counts them");
 };
 
 template <class C, bool GATE, bool F32>
@@ -399,10 +399,12 @@ __device__ __forceinline__ void linear_tile(uint8_t* smem, const LinearArgs& a, 
 #pragma unroll
     for (int j = 0; j < C::NJ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  // The rings' fill, in the order that a stage's wait counts on, as if stages
+  // A unit's first stage issues its copies of W and its scales beside its x,
+  // so what is issued between a stage's x and its start does not depend on
+  // which of the two it is. The rings' fill keeps that order, as if stages
   // 1 - NX .. -1 had issued it (but for the scales of units before the first:
   // as many copies of the first W once more).
-  constexpr int kHalf = C::MI / 2, kM = kHalf * C::NJ, kWh = C::kWh, kG = C::kX + kWh;
+  constexpr int kHalf = C::MI / 2, kM = kHalf * C::NJ;
   constexpr int kUnits = (C::NX - 1) / 2;   // those stages' units
   unrolled<C::NW - 1 - kUnits>([&](auto u) {
 #pragma unroll
@@ -412,8 +414,10 @@ __device__ __forceinline__ void linear_tile(uint8_t* smem, const LinearArgs& a, 
     constexpr int v = decltype(vc)::value, u = C::NW - 1 - kUnits + v / 2;
 #pragma unroll
     for (int j = 0; j < C::kX; ++j) issue_x(smem + v * C::kXBytes, v, j);
+    if constexpr (v % 2 == 0) {
 #pragma unroll
-    for (int j = 0; j < kWh; ++j) issue_w(ring_w + u * C::kWBytes, u, v % 2 * kWh + j);
+      for (int j = 0; j < C::kW; ++j) issue_w(ring_w + u * C::kWBytes, u, j);
+    }
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (v % 2 == 0 && v < C::NX - 3) {
 #pragma unroll
@@ -507,11 +511,12 @@ __device__ __forceinline__ void linear_tile(uint8_t* smem, const LinearArgs& a, 
             });
         }
         // copies over the whole stage, x's first, then W's, then the scales
+        constexpr int kG = C::kX + (p ? 0 : C::kW);
         unrolled<kG>([&](auto cc) {
           constexpr int c = decltype(cc)::value;
           if constexpr (c * 4 * kM / kG == h * kM + m) {
             if constexpr (c < C::kX) issue_x(to_x, s + C::NX - 1, c);
-            else issue_w(to_w, u + C::NW - 1, p * kWh + c - C::kX);
+            else issue_w(to_w, u + C::NW - 1, c - C::kX);
           }
         });
         if constexpr (p == 0 && h == 3) {
@@ -614,7 +619,7 @@ hipError_t launch_tiles(const LinearArgs& a, bool gate, bool f32, hipStream_t st
 }
 
 using Linear256 = LinearShape<256, 256, 2, 4, 1, 3, 3>;
-using Linear128 = LinearShape<128, 128, 2, 2, 2, 3, 3>;
+using Linear128 = LinearShape<128, 128, 2, 4, 2, 3, 3>;
 
 }  // namespace
 

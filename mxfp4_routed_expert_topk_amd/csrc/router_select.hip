@@ -223,9 +223,8 @@ __device__ __forceinline__ bool there(int j) { return j < PER - 2; }
 // value can be off, so that no expert of the fp64 order is lost, and only the
 // packed ones get fp64 values: one exponential a lane for six. Groups are
 // graded in fp32 too where the grades at the border are further apart than
-// that, else in fp64. Left to the rounds are a bias on softmax scores (whose
-// sum would have to be fp64) and more than 64 experts that reach the bound
-// (many equal ones).
+// that, else in fp64. (Softmax scores need their sum in fp64 too.) Left to the
+// rounds are rows of which more than 64 experts reach the bound, many equal ones.
 template <int PER, bool BIAS, bool F32>
 __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectArgs a) {
   __shared__ double shared[kTokensPerBlock][PER * kWave];
@@ -251,7 +250,7 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
   if (softmax) {
     top = wave_max(top);
     if (top == -INFINITY) top = 0.f;   // every expert masked
-    if (!a.renormalize) {
+    if (!a.renormalize || BIAS) {
 #pragma unroll
       for (int j = 0; j < PER; ++j) total += quick_exp(l[j] - top);
       total = wave_sum(total);
@@ -260,105 +259,112 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
 
   // fp32 values: the logit, or an approximate score plus the bias
   float value[PER];
-  bool settled = !(BIAS && softmax);
-  // An approximate value v is off by less than kOff (1 + |v|): the exponential by (1.5 |x| + 2) u of itself, which
-  // 1 / (1 + e) passes on as 0.7 u at most, the reciprocal 2 u, two roundings and the sum's: 4.7 u + u |v|; 8 u taken.
-  constexpr float kOff = 0x1p-21f;
-  if (settled) {
-    const bool graded = limited && !BIAS && a.group_top == 2;
+  // An approximate value v is off by less than off (1 + |v|). The exponential: (2.5 |x| + 2) u of itself. A sigmoid
+  // passes that on as 0.7 u at most; its reciprocal 2 u, two roundings and the sum's: 4.7 u + u |v|; 8 u taken. A
+  // softmax score, at most 1: its own and its sum's exponentials (the sum's average |x| is at most ln 1024), the
+  // sum's 22 additions in a row, a quotient: 64 u taken.
+  const float off = BIAS && softmax ? 0x1p-18f : 0x1p-21f;
+  const bool graded = limited && !BIAS && a.group_top == 2;
+  const float share = 1.f / total;
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      value[j] = l[j];
-      if (BIAS || graded) {
-        const float small = quick_exp(softmax ? l[j] - top : -fabsf(l[j]));
-        const float s = softmax ? small : (l[j] < 0.f ? small : 1.f) * __builtin_amdgcn_rcpf(1.f + small);
-        value[j] = l[j] == -INFINITY || (BIAS && !(b[j] > -INFINITY)) ? -INFINITY : s + b[j];
+  for (int j = 0; j < PER; ++j) {
+    value[j] = l[j];
+    if (BIAS || graded) {
+      const float small = quick_exp(softmax ? l[j] - top : -fabsf(l[j]));
+      const float s = softmax ? (BIAS ? small * share : small) : (l[j] < 0.f ? small : 1.f) * __builtin_amdgcn_rcpf(1.f + small);
+      value[j] = l[j] == -INFINITY || (BIAS && !(b[j] > -INFINITY)) ? -INFINITY : s + b[j];
+    }
+  }
+  if (limited) {
+    float gap;
+    unsigned long long open = open_groups<PER, float>(a, value, reinterpret_cast<float*>(shared[wave]), lane, gap);
+    if (BIAS || graded) {
+      float most = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < PER; ++j)
+        if (value[j] > -INFINITY) most = fmaxf(most, fabsf(value[j]));
+      most = wave_max(most);
+      // A gap between two sums of two values, each off by off (1 + most) and once rounded. One that could be
+      // of the other sign is decided in fp64; a gap to a group without experts is infinite.
+      if (most > -INFINITY && !(gap > 4.f * off * (1.f + most))) {
+        double v[PER], exact_gap;
+        exact_values<PER, BIAS>(a, l, b, top, v);
+        wave_lds_order();
+        open = open_groups<PER, double>(a, v, shared[wave], lane, exact_gap);
       }
     }
-    if (limited) {
-      float gap;
-      unsigned long long open = open_groups<PER, float>(a, value, reinterpret_cast<float*>(shared[wave]), lane, gap);
-      if (BIAS || graded) {
-        float most = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < PER; ++j)
-          if (value[j] > -INFINITY) most = fmaxf(most, fabsf(value[j]));
-        most = wave_max(most);
-        // A gap between two sums of two values, each off by kOff (1 + most) and once rounded. One that could be
-        // of the other sign is decided in fp64; a gap to a group without experts is infinite.
-        if (most > -INFINITY && !(gap > 4.f * kOff * (1.f + most))) {
-          double v[PER], exact_gap;
-          exact_values<PER, BIAS>(a, l, b, top, v);
-          wave_lds_order();
-          open = open_groups<PER, double>(a, v, shared[wave], lane, exact_gap);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        if (graded) value[j] = l[j];
-        if (!group_open(a, open, lane + kWave * j)) value[j] = -INFINITY;
-      }
+    for (int j = 0; j < PER; ++j) {
+      if (graded) value[j] = l[j];
+      if (!group_open(a, open, lane + kWave * j)) value[j] = -INFINITY;
     }
   }
 
   int id = -1, slot = lane;   // this lane's expert, and its place among the chosen
   float x = -INFINITY;
+  float bound = -kMost;   // what a candidate reaches
+  if (PER > 1) {
+    float most = value[0];
+#pragma unroll
+    for (int j = 1; j < PER; ++j) most = fmaxf(most, value[j]);
+    const uint32_t key = most > -INFINITY ? order_key(most) : 0;
+    uint32_t kth = 0;   // of the lanes' largest keys, the k-th or a little less
+    for (int bit = 31; bit >= 0; --bit) {
+      const uint32_t next = kth | 1u << bit;
+      const int n = __popcll(__ballot(key >= next));
+      if (n >= k) kth = next;
+      if (n == k) break;
+    }
+    if (kth) bound = __uint_as_float(kth & 0x80000000u ? kth ^ 0x80000000u : ~kth);   // else fewer than k lanes have one
+    if (BIAS) {
+      bound -= 2.f * off * (1.f + fabsf(bound));
+      if (!(bound > -kMost)) bound = -kMost;   // NaN of an infinite bias: every expert is a candidate
+    }
+  }
+  int n = 0;
+  uint2* const packed = reinterpret_cast<uint2*>(shared[wave]);
+  wave_lds_order();   // the grades have been read
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const bool in = value[j] >= bound;
+    const unsigned long long mask = __ballot(in);
+    const int at = __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, n));
+    if (in) packed[at] = make_uint2(lane + kWave * j, __float_as_uint(l[j]));   // ids ascend; there is room for all
+    n += __popcll(mask);
+  }
+  wave_lds_order();
+  const bool settled = n <= kWave;
   if (settled) {
-    float bound = -kMost;   // what a candidate reaches
-    if (PER > 1) {
-      float most = value[0];
-#pragma unroll
-      for (int j = 1; j < PER; ++j) most = fmaxf(most, value[j]);
-      const uint32_t key = most > -INFINITY ? order_key(most) : 0;
-      uint32_t kth = 0;   // of the lanes' largest keys, the k-th or a little less
-      for (int bit = 31; bit >= 0; --bit) {
-        const uint32_t next = kth | 1u << bit;
-        const int n = __popcll(__ballot(key >= next));
-        if (n >= k) kth = next;
-        if (n == k) break;
-      }
-      if (kth) bound = __uint_as_float(kth & 0x80000000u ? kth ^ 0x80000000u : ~kth);   // else fewer than k lanes have one
-      if (BIAS) {
-        bound -= 2.f * kOff * (1.f + fabsf(bound));
-        if (!(bound > -kMost)) bound = -kMost;   // NaN of an infinite bias: every expert is a candidate
-      }
+    if (lane < n) {
+      const uint2 v = packed[lane];
+      id = (int)v.x;
+      x = __uint_as_float(v.y);
     }
-    int n = 0;
-    uint2* const packed = reinterpret_cast<uint2*>(shared[wave]);
-    wave_lds_order();   // the grades have been read
+    slot = 0;   // how many candidates rank before the lane's
+    if constexpr (BIAS) {
+      double score = 0.0;
+      if (softmax) {
+        double sum = 0.0;
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const bool in = value[j] >= bound;
-      const unsigned long long mask = __ballot(in);
-      const int at = __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, n));
-      if (in) packed[at] = make_uint2(lane + kWave * j, __float_as_uint(l[j]));   // ids ascend; there is room for all
-      n += __popcll(mask);
-    }
-    wave_lds_order();
-    settled = n <= kWave;
-    if (settled) {
-      if (lane < n) {
-        const uint2 v = packed[lane];
-        id = (int)v.x;
-        x = __uint_as_float(v.y);
-      }
-      slot = 0;   // how many candidates rank before the lane's
-      if constexpr (BIAS) {
-        const unsigned long long key = lane < n ? order_key(1.0 / (1.0 + exp(-(double)x)) + (double)a.bias[id]) : 0;
-        for (int s = 0; s < n; ++s) {
-          const unsigned long long other = (unsigned long long)(uint32_t)__builtin_amdgcn_readlane((int)(key >> 32), s) << 32 |
-                                           (uint32_t)__builtin_amdgcn_readlane((int)key, s);
-          slot += other > key || (other == key && s < lane);
-        }
+        for (int j = 0; j < PER; ++j) sum += exp((double)l[j] - (double)top);
+        score = exp((double)x - (double)top) * (1.0 / wave_sum(sum));
       } else {
-        const uint32_t high = order_key(x);
-        const unsigned long long key = (unsigned long long)high << 32 | (uint32_t)(kWave - lane);
-        for (int s = 0; s < n; ++s)
-          slot += ((unsigned long long)(uint32_t)__builtin_amdgcn_readlane((int)high, s) << 32 | (uint32_t)(kWave - s)) > key;
+        score = 1.0 / (1.0 + exp(-(double)x));
       }
-      if (lane >= n) slot = lane;   // an empty slot, if it is one
-      else if (slot >= k) id = -1;
+      const unsigned long long key = lane < n ? order_key(score + (double)a.bias[id]) : 0;
+      for (int s = 0; s < n; ++s) {
+        const unsigned long long other = (unsigned long long)(uint32_t)__builtin_amdgcn_readlane((int)(key >> 32), s) << 32 |
+                                         (uint32_t)__builtin_amdgcn_readlane((int)key, s);
+        slot += other > key || (other == key && s < lane);
+      }
+    } else {
+      const uint32_t high = order_key(x);
+      const unsigned long long key = (unsigned long long)high << 32 | (uint32_t)(kWave - lane);
+      for (int s = 0; s < n; ++s)
+        slot += ((unsigned long long)(uint32_t)__builtin_amdgcn_readlane((int)high, s) << 32 | (uint32_t)(kWave - s)) > key;
     }
+    if (lane >= n) slot = lane;   // an empty slot, if it is one
+    else if (slot >= k) id = -1;
   }
   if (!settled) {
     wave_lds_order();
