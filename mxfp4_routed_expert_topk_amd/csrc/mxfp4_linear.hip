@@ -365,8 +365,8 @@ __device__ __forceinline__ void linear_tile(uint8_t* smem, const LinearArgs& a, 
   // Scales: a lane loads the four bytes of a unit's blocks of one row, of the
   // wave's 16-row block lane / 16 (and 4 more, ..), and the lanes that multiply
   // that row take them from it. (A lane that loads its own rows' makes every
-  // load touch sixteen lines four times over, 64 clocks: 128 x 128 tiles of 128 rows 65 -> 60 us.) The
-  // matrix's last four bytes may start before the unit's and are moved down;
+  // load touch sixteen lines four times over, 64 clocks.) They are loaded two
+  // units ahead (one: 1024 rows of 4096 x 7168 take 62.8 us for 59.9). The matrix's last four bytes may start before the unit's and are moved down;
   // past K they are 0, so that codes there are finite whatever they are (x is 0).
   constexpr int kSc = C::kSc;
   const int scales = a.n * groups, last = max(scales - 4, 0);
@@ -378,9 +378,9 @@ __device__ __forceinline__ void linear_tile(uint8_t* smem, const LinearArgs& a, 
     const int b = wn * C::NJ + min(4 * i + q, C::NJ - 1);
     srow[i] = (min(c0 + 16 * (GATE ? b >> 1 : b) + rl, cols - 1) + (GATE && (b & 1) ? cols : 0)) * groups;
   }
-  uint32_t sc[C::NJ], next[kSc];
+  uint32_t sc[C::NJ], next[kSc], far[kSc];   // in use, of the next unit, of the one after it
   auto load_scale = [&](int i, int u) {
-    next[i] = __builtin_amdgcn_raw_buffer_load_b32(srsrc, min(srow[i] + 4 * u, last), 0, 0);
+    far[i] = __builtin_amdgcn_raw_buffer_load_b32(srsrc, min(srow[i] + 4 * u, last), 0, 0);
   };
   // the byte of lane quarter q's block of the unit's first stage in bits 7:0, of the second in 23:16
   auto take_scales = [&](int u) {
@@ -402,14 +402,24 @@ __device__ __forceinline__ void linear_tile(uint8_t* smem, const LinearArgs& a, 
   // A unit's first stage issues its copies of W and its scales beside its x,
   // so what is issued between a stage's x and its start does not depend on
   // which of the two it is. The rings' fill keeps that order, as if stages
-  // 1 - NX .. -1 had issued it (but for the scales of units before the first:
-  // as many copies of the first W once more).
+  // 1 - NX .. -1 had issued it.
   constexpr int kHalf = C::MI / 2, kM = kHalf * C::NJ;
   constexpr int kUnits = (C::NX - 1) / 2;   // those stages' units
   unrolled<C::NW - 1 - kUnits>([&](auto u) {
 #pragma unroll
     for (int j = 0; j < C::kW; ++j) issue_w(ring_w + u * C::kWBytes, u, j);
   });
+  if (scales >= 4) {
+#pragma unroll
+    for (int i = 0; i < kSc; ++i) load_scale(i, 0);
+  } else {   // one unit, byte by byte
+    uint32_t v = 0;
+    for (int g = 0; g < scales; ++g) v |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(srsrc, g, 0, 0) << (8 * g);
+#pragma unroll
+    for (int i = 0; i < kSc; ++i) far[i] = v;
+  }
+#pragma unroll
+  for (int i = 0; i < kSc; ++i) next[i] = far[i];
   unrolled<C::NX - 1>([&](auto vc) {
     constexpr int v = decltype(vc)::value, u = C::NW - 1 - kUnits + v / 2;
 #pragma unroll
@@ -419,18 +429,9 @@ __device__ __forceinline__ void linear_tile(uint8_t* smem, const LinearArgs& a, 
       for (int j = 0; j < C::kW; ++j) issue_w(ring_w + u * C::kWBytes, u, j);
     }
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (v % 2 == 0 && v < C::NX - 3) {
+    if constexpr (v % 2 == 0) {
 #pragma unroll
-      for (int j = 0; j < kSc; ++j) issue_w(ring_w, 0, 0);
-    } else if constexpr (v == C::NX - 3) {
-#pragma unroll
-      for (int j = 0; j < kSc; ++j) load_scale(j, 0);
-      if (scales < 4) {   // one unit, byte by byte
-        uint32_t v = 0;
-        for (int g = 0; g < scales; ++g) v |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(srsrc, g, 0, 0) << (8 * g);
-#pragma unroll
-        for (int j = 0; j < kSc; ++j) next[j] = v;
-      }
+      for (int j = 0; j < kSc; ++j) load_scale(j, max(2 - kUnits + v / 2, 0));
     }
     __builtin_amdgcn_sched_barrier(0);
   });
@@ -520,7 +521,13 @@ __device__ __forceinline__ void linear_tile(uint8_t* smem, const LinearArgs& a, 
           }
         });
         if constexpr (p == 0 && h == 3) {
-          unrolled<kSc>([&](auto b) { if constexpr (b * kM / kSc == m) load_scale(b, u + 1); });
+          unrolled<kSc>([&](auto b) {
+            if constexpr (b * kM / kSc == m) {
+              next[b] = far[b];
+              asm volatile("" : "+v"(next[b]));   // here and not earlier, where it would wait for them
+              load_scale(b, u + 2);
+            }
+          });
         }
         __builtin_amdgcn_sched_barrier(0);
       });
