@@ -166,6 +166,20 @@ def test_select_masks(dtype, score, renormalize, biased, groups):
     assert (ids[:2] == -1).all() and (w[:2] == 0).all()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [48, 128, 640])
+@pytest.mark.parametrize("groups", [{}, dict(num_groups=16, group_limit=5, group_top=2),
+                                    dict(num_groups=8, group_limit=7, group_top=1)])
+def test_select_extreme_biases(score, E, groups):
+    """Biases of the type's extremes and of no size, whose sums two by two pass fp32's range."""
+    rng = np.random.default_rng(E)
+    l = logits_of(rng, 6, E, F32)
+    l[4, : E // 2] = -INF
+    for values in ([-F32_MAX, F32_MAX], [-F32_MAX], [F32_MAX], [INF, -INF, 0.0], [INF, F32_MAX, -F32_MAX, 1e-45, -1e-45],
+                   [-F32_MAX, -F32_MAX, -F32_MAX, -INF, 0.25]):
+        check_select(l, 6, score, bias=rng.choice(values, E), **groups)
+
+
 @pytest.mark.parametrize("E,near", [(40, 40), (384, 30), (384, 384), (896, 60), (1024, 65)])
 @pytest.mark.parametrize("groups", [{}, dict(num_groups=8, group_limit=3, group_top=2),
                                     dict(num_groups=8, group_limit=4, group_top=1)])
@@ -489,6 +503,33 @@ def test_linear_beyond_32_bit_offsets():
     assert torch.equal(out[:, -2:], want) and want.any() and not out[:, :-2].any()
 
 
+def test_linear_gated_halves_far_apart():
+    """w3 starts 2 GiB behind w1."""
+    g = torch.Generator(device=dev()).manual_seed(2)
+    n, k = 1 << 18, 32768
+    codes = torch.zeros((n, k // 2), dtype=torch.uint8, device=dev())
+    scales = torch.full((n, k // 32), 121, dtype=torch.uint8, device=dev())
+    rows = [5, n // 2 - 1, n // 2 + 5, n - 1]
+    codes[rows] = torch.randint(0, 256, (4, k // 2), dtype=torch.uint8, device=dev(), generator=g)
+    for m in (1, 40):
+        x = torch.randint(-2, 3, (m, k), device=dev(), generator=g).to(BF)   # sums are exact in any order
+        out = moe.mxfp4_linear(x, codes, scales, gate=True, dtype=F32)
+        want = moe.mxfp4_linear(x, codes[rows].clone(), scales[:4].clone(), gate=True, dtype=F32)
+        assert torch.equal(out[:, [5, n // 2 - 1]], want) and want.any()
+        out[:, [5, n // 2 - 1]] = 0
+        assert not out.any()
+
+
+@pytest.mark.parametrize("m", [3, 40, 300])
+def test_linear_rows_as_far_apart_as_they_may_be(m):
+    rng = np.random.default_rng(m)
+    x = up(rng.standard_normal((m, 352)).astype(np.float32)).to(BF)
+    codes, scales = map(up, mx(rng, 200, 352))
+    wide = torch.empty((m, 1 << 20), dtype=BF, device=dev())[:, :352]
+    wide.copy_(x)
+    assert torch.equal(moe.mxfp4_linear(wide, codes, scales), moe.mxfp4_linear(x, codes, scales))
+
+
 # ------------------------------------------------------------------ combine
 def routes(rng, T, k, experts, resident):
     """(rowpos [T, k], perm [T k], valid) of random ids, as the layer's route stage sorts them."""
@@ -713,6 +754,24 @@ def test_other_stream():
     s.synchronize()
     for a, b in zip(got, want):
         assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_two_streams_at_once():
+    """The same calls on two streams, enqueued in turn, share no memory."""
+    calls, _ = some_calls()
+    others, _ = some_calls()
+    want = [tuple(t.clone() for t in c()) for c in calls]
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(5):
+        for a, b in zip(calls, others):
+            for s, c in zip(streams, (a, b)):
+                with torch.cuda.stream(s):
+                    got.append(tuple(t.clone() for t in c()))
+    torch.cuda.synchronize()
+    for i, res in enumerate(got):
+        assert all(torch.equal(p, q) for p, q in zip(res, want[i // 2 % len(want)])), i
 
 
 def test_stream_argument():
