@@ -597,11 +597,13 @@ __device__ __forceinline__ void linear_tile(uint8_t* smem, const LinearArgs& a, 
       }
     } else {
       using V = std::conditional_t<F32, float, uint16_t>;
-      for (int r = 0; r < 32 && mw + 16 * i + r < mrows; ++r)
-        for (int n = lane_; n < kBlocks * 16; n += kWave) {
-          const V v = *reinterpret_cast<const V*>(stg + r * kRowBytes + place(r, n / (16 / kSize)) + n % (16 / kSize) * kSize);
-          if (cw + n < ncols) static_cast<V*>(a.out)[(size_t)(m0 + mw + 16 * i + r) * cols + c0 + cw + n] = v;
-        }
+      constexpr int kWide = kBlocks * 16;
+#pragma unroll 8
+      for (int k = 0; k < 32 * kWide / kWave; ++k) {
+        const int r = (k * kWave + lane_) / kWide, n = (k * kWave + lane_) % kWide, m = mw + 16 * i + r;
+        const V v = *reinterpret_cast<const V*>(stg + r * kRowBytes + place(r, n / (16 / kSize)) + n % (16 / kSize) * kSize);
+        if (m < mrows && cw + n < ncols) static_cast<V*>(a.out)[(size_t)(m0 + m) * cols + c0 + cw + n] = v;
+      }
     }
     asm volatile("" ::: "memory");
   }
