@@ -671,8 +671,13 @@ hipError_t launch_mxfp4_linear(const LinearArgs& a, bool gate, bool f32, hipStre
   }
   // 256 x 256 tiles once they fill most of the CUs (K 7168 to 4096 columns: 2048
   // rows, 128 of them, 140 against 106 us; K 2048 to 7168: 2048 rows, 224 of them,
-  // 49 against 59).
-  if ((long long)((a.m + 255) / 256) * ((a.n + 255) / 256) >= 192) return launch_tiles<Linear256>(a, gate, f32, stream);
+  // 49 against 59), but not where a second round of them would run on few CUs (K 7168 to
+  // 4096: 4352 rows, 272 tiles, 282 against 247, 5120 rows, 320, 285 against 265, 5632
+  // rows, 352, 287 against 302; K 2048 to 7168: 2560 rows, 280 tiles, 88 against 76,
+  // 3000 rows, 336, 89.2 against 88.7, 3584 rows, 392, 93 against 103. With more rounds
+  // the last weighs less: 8448 rows of the first, 528 tiles, 433 against 449).
+  const long long large = (long long)((a.m + 255) / 256) * ((a.n + 255) / 256);
+  if (large >= 192 && !(large > 256 && large <= 336)) return launch_tiles<Linear256>(a, gate, f32, stream);
   return launch_tiles<Linear128>(a, gate, f32, stream);
 }
 
