@@ -26,6 +26,7 @@ __device__ __forceinline__ float load_logit(const void* p, size_t i) {
   return F32 ? static_cast<const float*>(p)[i] : __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
 }
 constexpr float kMost = 3.402823466e38f;   // fp32's largest number
+constexpr int kNanOrInf = 0x203;           // v_cmp_class: NaN or +inf
 // NaN as -inf, +inf as the largest number (as integers: what lies above it is infinite or NaN)
 __device__ __forceinline__ float cleaned(float l) {
   return l > -INFINITY ? __int_as_float(min(__float_as_int(l), __float_as_int(kMost))) : -INFINITY;
@@ -67,10 +68,11 @@ __device__ __forceinline__ uint32_t reduce32(uint32_t v, uint32_t none, F f) {
 __device__ __forceinline__ float wave_sum(float v) {
   return __uint_as_float(reduce32(__float_as_uint(v), 0u, [](uint32_t a, uint32_t b) { return __float_as_uint(__uint_as_float(a) + __uint_as_float(b)); }));
 }
-__device__ __forceinline__ float wave_max(float v) {
-  return __uint_as_float(reduce32(__float_as_uint(v), __float_as_uint(-INFINITY), [](uint32_t a, uint32_t b) { return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b))); }));
-}
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) { return reduce32(v, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; }); }
+__device__ __forceinline__ float wave_max(float v) {   // of no NaN
+  const uint32_t key = wave_max(order_key(v));
+  return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
 __device__ __forceinline__ double wave_sum(double v) { return wave_reduce(v, [](double a, double b) { return a + b; }); }
 
 // 2^(x log2 e) on the hardware's exponential: off by (|x| + 2) u of the value
@@ -126,11 +128,22 @@ __device__ __forceinline__ unsigned long long open_groups(const SelectArgs& a, c
   return __ballot(is && better < a.limit);
 }
 
-// Whether expert e's group is open.
-__device__ __forceinline__ bool group_open(const SelectArgs& a, unsigned long long open, int e) {
-  const int of = (int)(((float)e + 0.5f) * a.inverse);   // e / per, exact below 1024 experts
-  const uint32_t word = a.groups > 32 && of >= 32 ? (uint32_t)(open >> 32) : (uint32_t)open;
-  return word >> (of & 31) & 1;
+// Sets what is not of an open group to `none`: bit g of `open` becomes the sign
+// of the bits in reverse order, g to the left.
+template <int PER, class V>
+__device__ __forceinline__ void keep_open(const SelectArgs& a, unsigned long long open, int lane, V (&value)[PER],
+                                          V none = (V)-INFINITY) {
+  const float e = (float)lane + 0.5f;
+  auto group = [&](int j) { return (uint32_t)((e + (float)(kWave * j)) * a.inverse); };   // exact below 1024 experts
+  if (a.groups <= 32) {
+    const uint32_t bits = __brev((uint32_t)open);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) value[j] = (int32_t)(bits << (group(j) & 31)) < 0 ? value[j] : none;
+  } else {
+    const unsigned long long bits = __brevll(open);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) value[j] = (long long)(bits << (group(j) & 63)) < 0 ? value[j] : none;
+  }
 }
 
 // The fp64 values that groups are graded by (-inf: masked or switched off).
@@ -175,10 +188,7 @@ __device__ __forceinline__ int select_by_rounds(const SelectArgs& a, const float
   }
   if (a.groups > a.limit) {
     double gap;
-    const unsigned long long open = open_groups<PER, double>(a, v, graded, lane, gap);
-#pragma unroll
-    for (int j = 0; j < PER; ++j)
-      if (!group_open(a, open, lane + kWave * j)) key[j] = 0;
+    keep_open(a, open_groups<PER, double>(a, v, graded, lane, gap), lane, key, (Key)0);
   }
   int my_id = -1;
   for (int r = 0; r < a.top_k; ++r) {
@@ -236,16 +246,23 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
   const size_t row = (size_t)t * a.ld;
   float l[PER], b[PER];   // l: -inf where masked
   float top = -INFINITY;
+  bool special = false;
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const int e = lane + kWave * j;
     const bool in = there<PER>(j) || e < E;
     const int at = there<PER>(j) ? e : min(e, E - 1);   // loaded without a branch, which would wait
-    l[j] = cleaned(load_logit<F32>(a.logits, row + at));
+    l[j] = load_logit<F32>(a.logits, row + at);
     b[j] = BIAS ? a.bias[at] : 0.f;
     if (!in) l[j] = -INFINITY;
-    top = fmaxf(top, l[j]);
+    special |= __builtin_amdgcn_classf(l[j], kNanOrInf);
   }
+  if (__ballot(special)) {   // rare: one test a logit, where cleaning takes three instructions
+#pragma unroll
+    for (int j = 0; j < PER; ++j) l[j] = cleaned(l[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < PER; ++j) top = fmaxf(top, l[j]);
   float total = 0.f;   // of exp(l - top)
   if (softmax) {
     top = wave_max(top);
@@ -257,32 +274,45 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
     }
   }
 
-  // fp32 values: the logit, or an approximate score plus the bias
-  float value[PER];
+  // What experts are compared by: the logit, or an approximate score plus the bias, in fp32.
   // An approximate value v is off by less than off (1 + |v|). The exponential: (2.5 |x| + 2) u of itself. A sigmoid
   // passes that on as 0.7 u at most; its reciprocal 2 u, two roundings and the sum's: 4.7 u + u |v|; 8 u taken. A
   // softmax score, at most 1: its own and its sum's exponentials (the sum's average |x| is at most ln 1024), the
   // sum's 22 additions in a row, a quotient: 64 u taken.
   const float off = BIAS && softmax ? 0x1p-18f : 0x1p-21f;
-  const bool graded = limited && !BIAS && a.group_top == 2;
-  const float share = 1.f / total;
+  float value[PER];
+  auto put_scores = [&](float (&to)[PER], float share) {   // -inf for masked experts
+    auto put = [&](auto score) {
 #pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    value[j] = l[j];
-    if (BIAS || graded) {
-      const float small = quick_exp(softmax ? l[j] - top : -fabsf(l[j]));
-      const float s = softmax ? (BIAS ? small * share : small) : (l[j] < 0.f ? small : 1.f) * __builtin_amdgcn_rcpf(1.f + small);
-      value[j] = l[j] == -INFINITY || (BIAS && !(b[j] > -INFINITY)) ? -INFINITY : s + b[j];
-    }
+      for (int j = 0; j < PER; ++j) to[j] = l[j] == -INFINITY ? -INFINITY : score(l[j]);
+    };
+    if (softmax) put([&](float x) { return quick_exp(x - top) * share; });
+    else put([&](float x) { return __builtin_amdgcn_rcpf(1.f + quick_exp(-x)); });
+  };
+  if constexpr (BIAS) {
+    put_scores(value, 1.f / total);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) value[j] = fmaxf(value[j] + b[j], -INFINITY);   // (NaN, of an infinite bias or one that is NaN: -inf)
+  } else {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) value[j] = l[j];
   }
   if (limited) {
+    const bool graded = !BIAS && a.group_top == 2;   // by the scores' sums, though experts rank by logit
+    float grade[PER];
+    if (graded) {
+      put_scores(grade, 1.f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) grade[j] = value[j];
+    }
     float gap;
-    unsigned long long open = open_groups<PER, float>(a, value, reinterpret_cast<float*>(shared[wave]), lane, gap);
+    unsigned long long open = open_groups<PER, float>(a, grade, reinterpret_cast<float*>(shared[wave]), lane, gap);
     if (BIAS || graded) {
       float most = -INFINITY;
 #pragma unroll
       for (int j = 0; j < PER; ++j)
-        if (value[j] > -INFINITY) most = fmaxf(most, fabsf(value[j]));
+        if (grade[j] > -INFINITY) most = fmaxf(most, fabsf(grade[j]));
       most = wave_max(most);
       // A gap between two sums of two values, each off by off (1 + most) and once rounded. One that could be
       // of the other sign is decided in fp64; a gap to a group without experts is infinite.
@@ -293,11 +323,7 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
         open = open_groups<PER, double>(a, v, shared[wave], lane, exact_gap);
       }
     }
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      if (graded) value[j] = l[j];
-      if (!group_open(a, open, lane + kWave * j)) value[j] = -INFINITY;
-    }
+    keep_open(a, open, lane, value);
   }
 
   int id = -1, slot = lane;   // this lane's expert, and its place among the chosen
@@ -307,7 +333,8 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
     float most = value[0];
 #pragma unroll
     for (int j = 1; j < PER; ++j) most = fmaxf(most, value[j]);
-    const uint32_t key = most > -INFINITY ? order_key(most) : 0;
+    uint32_t key = most > -INFINITY ? order_key(most) : 0;
+    asm volatile("" : "+v"(key));   // (else the search does its selection in every step)
     uint32_t kth = 0;   // of the lanes' largest keys, the k-th or a little less
     for (int bit = 31; bit >= 0; --bit) {
       const uint32_t next = kth | 1u << bit;
@@ -328,8 +355,8 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
   for (int j = 0; j < PER; ++j) {
     const bool in = value[j] >= bound;
     const unsigned long long mask = __ballot(in);
-    const int at = __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, n));
-    if (in) packed[at] = make_uint2(lane + kWave * j, __float_as_uint(l[j]));   // ids ascend; there is room for all
+    const int at = __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+    if (in) packed[n + at] = make_uint2(lane + kWave * j, __float_as_uint(l[j]));   // ids ascend; there is room for all
     n += __popcll(mask);
   }
   wave_lds_order();
