@@ -230,10 +230,10 @@ __device__ __forceinline__ bool there(int j) { return j < PER - 2; }
 // for 16383 tokens of 896 experts, top-16, where this takes 17.5;
 // 4133 tokens of 384, top-8, sigmoid scores, a bias and four of eight groups: 19.2 and 8.7.
 //   With a bias the bound is taken in fp32 and lowered by twice what an fp32
-// value can be off, so that no expert of the fp64 order is lost, and only the
-// packed ones get fp64 values: one exponential a lane for six. Groups are
-// graded in fp32 too where the grades at the border are further apart than
-// that, else in fp64. (Softmax scores need their sum in fp64 too.) Left to the
+// value can be off, so that no expert of the fp64 order is lost. The packed ones
+// get fp64 values (one exponential a lane, softmax scores their sum in fp64
+// too) where two of them are closer than that. Groups are graded in fp32 too
+// where the grades at the border are further apart, else in fp64. Left to the
 // rounds are rows of which more than 64 experts reach the bound, many equal ones.
 template <int PER, bool BIAS, bool F32>
 __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectArgs a) {
@@ -369,20 +369,33 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
     }
     slot = 0;   // how many candidates rank before the lane's
     if constexpr (BIAS) {
-      double score = 0.0;
-      if (softmax) {
-        double sum = 0.0;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) sum += exp((double)l[j] - (double)top);
-        score = exp((double)x - (double)top) * (1.0 / wave_sum(sum));
-      } else {
-        score = 1.0 / (1.0 + exp(-(double)x));
-      }
-      const unsigned long long key = lane < n ? order_key(score + (double)a.bias[id]) : 0;
+      // In fp32 first, which settles the order unless two values are closer than both can be off.
+      float v = softmax ? quick_exp(x - top) * (1.f / total) : __builtin_amdgcn_rcpf(1.f + quick_exp(-x));
+      v = lane < n ? v + a.bias[id] : -INFINITY;
+      const float near = 4.f * off * (1.f + fabsf(v));
+      int close = 0;   // itself, and others
       for (int s = 0; s < n; ++s) {
-        const unsigned long long other = (unsigned long long)(uint32_t)__builtin_amdgcn_readlane((int)(key >> 32), s) << 32 |
-                                         (uint32_t)__builtin_amdgcn_readlane((int)key, s);
-        slot += other > key || (other == key && s < lane);
+        const float other = at_lane(v, s);
+        slot += other > v;
+        close += !(fabsf(other - v) > near);
+      }
+      if (__ballot(lane < n && close > 1)) {
+        slot = 0;
+        double score = 0.0;
+        if (softmax) {
+          double sum = 0.0;
+#pragma unroll
+          for (int j = 0; j < PER; ++j) sum += exp((double)l[j] - (double)top);
+          score = exp((double)x - (double)top) * (1.0 / wave_sum(sum));
+        } else {
+          score = 1.0 / (1.0 + exp(-(double)x));
+        }
+        const unsigned long long key = lane < n ? order_key(score + (double)a.bias[id]) : 0;
+        for (int s = 0; s < n; ++s) {
+          const unsigned long long other = (unsigned long long)(uint32_t)__builtin_amdgcn_readlane((int)(key >> 32), s) << 32 |
+                                           (uint32_t)__builtin_amdgcn_readlane((int)key, s);
+          slot += other > key || (other == key && s < lane);
+        }
       }
     } else {
       const uint32_t high = order_key(x);
