@@ -227,8 +227,9 @@ __device__ __forceinline__ bool there(int j) { return j < PER - 2; }
 // ballots, bounds the k-th largest of all from below; what reaches it, about
 // k + 2 experts, is packed to one a lane, ordered exactly and ranked by
 // comparison with every other. k rounds of the best over the wave took 80 us
-// for 16383 tokens of 896 experts, top-16, where this takes 17.5;
-// 4133 tokens of 384, top-8, sigmoid scores, a bias and four of eight groups: 19.2 and 8.7.
+// for 16383 tokens of 896 experts, top-16, where this takes 16.1;
+// 4133 tokens of 384, top-8, sigmoid scores, a bias and four of eight groups: 19.2 and 7.6. Most of it is the
+// issue of vector instructions (74 and 84 % of the SIMDs' time at 450 and 740 a wave; now fewer).
 //   With a bias the bound is taken in fp32 and lowered by twice what an fp32
 // value can be off, so that no expert of the fp64 order is lost. The packed ones
 // get fp64 values (one exponential a lane, softmax scores their sum in fp64
@@ -328,38 +329,59 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
 
   int id = -1, slot = lane;   // this lane's expert, and its place among the chosen
   float x = -INFINITY;
-  float bound = -kMost;   // what a candidate reaches
-  if (PER > 1) {
+  // What a candidate reaches, from a key that k values reach.
+  auto bound_of = [&](uint32_t key) {
+    float v = __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+    if (BIAS) v -= 2.f * off * (1.f + fabsf(v));
+    return v > -kMost ? v : -kMost;   // (NaN of an infinite bias: every expert is a candidate)
+  };
+  float bound = -kMost;
+  uint32_t kth = 0;   // of the lanes' largest keys, the k-th or a little less; 0: fewer than k lanes have one
+  // One logit a lane may all be candidates: without a search up to 16 experts (65536 tokens, top-8: 16 experts
+  // 19.4 us without one and 19.7 with, 32 25.8 and 20.8, 64 40 and 22).
+  if (PER > 1 || E > 16) {
     float most = value[0];
 #pragma unroll
     for (int j = 1; j < PER; ++j) most = fmaxf(most, value[j]);
     uint32_t key = most > -INFINITY ? order_key(most) : 0;
     asm volatile("" : "+v"(key));   // (else the search does its selection in every step)
-    uint32_t kth = 0;   // of the lanes' largest keys, the k-th or a little less
     for (int bit = 31; bit >= 0; --bit) {
       const uint32_t next = kth | 1u << bit;
       const int n = __popcll(__ballot(key >= next));
       if (n >= k) kth = next;
       if (n == k) break;
     }
-    if (kth) bound = __uint_as_float(kth & 0x80000000u ? kth ^ 0x80000000u : ~kth);   // else fewer than k lanes have one
-    if (BIAS) {
-      bound -= 2.f * off * (1.f + fabsf(bound));
-      if (!(bound > -kMost)) bound = -kMost;   // NaN of an infinite bias: every expert is a candidate
-    }
+    if (kth) bound = bound_of(kth);
   }
-  int n = 0;
+  int n;
   uint2* const packed = reinterpret_cast<uint2*>(shared[wave]);
   wave_lds_order();   // the grades have been read
+  for (bool again = false;; again = true) {
+    n = 0;
 #pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    const bool in = value[j] >= bound;
-    const unsigned long long mask = __ballot(in);
-    const int at = __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
-    if (in) packed[n + at] = make_uint2(lane + kWave * j, __float_as_uint(l[j]));   // ids ascend; there is room for all
-    n += __popcll(mask);
+    for (int j = 0; j < PER; ++j) {
+      const bool in = value[j] >= bound;
+      const unsigned long long mask = __ballot(in);
+      const int at = __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+      if (in) packed[n + at] = make_uint2(lane + kWave * j, __float_as_uint(l[j]));   // ids ascend; there is room for all
+      n += __popcll(mask);
+    }
+    wave_lds_order();
+    if (PER == 1 || n <= kWave || again || !kth) break;
+    // More than a wave holds (top-32 of 1024: few rows of a thousand, but the rounds for them
+    // were the kernel's time, 4096 tokens 20 to 29 us for 12 to 14): a higher bound from a search over every value, until k and no more than the wave has reach it.
+    for (int bit = 31; bit >= 0; --bit) {
+      const uint32_t next = kth | 1u << bit;
+      if (next == kth) continue;
+      const float reach = __uint_as_float(next & 0x80000000u ? next ^ 0x80000000u : ~next);
+      n = 0;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) n += __popcll(__ballot(value[j] >= reach));
+      if (n >= k) kth = next;
+      if (n >= k && n < kWave - 8) break;
+    }
+    bound = bound_of(kth);
   }
-  wave_lds_order();
   const bool settled = n <= kWave;
   if (settled) {
     if (lane < n) {

@@ -214,6 +214,24 @@ def test_select_of_few_lanes_with_experts():
             check_select(up(l), 32, score, bias=bias, num_groups=2, group_limit=1, group_top=2)
 
 
+@pytest.mark.parametrize("E,k", [(1024, 32), (896, 32), (520, 30), (128, 32)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_select_where_the_best_share_lanes(E, k, score):
+    """Experts above all others sit 64 apart, several to a lane, and more than 64 experts lie above the
+    k-th of the lanes' best."""
+    rng = np.random.default_rng(E)
+    l = rng.standard_normal((5, E)).astype(np.float32)
+    for t, lanes in enumerate((k - 1, k - 2, 12, 8, 20)):
+        e = np.arange(E)
+        l[t, e % 64 < lanes] += 6.0
+    l[4] = l[4].round(1)   # many equal ones
+    for dtype in (F32, BF):
+        check_select(up(l).to(dtype), k, score)
+        check_select(up(l).to(dtype), k, score, bias=rng.standard_normal(E) * 0.01)
+        check_select(up(l).to(dtype), k, score, bias=rng.choice([0.0, INF, -INF], E, p=[0.5, 0.3, 0.2]))
+    check_select(up(l), k // 2, score, bias=rng.standard_normal(E) * 0.01, num_groups=2, group_limit=1, group_top=2)
+
+
 def test_select_keeps_scores_that_underflow():
     """Renormalised weights of experts that only the bias selects: their softmax is below
     fp32's range, the ratio is not."""
