@@ -627,8 +627,11 @@ hipError_t launch_tiles(const LinearArgs& a, bool gate, bool f32, hipStream_t st
   return hipGetLastError();
 }
 
+// Four waves of 64 x 64 for the smaller tile: in eight of 64 x 32, which read x from
+// LDS twice as often, 1900 rows of 4096 x 7168 take 109 us for 102, up to 300 rows the
+// same. (Eight of 128 x 64 for the larger one: four of 128 x 128 take 227 for 168.)
 using Linear256 = LinearShape<256, 256, 2, 4, 1, 3, 3>;
-using Linear128 = LinearShape<128, 128, 2, 4, 2, 3, 3>;
+using Linear128 = LinearShape<128, 128, 2, 2, 2, 3, 3>;
 
 }  // namespace
 
@@ -640,8 +643,8 @@ hipError_t launch_mxfp4_linear(const LinearArgs& a, bool gate, bool f32, hipStre
   // (2048 in the form for up to 16 rows).
   const bool streams = (long long)a.n * groups >= 4 && (!gate || (long long)(a.n / 2) * groups * 16 < (1ll << 31));
   // Up to 4096 blocks it beats the 128 x 128 tiles, over a long K up to 8192 (K 7168
-  // to 4096 columns: 512 rows, 8192 blocks, 43 against 60 us, 1024 rows 81 against
-  // 61; K 2048 to 7168: 128 rows, 3584 blocks, 11.8 against 19.7, 256 rows 20.3
+  // to 4096 columns: 512 rows, 8192 blocks, 43 against 58 us, 1024 rows 81 against
+  // 59; K 2048 to 7168: 128 rows, 3584 blocks, 11.8 against 19.7, 256 rows 20.3
   // against 19.7; K 512 to 1024: 2048 rows, 8192 blocks, 11.0 against 7.8).
   if (streams && blocks <= (a.k > 4096 ? 8192 : 4096) && (groups <= 512 || a.m <= 16)) {
     if (groups > 512) return launch_rows<1, 1, 8, 3, 4, 2048>(a, gate, f32, stream);
@@ -670,14 +673,14 @@ hipError_t launch_mxfp4_linear(const LinearArgs& a, bool gate, bool f32, hipStre
     return launch_rows<4, 4, 4, 1, 16, 512>(a, gate, f32, stream);
   }
   // 256 x 256 tiles once they fill most of the CUs (K 7168 to 4096 columns: 2048
-  // rows, 128 of them, 140 against 106 us; K 2048 to 7168: 2048 rows, 224 of them,
-  // 49 against 59), but not where a second round of them would run on few CUs (K 7168 to
-  // 4096: 4352 rows, 272 tiles, 282 against 247, 5120 rows, 320, 285 against 265, 5632
-  // rows, 352, 287 against 302; K 2048 to 7168: 2560 rows, 280 tiles, 88 against 76,
-  // 3000 rows, 336, 89.2 against 88.7, 3584 rows, 392, 93 against 103. With more rounds
-  // the last weighs less: 8448 rows of the first, 528 tiles, 433 against 449).
+  // rows, 128 of them, 140 against 99 us, 2560 rows, 160, 141 against 143; K 2048 to 7168:
+  // 1500 rows, 168 of them, 44.4 against 44.7, 1792 rows, 196, 44 against 55), but not where
+  // a second round of them would run on few CUs (K 7168 to 4096: 4352 rows, 272 tiles, 278
+  // against 230, 5632 rows, 352, 282 against 275, 6000 rows, 384, 284 against 285; K 2048 to
+  // 7168: 2560 rows, 280 tiles, 86 against 69, 3000 rows, 336, 87 against 82, 3584 rows, 392,
+  // 88 against 96). With more rounds the last weighs less.
   const long long large = (long long)((a.m + 255) / 256) * ((a.n + 255) / 256);
-  if (large >= 192 && !(large > 256 && large <= 336)) return launch_tiles<Linear256>(a, gate, f32, stream);
+  if (large >= 160 && !(large > 256 && large <= 352)) return launch_tiles<Linear256>(a, gate, f32, stream);
   return launch_tiles<Linear128>(a, gate, f32, stream);
 }
 

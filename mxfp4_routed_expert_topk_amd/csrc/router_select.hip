@@ -229,7 +229,7 @@ __device__ __forceinline__ bool there(int j) { return j < PER - 2; }
 // comparison with every other. k rounds of the best over the wave took 80 us
 // for 16383 tokens of 896 experts, top-16, where this takes 16.1;
 // 4133 tokens of 384, top-8, sigmoid scores, a bias and four of eight groups: 19.2 and 7.6. Most of it is the
-// issue of vector instructions (74 and 84 % of the SIMDs' time at 450 and 740 a wave; now fewer).
+// issue of vector instructions (330 and 560 a wave, 70 % of the SIMDs' time).
 //   With a bias the bound is taken in fp32 and lowered by twice what an fp32
 // value can be off, so that no expert of the fp64 order is lost. The packed ones
 // get fp64 values (one exponential a lane, softmax scores their sum in fp64
