@@ -52,7 +52,8 @@ EXPORTS = ("moe_mxfp4_query_sizes", "moe_mxfp4_plan", "moe_mxfp4_forward", "moe_
            "moe_router_topk", "moe_mxfp4_quantize", "moe_mxfp4_dequantize", "moe_mxfp4_matmul",
            "moe_grouped_matmul", "moe_grouped_matmul_backward", "moe_grouped_matmul_workspace",
            "moe_grouped_matmul_backward_workspace", "moe_router_select", "moe_router_select_backward",
-           "moe_mxfp4_linear", "moe_expert_combine", "moe_expert_combine_backward", "moe_probe_memory", "moe_probe_mfma", "moe_probe_mfma_f8f4_blocks",
+           "moe_mxfp4_linear", "moe_expert_combine", "moe_expert_combine_backward",
+           "moe_probe_memory", "moe_probe_mfma", "moe_probe_mfma_f8f4_blocks",
            "moe_mxfp4_set_stage_events",
            "moe_mxfp4_destroy", "moe_mxfp4_last_error")
 _STATUS_FNS = tuple(n for n in EXPORTS if n not in ("moe_mxfp4_destroy", "moe_mxfp4_last_error") and not n.endswith("_workspace"))

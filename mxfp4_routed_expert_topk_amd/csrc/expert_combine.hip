@@ -70,11 +70,12 @@ __global__ __launch_bounds__(kThreads) void expert_combine(CombineArgs a) {
 }
 
 // A workgroup takes up to eight slots of a token (fewer where tokens are few:
-// two tokens of 16 x 6712, 10.1 us in one each, 4.4); a thread owns columns 8 threadIdx.x + 8 blockDim.x i
-// and keeps dout's in registers over the slots, whose rows of y are loaded
-// eight together. dout is read once (with a loop over the slots outside, and a
-// wait for each row, 4096 tokens of 8 x 7168 took 285 us, so 194: 1.0 GB at 5.1 TB/s). y passes the caches by and dy
-// too (206 and 208 us with plain loads or stores).
+// two tokens of 16 x 6712, 10.1 us in one each, 4.4); a thread owns columns
+// 8 threadIdx.x + 8 blockDim.x i and keeps dout's in registers over the slots,
+// whose rows of y are loaded eight together. dout is read once (with a loop
+// over the slots outside, and a wait for each row, 4096 tokens of 8 x 7168 took
+// 285 us, so 194: 1.0 GB at 5.1 TB/s). y passes the caches by and dy too (206
+// and 208 us with plain loads or stores).
 // A row of dy belongs to the route that perm names alone, whatever rowpos
 // holds, so no two workgroups write one.
 //   dweights: a thread's products in the order of its columns, then the wave's

@@ -366,8 +366,9 @@ __device__ __forceinline__ void linear_tile(uint8_t* smem, const LinearArgs& a, 
   // wave's 16-row block lane / 16 (and 4 more, ..), and the lanes that multiply
   // that row take them from it. (A lane that loads its own rows' makes every
   // load touch sixteen lines four times over, 64 clocks.) They are loaded two
-  // units ahead (one: 1024 rows of 4096 x 7168 take 62.8 us for 59.9). The matrix's last four bytes may start before the unit's and are moved down;
-  // past K they are 0, so that codes there are finite whatever they are (x is 0).
+  // units ahead (one: 1024 rows of 4096 x 7168 take 62.8 us for 59.9). The
+  // matrix's last four bytes may start before the unit's and are moved down; past
+  // K they are 0, so that codes there are finite whatever they are (x is 0).
   constexpr int kSc = C::kSc;
   const int scales = a.n * groups, last = max(scales - 4, 0);
   const __amdgpu_buffer_rsrc_t srsrc =

@@ -1,7 +1,8 @@
 // C entries of the operators beside the layer (MXFP4 quantiser and products,
 // grouped products, scored router, experts' combine): argument checks before
-// any launch, then one enqueue (two or three where a long sum is split).  Nothing here allocates or synchronises, so every call
-// may be captured in a graph.
+// any launch, then one enqueue (two or three where a long sum is split).
+// Nothing here allocates or synchronises, so every call may be captured in a
+// graph.
 #include <hip/hip_runtime.h>
 
 #include <cmath>

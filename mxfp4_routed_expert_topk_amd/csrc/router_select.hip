@@ -66,9 +66,13 @@ __device__ __forceinline__ uint32_t reduce32(uint32_t v, uint32_t none, F f) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, kWave - 1);
 }
 __device__ __forceinline__ float wave_sum(float v) {
-  return __uint_as_float(reduce32(__float_as_uint(v), 0u, [](uint32_t a, uint32_t b) { return __float_as_uint(__uint_as_float(a) + __uint_as_float(b)); }));
+  return __uint_as_float(reduce32(__float_as_uint(v), 0u, [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
 }
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) { return reduce32(v, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; }); }
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  return reduce32(v, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
 __device__ __forceinline__ float wave_max(float v) {   // of no NaN
   const uint32_t key = wave_max(order_key(v));
   return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
@@ -293,7 +297,7 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
   if constexpr (BIAS) {
     put_scores(value, 1.f / total);
 #pragma unroll
-    for (int j = 0; j < PER; ++j) value[j] = fmaxf(value[j] + b[j], -INFINITY);   // (NaN, of an infinite bias or one that is NaN: -inf)
+    for (int j = 0; j < PER; ++j) value[j] = fmaxf(value[j] + b[j], -INFINITY);   // (NaN, by the bias: -inf)
   } else {
 #pragma unroll
     for (int j = 0; j < PER; ++j) value[j] = l[j];
@@ -368,8 +372,9 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
     }
     wave_lds_order();
     if (PER == 1 || n <= kWave || again || !kth) break;
-    // More than a wave holds (top-32 of 1024: few rows of a thousand, but the rounds for them
-    // were the kernel's time, 4096 tokens 20 to 29 us for 12 to 14): a higher bound from a search over every value, until k and no more than the wave has reach it.
+    // More than a wave holds (top-32 of 1024: few rows of a thousand, but the rounds for them were the kernel's
+    // time, 4096 tokens 20 to 29 us for 12 to 14): a higher bound from a search over every value, until k and no
+    // more than the wave has reach it.
     for (int bit = 31; bit >= 0; --bit) {
       const uint32_t next = kth | 1u << bit;
       if (next == kth) continue;
