@@ -101,7 +101,8 @@ __device__ __forceinline__ void linear_rows_block(uint8_t* smem, uint32_t* scale
     xoff[t] = 4 * t + q < mrows ? (uint32_t)((4 * t + q) * a.ldx * 2) + 16 * xpiece(t) : kPastEnd;
   uint8_t* const ring = smem + wave * DEPTH * kPlace;
   // W's copies: lane -> row lane / 4, piece lane % 4 in its place. With a gate, w1
-  // and w3 have a resource each, but one reaches both with RB 1 (2^31 bytes at most).
+  // and w3 have a resource each, but with RB 1 one reaches both, from w1's first row of the
+  // block to the end of w3's eighth: (n / 2 + 8) pitch bytes, which the launcher keeps below 2^31.
   const uint32_t pitch = (uint32_t)groups * 16;
   constexpr int kHalves = GATE && RB > 1 ? 2 : 1;
   const int wpiece = (lane & 3) ^ (2 * (lane >> 5));
@@ -640,9 +641,10 @@ hipError_t launch_mxfp4_linear(const LinearArgs& a, bool gate, bool f32, hipStre
   const int groups = a.k / 32;
   const long long mb = (a.m + 15) / 16, blocks = mb * ((a.n + 15) / 16);   // 16 x 16 outputs, gated ones counted twice
   // The streaming kernel reads scales four at a time and reaches both halves
-  // of a gated matrix with 32-bit offsets; its rows of W hold up to 512 scales
-  // (2048 in the form for up to 16 rows).
-  const bool streams = (long long)a.n * groups >= 4 && (!gate || (long long)(a.n / 2) * groups * 16 < (1ll << 31));
+  // of a gated matrix from one address: the eight rows of w3 end (n / 2 + 8)
+  // rows behind w1's first, within a resource of 2^31 - 1 bytes. Its rows of W hold
+  // up to 512 scales (2048 in the form for up to 16 rows).
+  const bool streams = (long long)a.n * groups >= 4 && (!gate || (a.n / 2 + 8ll) * groups * 16 < (1ll << 31));
   // Up to 4096 blocks it beats the 128 x 128 tiles, over a long K up to 8192 (K 7168
   // to 4096 columns: 512 rows, 8192 blocks, 43 against 58 us, 1024 rows 81 against
   // 59; K 2048 to 7168: 128 rows, 3584 blocks, 11.8 against 19.7, 256 rows 20.3

@@ -538,6 +538,28 @@ def test_linear_gated_halves_far_apart():
         assert not out.any()
 
 
+def test_linear_gated_halves_at_the_border_of_32_bit_offsets():
+    """w3 starts a few rows less than 2 GiB behind w1: the last size whose rows of w3 the streaming kernel
+    reaches from w1's (131054), the first that it does not and the last below 2 GiB."""
+    g = torch.Generator(device=dev()).manual_seed(3)
+    k = 65536
+    codes = torch.zeros((131070, k // 2), dtype=torch.uint8, device=dev())
+    scales = torch.full((131070, k // 32), 121, dtype=torch.uint8, device=dev())
+    for n in (131054, 131056, 131070):
+        half = n // 2
+        cols = [*range(16), 32767, *range(half - 9, half)]       # every row of the first and the last workgroups
+        rows = cols + [half + c for c in cols]
+        codes[rows] = torch.randint(0, 256, (len(rows), k // 2), dtype=torch.uint8, device=dev(), generator=g)
+        for m in (1, 3, 16):
+            x = torch.randint(-2, 3, (m, k), device=dev(), generator=g).to(BF)   # sums are exact in any order
+            out = moe.mxfp4_linear(x, codes[:n], scales[:n], gate=True, dtype=F32)
+            want = moe.mxfp4_linear(x, codes[rows].clone(), scales[:len(rows)].clone(), gate=True, dtype=F32)
+            assert want.any(0).all() and torch.equal(out[:, cols], want), (n, m)
+            out[:, cols] = 0
+            assert not out.any(), (n, m)
+        codes[rows] = 0
+
+
 @pytest.mark.parametrize("m", [3, 40, 300])
 def test_linear_rows_as_far_apart_as_they_may_be(m):
     rng = np.random.default_rng(m)
