@@ -435,6 +435,30 @@ def test_linear_of_real_values(m, n, k, gate, dtype):
     assert (np.abs(f64(got) - y) <= tol).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("m", [4, 40, 70000, 100000])
+def test_linear_gate_far_below_zero(m, dtype):
+    """Gates whose exp(-g) passes fp32's range and up to it, times values that bring the product back into
+    it. W's rows have one unit weight each, so g and u are x's first two columns, exactly."""
+    g = [-89.0, -100.0, -88.5, -103.0, -104.0, -85.0, -87.5, -90.0, -95.0, -110.0, -120.0, -150.0, -176.0,
+         -63.75, -64.0, -64.5, -20.0, -1.0, -0.0, 0.0, 1.0, 30.0, 88.0, 89.0, 200.0, 1e30, -1e30]
+    u = [-2.0 ** 127, 2.0 ** 100, 2.0 ** 60, -3.0, 1.0]
+    pairs = np.array([(a, b) for a in g for b in u if a < 0 or abs(a * b) < 2.0 ** 127])
+    x = np.zeros((m, 32), np.float32)
+    x[:, :2] = pairs[np.arange(m) % len(pairs)]
+    codes = np.zeros((8, 16), np.uint8)
+    codes[:4, 0], codes[4:, 0] = 0x02, 0x20        # 1 in column 0 of w1's rows, in column 1 of w3's
+    xb = up(x).to(BF)
+    got = moe.mxfp4_linear(xb, up(codes), up(np.full((8, 1), 127, np.uint8)), gate=True, dtype=dtype)
+    a, b = f64(xb)[:, 0], f64(xb)[:, 1]
+    e = np.exp(-np.abs(a))
+    want = (a * np.where(a < 0, e, 1.0) / (1.0 + e) * b)[:, None]
+    # two exponentials of g / 2, 2 u and their arguments' |g| / 2 u each, three products; below g = -174 the
+    # exponential is subnormal: twice 2^-150 off, times |g u exp(g / 2)| < 2^8; bf16's own subnormals: 2^-134
+    tol = (np.abs(a) + 7)[:, None] * U * np.abs(want) + 2.0 ** -141
+    assert (np.abs(f64(got) - want) <= tol + half_step(got) * (np.abs(want) + tol) + (2.0 ** -134 if dtype == BF else 0)).all()
+
+
 def test_linear_takes_every_scale_byte():
     """Weights 2^-128 .. 6 2^127 and NaN, exact where the product is: one column a byte."""
     codes = np.tile(np.arange(256, dtype=np.uint8).reshape(16, 16), (16, 1))   # every code pair in each block of 16 rows
