@@ -13,6 +13,7 @@
 // the exponential's last bit.
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "moe_internal.h"
 
@@ -97,11 +98,11 @@ __device__ __forceinline__ double at_lane(double v, int lane) {
   return __longlong_as_double((long long)((unsigned long long)hi << 32 | (uint32_t)__builtin_amdgcn_readlane((int)u, lane)));
 }
 
-// The groups that stay (bit g), from each expert's value (-INFINITY: none).
+// The groups that stay (bit g), from each expert's value over `total` (-INFINITY: none).
 // gap: what separates the last that stays from the first that does not.
 template <int PER, class V>
 __device__ __forceinline__ unsigned long long open_groups(const SelectArgs& a, const V (&value)[PER], V* graded, int lane,
-                                                          V& gap) {
+                                                          V& gap, double total = 1.0) {
 #pragma unroll
   for (int j = 0; j < PER; ++j) graded[lane + kWave * j] = value[j];
   wave_lds_order();
@@ -117,6 +118,10 @@ __device__ __forceinline__ unsigned long long open_groups(const SelectArgs& a, c
     const V f = __shfl_xor(first, off, kWave), s = __shfl_xor(second, off, kWave);
     second = max(min(first, f), max(second, s));
     first = max(first, f);
+  }
+  if constexpr (std::is_same_v<V, double>) {   // the order of the values is theirs before it too
+    first /= total;
+    second /= total;
   }
   const V sum = a.group_top == 2 && second > -INFINITY ? first + second : first;
   const V grade = __shfl(sum, lane << a.side & (kWave - 1), kWave);   // group g on lane g
@@ -150,10 +155,13 @@ __device__ __forceinline__ void keep_open(const SelectArgs& a, unsigned long lon
   }
 }
 
-// The fp64 values that groups are graded by (-inf: masked or switched off).
+// The fp64 values that groups are graded by (-inf: masked or switched off), and
+// what they are to be divided by: scores are quotients, and sums of exponentials
+// alone round, and tie, differently. With a bias they are divided here.
 template <int PER, bool BIAS>
-__device__ __forceinline__ void exact_values(const SelectArgs& a, const float (&l)[PER], const float (&b)[PER], float top,
-                                             double (&v)[PER]) {
+__device__ __forceinline__ double exact_values(const SelectArgs& a, const float (&l)[PER], const float (&b)[PER], float top,
+                                               double (&v)[PER]) {
+  double total = 1.0;
 #pragma unroll
   for (int j = 0; j < PER; ++j) v[j] = (double)l[j];
   if (BIAS || (a.groups > a.limit && a.group_top == 2)) {
@@ -164,15 +172,17 @@ __device__ __forceinline__ void exact_values(const SelectArgs& a, const float (&
       v[j] = a.score == 0 ? exp(x - (double)top) : 1.0 / (1.0 + exp(-x));
       sum += v[j];
     }
+    if (a.score == 0) total = at_lane(wave_sum(sum), 0);   // (in scalar registers)
     if (BIAS) {
-      const double scale = a.score == 0 ? 1.0 / wave_sum(sum) : 1.0;
 #pragma unroll
-      for (int j = 0; j < PER; ++j) v[j] = v[j] * scale + (double)b[j];
+      for (int j = 0; j < PER; ++j) v[j] = v[j] / total + (double)b[j];
+      total = 1.0;
     }
   }
 #pragma unroll
   for (int j = 0; j < PER; ++j)
     if (l[j] == -INFINITY || (BIAS && !(b[j] > -INFINITY))) v[j] = -INFINITY;
+  return total;
 }
 
 // The ids of a token's slots, slot r on lane r (-1: none), by k rounds of the
@@ -183,7 +193,7 @@ __device__ __forceinline__ int select_by_rounds(const SelectArgs& a, const float
                                                 double* graded, int lane) {
   using Key = std::conditional_t<BIAS, unsigned long long, uint32_t>;
   double v[PER];
-  exact_values<PER, BIAS>(a, l, b, top, v);
+  const double total = exact_values<PER, BIAS>(a, l, b, top, v);
   Key key[PER];   // 0: masked, taken or not there
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
@@ -192,7 +202,7 @@ __device__ __forceinline__ int select_by_rounds(const SelectArgs& a, const float
   }
   if (a.groups > a.limit) {
     double gap;
-    keep_open(a, open_groups<PER, double>(a, v, graded, lane, gap), lane, key, (Key)0);
+    keep_open(a, open_groups<PER, double>(a, v, graded, lane, gap, total), lane, key, (Key)0);
   }
   int my_id = -1;
   for (int r = 0; r < a.top_k; ++r) {
@@ -323,9 +333,9 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
       // of the other sign is decided in fp64; a gap to a group without experts is infinite.
       if (most > -INFINITY && !(gap > 4.f * off * (1.f + most))) {
         double v[PER], exact_gap;
-        exact_values<PER, BIAS>(a, l, b, top, v);
+        const double total = exact_values<PER, BIAS>(a, l, b, top, v);
         wave_lds_order();
-        open = open_groups<PER, double>(a, v, shared[wave], lane, exact_gap);
+        open = open_groups<PER, double>(a, v, shared[wave], lane, exact_gap, total);
       }
     }
     keep_open(a, open, lane, value);
@@ -413,7 +423,7 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
           double sum = 0.0;
 #pragma unroll
           for (int j = 0; j < PER; ++j) sum += exp((double)l[j] - (double)top);
-          score = exp((double)x - (double)top) * (1.0 / wave_sum(sum));
+          score = exp((double)x - (double)top) / wave_sum(sum);
         } else {
           score = 1.0 / (1.0 + exp(-(double)x));
         }

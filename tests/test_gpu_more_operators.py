@@ -199,6 +199,30 @@ def test_select_orders_values_that_fp32_cannot(E, near, groups, score):
     check_select(up(l), 8, score, bias=bias, **groups)
 
 
+def test_select_grades_groups_by_normalised_scores():
+    """Softmax scores without a bias: sums of two that are equal before the division by the row's sum and
+    not after it, or the other way round. The best expert of every group has the row's largest logit."""
+    rng = np.random.default_rng(17)
+    differ = 0
+    for G in (3, 5, 6, 7, 12, 24, 33):
+        l = np.zeros((60, 2 * G), np.float32)
+        l[:, 1::2] = rng.choice([-38.5, -38.0, -37.25, -36.875, -36.75, -36.5, -36.0], (60, G))
+        e = np.exp(l.astype(np.float64)).reshape(60, G, 2)
+
+        def best(total):          # the two best groups, equal ones in the order of their numbers
+            return np.argsort(-(e / total).sum(2), axis=1, kind="stable")[:, :2]
+        # rows whose answer does not hang on the last bit of the row's sum, which goes with its order
+        total = e.sum((1, 2), keepdims=True)
+        sure = np.array([(best(total * (1 + d)) == best(total)).all(1) for d in (-2.0 ** -52, 2.0 ** -51)]).all(0)
+        differ += int((best(np.ones_like(total)) != best(total))[sure, 0].sum())
+        for limit in (1, 2):
+            check_select(up(l[sure]), 2, num_groups=G, group_limit=limit, group_top=2)
+    assert differ > 20
+    ids, _ = check_select(up(np.array([[0, -38.5, 0, -38.5, 0, -36.8]], np.float32)), 2, num_groups=3, group_limit=1,
+                          group_top=2)
+    assert ids.tolist() == [[4, 5]]
+
+
 def test_select_of_few_lanes_with_experts():
     """Fewer lanes than slots hold an open expert; one lane holds many."""
     l = np.full((4, 1024), -INF, np.float32)
