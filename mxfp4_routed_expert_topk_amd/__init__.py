@@ -182,6 +182,14 @@ def _too_large(**sizes):
     return MoeError(MOE_ERR_SHAPE, "sizes must be below 2^31, got " + ", ".join(f"{n}={v}" for n, v in sizes.items()))
 
 
+def _need_int32(**values):
+    """Raise MoeError(MOE_ERR_SHAPE) for a value that no int32 holds, negative
+    ones too: ctypes would pass its low 32 bits on."""
+    if any(not -1 << 31 <= v < 1 << 31 for v in values.values()):
+        raise MoeError(MOE_ERR_SHAPE, "values must be below 2^31 and at least -2^31, got "
+                       + ", ".join(f"{n}={v}" for n, v in values.items()))
+
+
 def _stream(stream=None) -> int:
     import torch
     s = torch.cuda.current_stream() if stream is None else stream
@@ -675,6 +683,11 @@ def _warn_no_graph(name: str, gradient: str, *tensors):
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 
 
+def _need_score(score):
+    if score not in (MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID):
+        raise _arg_error(f"score must be MOE_SCORE_SOFTMAX (0) or MOE_SCORE_SIGMOID (1), got {score!r}")
+
+
 def _logits(logits):
     """(rows, experts, row stride, type code) of a router's logits."""
     import torch
@@ -698,8 +711,9 @@ def router_select(logits, top_k, score=MOE_SCORE_SOFTMAX, bias=None, num_groups=
     call that autograd would have recorded warns)."""
     import torch
     rows, experts, ld, code = _logits(logits)
-    if (top_k | num_groups | group_limit | group_top) >> 31 > 0:   # (negative ones are the library's to refuse)
-        raise _too_large(top_k=top_k, num_groups=num_groups, group_limit=group_limit, group_top=group_top)
+    if (top_k | num_groups | group_limit | group_top) >> 31:   # too large, or negative, which the library refuses
+        _need_int32(top_k=top_k, num_groups=num_groups, group_limit=group_limit, group_top=group_top)
+    _need_score(score)
     if not 0 < top_k <= experts:
         raise MoeError(MOE_ERR_SHAPE, f"top_k must be in [1, {experts}], got {top_k}")
     shape = (rows, top_k)
@@ -732,6 +746,7 @@ def router_select_backward(dweights, logits, ids, score=MOE_SCORE_SOFTMAX, renor
     scale as there (moe_router_select_backward)."""
     import torch
     rows, experts, ld, code = _logits(logits)
+    _need_score(score)
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
         raise _arg_error("ids must be a 2-D torch.Tensor [T, top_k]")
     shape = (rows, ids.shape[1])

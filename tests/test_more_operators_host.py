@@ -282,6 +282,37 @@ def test_sizes_that_no_int32_holds_are_refused(lib, call, needle):
     assert ei.value.status == 2 and needle in ei.value.message, ei.value.message
 
 
+@pytest.mark.parametrize("change,status,needle", [
+    (dict(num_groups=2 - BIG), 2, f"num_groups={2 - BIG}"),
+    (dict(num_groups=4, group_limit=2 - BIG), 2, f"group_limit={2 - BIG}"),
+    (dict(group_top=1 - BIG), 2, f"group_top={1 - BIG}"),
+    (dict(top_k=2 - BIG), 2, "top_k"),
+    (dict(num_groups=-1, group_top=BIG + 1), 2, f"group_top={BIG + 1}"),   # a negative one does not hide a large one
+    (dict(num_groups=-4), 2, "num_groups must divide num_experts=8 and be in [1, 64], got -4"),
+    (dict(num_groups=-2 ** 31), 2, "num_groups must divide"),
+    (dict(group_limit=-1), 2, "group_limit must be in"),
+    (dict(group_top=-1), 2, "group_top must be 1 or 2"),
+    (dict(score=BIG), 1, f"got {BIG}"),                                   # its low 32 bits are softmax's
+    (dict(score=1 - BIG), 1, "score must be"),
+    (dict(score=2), 1, "score must be MOE_SCORE_SOFTMAX (0) or MOE_SCORE_SIGMOID (1), got 2"),
+    (dict(score="sigmoid"), 1, "score must be"),
+    (dict(score=None), 1, "score must be"),
+])
+def test_select_refuses_what_no_int32_holds(lib, monkeypatch, change, status, needle):
+    """Arguments reach the C entry as int32; what it refuses it refuses on the values given."""
+    def launch(fn, args, like, stream, tensors):
+        moe._check(fn(*args, None))
+    monkeypatch.setattr(moe, "_launch", launch)   # tensors of no rows: nothing is enqueued
+    kw = {"top_k": 2, **change}
+    with pytest.raises(moe.MoeError) as ei:
+        moe.router_select(f(0, 8), **kw)
+    assert ei.value.status == status and needle in ei.value.message, ei.value.message
+    if "score" in change:
+        with pytest.raises(moe.MoeError) as ei:
+            moe.router_select_backward(f(0, 2), f(0, 8), i(0, 2), **change)
+        assert ei.value.status == status and needle in ei.value.message, ei.value.message
+
+
 @pytest.mark.parametrize("call,name", [
     (lambda t: moe.router_select(t["logits"], 2), "logits"),
     (lambda t: moe.mxfp4_linear(t["x"], u(4, 32), u(4, 2)), "x"),
