@@ -508,6 +508,38 @@ def test_linear_takes_every_scale_byte():
                 np.testing.assert_array_equal(got[r][ok], v[ok])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("m", [3, 16, 40, 128, 200, 300, 1000, 8192])
+def test_linear_takes_every_scale_byte_beside_others(m, dtype):
+    """Every byte as the scale of each block of a row, any other bytes beside it (none of NaN or infinite
+    weights, which x's zeros would turn to NaN); x is one value in one block, so products are exact. m reaches
+    the streaming kernel's shapes and both tile shapes."""
+    blocks = 7                                     # a dword of scales and three bytes of the next
+    rng = np.random.default_rng(31)
+    n, k = 256 * blocks, 32 * blocks
+    scales = rng.choice([0, 1, 2, 3, 63, 64, 126, 127, 128, 129, 191, 250, 251, 252], (n, blocks)).astype(np.uint8)
+    at = np.arange(n) // 256                       # the block that a row's byte is tried in
+    scales[np.arange(n), at] = np.arange(n) % 256
+    codes = rng.integers(0, 256, (n, k // 2), dtype=np.uint8)
+    row = np.arange(m)
+    col = 32 * (row % blocks) + (row // blocks * 5) % 32
+    value = np.where(row % 3 == 2, 2.0 ** 100, 1.0) * np.where(row % 2, -1.0, 1.0)
+    x = np.zeros((m, k), np.float32)
+    x[row, col] = value
+    got = moe.mxfp4_linear(up(x).to(BF), up(codes), up(scales), dtype=dtype)
+    with np.errstate(over="ignore"):
+        w = oracle.mxfp4_values(codes, scales)
+    w = np.where(np.abs(w) >= 2.0 ** 128, np.copysign(np.inf, w), w)
+    w = up(w)
+    want = w[:, up(col)].t() * up(value).unsqueeze(1)
+    want = torch.where(want.abs() >= 2.0 ** 128, torch.copysign(torch.full_like(want, INF), want), want)
+    # an infinite weight times another zero of x is NaN
+    nan, inf = torch.isnan(w).any(1), torch.isinf(w)
+    bad = nan | (inf.sum(1).unsqueeze(0) - inf[:, up(col)].t().int() > 0)
+    assert torch.equal(torch.isnan(got), bad) and 0 < int(bad.sum()) < bad.numel() // 50
+    assert torch.equal(got.double()[~bad], want[~bad])
+
+
 @pytest.mark.parametrize("m", [1, 20, 200, 2000])
 def test_linear_rows_of_a_wider_matrix(m):
     rng = np.random.default_rng(m)
