@@ -683,9 +683,8 @@ def _warn_no_graph(name: str, gradient: str, *tensors):
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 
 
-def _need_score(score):
-    if score not in (MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID):
-        raise _arg_error(f"score must be MOE_SCORE_SOFTMAX (0) or MOE_SCORE_SIGMOID (1), got {score!r}")
+def _bad_score(score):
+    return _arg_error(f"score must be MOE_SCORE_SOFTMAX (0) or MOE_SCORE_SIGMOID (1), got {score!r}")
 
 
 def _logits(logits):
@@ -713,7 +712,8 @@ def router_select(logits, top_k, score=MOE_SCORE_SOFTMAX, bias=None, num_groups=
     rows, experts, ld, code = _logits(logits)
     if (top_k | num_groups | group_limit | group_top) >> 31:   # too large, or negative, which the library refuses
         _need_int32(top_k=top_k, num_groups=num_groups, group_limit=group_limit, group_top=group_top)
-    _need_score(score)
+    if score != MOE_SCORE_SOFTMAX and score != MOE_SCORE_SIGMOID:
+        raise _bad_score(score)
     if not 0 < top_k <= experts:
         raise MoeError(MOE_ERR_SHAPE, f"top_k must be in [1, {experts}], got {top_k}")
     shape = (rows, top_k)
@@ -746,7 +746,8 @@ def router_select_backward(dweights, logits, ids, score=MOE_SCORE_SOFTMAX, renor
     scale as there (moe_router_select_backward)."""
     import torch
     rows, experts, ld, code = _logits(logits)
-    _need_score(score)
+    if score != MOE_SCORE_SOFTMAX and score != MOE_SCORE_SIGMOID:
+        raise _bad_score(score)
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
         raise _arg_error("ids must be a 2-D torch.Tensor [T, top_k]")
     shape = (rows, ids.shape[1])
