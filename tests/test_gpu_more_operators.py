@@ -826,6 +826,68 @@ def test_combine_beyond_32_bit_offsets():
     assert dw.tolist() == [[float(H), 2.0 * H], [0.0, 0.0]]
 
 
+# ------------------------------------------------------------------ the largest sizes
+def test_select_of_the_most_tokens():
+    """2^24 rows of 8 experts: every row is one of 64, so all results are its own row's."""
+    T, k = 1 << 24, 2
+    rng = np.random.default_rng(41)
+    few = logits_of(rng, 64, 8, F32)
+    few[3] = -INF
+    l = few.repeat(T // 64, 1)
+    ids, w = moe.router_select(l, k, score=moe.MOE_SCORE_SIGMOID)
+    want = moe.router_select(few, k, score=moe.MOE_SCORE_SIGMOID)
+    check_select(few, k, "sigmoid")
+    assert (ids.view(-1, 64, k) == want[0]).all() and (w.view(-1, 64, k) == want[1]).all()
+    dw = up(rng.standard_normal((64, k)).astype(np.float32))
+    got = moe.router_select_backward(dw.repeat(T // 64, 1), l, ids, score=moe.MOE_SCORE_SIGMOID)
+    want = moe.router_select_backward(dw, few, want[0], score=moe.MOE_SCORE_SIGMOID)
+    assert (got.view(-1, 64, 8) == want).all()
+
+
+@pytest.mark.parametrize("m,n,k,gate", [(1 << 19, 18, 64, True), (5, 1 << 19, 96, False), (40, 1 << 19, 32, True),
+                                        (1 << 19, 1, 32, False), (300, 514, 65536, True), (16, 48, 65536, False),
+                                        (17, 4100, 65536, False)])
+def test_linear_at_its_limits(m, n, k, gate):
+    """Integer x and scales as in the exact test; sums below 2^24 quarters."""
+    rng = np.random.default_rng(43)
+    g = torch.Generator(device=dev()).manual_seed(43)
+    x = torch.randint(-1, 2, (m, k), device=dev(), generator=g).to(BF)
+    codes, scales = mx(rng, n, k, 126, 128)
+    got = moe.mxfp4_linear(x, up(codes), up(scales), gate=gate, dtype=F32)
+    w = up(oracle.mxfp4_values(codes, scales)).float()
+    y = torch.mm(x.float(), w.t().contiguous())     # exact: multiples of 1/4 below 2^20
+    if not gate:
+        assert torch.equal(got, y)
+        return
+    y = y.double()
+    a, u = y.chunk(2, dim=1)
+    want = a * torch.special.expit(a) * u
+    # two exponentials' arguments and three operations, as counted for gates far below zero
+    assert ((got.double() - want).abs() <= (a.abs() + 7) * U * want.abs() + 2.0 ** -139).all()
+
+
+def test_combine_of_the_most_tokens_and_slots():
+    """2^21 tokens of 32 slots; hidden 8. Slot s of token t is row 32 t + s, or none where t + s is a multiple of 5."""
+    T, k, H = 1 << 21, 32, 8
+    rows = T * k
+    at = torch.arange(rows, dtype=I32, device=dev())
+    none = (at // k + at % k) % 5 == 0
+    rowpos = at.masked_fill(none, -1).view(T, k)
+    perm = at.masked_fill(none, -7)
+    y = (at % 7 - 3).to(BF).unsqueeze(1).repeat(1, H)
+    y[:, 1:] = y[:, 1:] * torch.arange(1, H, device=dev(), dtype=torch.float32).to(BF)
+    out = moe.expert_combine(y, rowpos, dtype=F32)
+    want = y.masked_fill(none.unsqueeze(1), 0).view(T, k, H).float().sum(1)
+    assert torch.equal(out, want)
+    w = (at % 3 + 1).float().view(T, k)
+    dout = (torch.arange(T, device=dev()) % 11 - 5).to(BF).unsqueeze(1).repeat(1, H)
+    dy, dw = moe.expert_combine_backward(dout, y, rowpos, perm, w, dy=torch.full_like(y, 7.0))
+    want = (w.unsqueeze(2) * dout.float().unsqueeze(1)).to(BF).view(rows, H)
+    assert torch.equal(dy, want.masked_fill(none.unsqueeze(1), 7.0))
+    want = (y.view(T, k, H).float() * dout.float().unsqueeze(1)).sum(2).masked_fill(none.view(T, k), 0)
+    assert torch.equal(dw, want)
+
+
 # ------------------------------------------------------------------ streams, graphs, and all of them together
 def some_calls():
     """(callables, each a pass through one entry on inputs of its own, and the inputs to change)."""
