@@ -2,8 +2,8 @@
 //   y [M, N] = x [M, K] W [N, K]^T,   W = code 2^(byte - 127)
 // and, gated, silu(y[:, c]) y[:, c + N/2] for the fused w1||w3 of a shared
 // expert.  A weight has at most two significant bits, so W is exact in bf16
-// for every scale byte (0 is 2^-127, 255 NaN; 4 and 6 times 2^127 are infinite
-// there as in fp32); products are summed in fp32 on v_mfma_f32_16x16x32_bf16,
+// for every scale byte (0 is 2^-127, 255 NaN; 2^128 and above, of bytes 253 and 254,
+// is infinite there as in fp32); products are summed in fp32 on v_mfma_f32_16x16x32_bf16,
 // which keeps subnormal operands, and the sum is rounded once.
 #include <type_traits>
 

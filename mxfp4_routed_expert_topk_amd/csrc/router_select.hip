@@ -80,7 +80,10 @@ __device__ __forceinline__ float wave_max(float v) {   // of no NaN
 }
 __device__ __forceinline__ double wave_sum(double v) { return wave_reduce(v, [](double a, double b) { return a + b; }); }
 
-// 2^(x log2 e) on the hardware's exponential: off by (|x| + 2) u of the value
+// 2^(x log2 e) on the hardware's exponential: off by (1.25 |x| + 2) u of the value (the
+// product's rounding |x| u, the constant's, the instruction's 2 u; 0.95 of that is the
+// most found over [-87, 0]) and 0 below 2^-126.  Sums over all experts take it (16383 x
+// 896 scores: the gradient 30 us with expf, 25 with it), selected weights expf.
 __device__ __forceinline__ float quick_exp(float x) { return __expf(x); }
 
 __device__ __forceinline__ void wave_lds_order() {
@@ -290,10 +293,13 @@ __global__ __launch_bounds__(kTokensPerBlock* kWave) void router_select(SelectAr
   }
 
   // What experts are compared by: the logit, or an approximate score plus the bias, in fp32.
-  // An approximate value v is off by less than off (1 + |v|). The exponential: (2.5 |x| + 2) u of itself. A sigmoid
-  // passes that on as 0.7 u at most; its reciprocal 2 u, two roundings and the sum's: 4.7 u + u |v|; 8 u taken. A
-  // softmax score, at most 1: its own and its sum's exponentials (the sum's average |x| is at most ln 1024), the
-  // sum's 22 additions in a row, a quotient: 64 u taken.
+  // An approximate value v is off by less than off (1 + |v|): by u |v| of the bias's addition, and by what its score
+  // is off, for which 8 u and 64 u are taken:
+  //   sigmoid  (1.25 |x| + 2) u of the exponential reach the score times s (1 - s), 0.7 u at most; the rounding of
+  //            1 + exp u, the reciprocal 2 u: 3.7 u
+  //   softmax  x = l - top is rounded too, so (2.25 |x| + 2) u of an exponential: of the score's own, times s <=
+  //            exp(-|x|), 2.1 u; of the sum's, whose average |x| is at most ln 1024, 17.6 u; the sum's 22 additions in
+  //            a row 22 u; the reciprocal and the product 2 u: 44 u
   const float off = BIAS && softmax ? 0x1p-18f : 0x1p-21f;
   float value[PER];
   auto put_scores = [&](float (&to)[PER], float share) {   // -inf for masked experts
